@@ -227,6 +227,125 @@ enum siluquant_gemm_out { SILUQUANT_GEMM_OUT_F32 = 0, SILUQUANT_GEMM_OUT_BF16 = 
 int i8_gemm_group_scaled(const int8_t* A, const float* sA, const int8_t* B, const float* sB, void* C, int64_t M,
                          int64_t N, int64_t K, int64_t group, int64_t b_rows_per_scale, int c_dtype, hipStream_t stream);
 
+/* ---- the norm before the products, and the microscaled 4-bit format ----
+ *
+ * The operators below follow the conventions above: row-major contiguous
+ * tensors, buffers owned by the caller, nothing allocated, no state, every
+ * check on the host before any launch, work enqueued on `stream`. */
+
+/* Element types and code formats. */
+enum siluquant_dtype { SILUQUANT_F32 = 0, SILUQUANT_BF16 = 1 };
+enum siluquant_code_format { SILUQUANT_CODE_INT8 = 0, SILUQUANT_CODE_E4M3 = 1 };
+
+/*
+ * rms_norm_quant -- root-mean-square norm with the residual's addition, its
+ * output quantised by row groups: the operand of i8_gemm_group_scaled (int8)
+ * or of an E4M3 product.
+ *
+ *   h[t, d]  = bf16(x[t, d] + residual[t, d])        (one fp32 addition)
+ *   rstd[t]  = 1 / sqrt(sum_d h[t, d]^2 / D + eps)   (fp32)
+ *   y[t, d]  = bf16((h[t, d] * rstd[t]) * weight[d])
+ *   codes and scales of y by groups of `group` channels of a row, as
+ *   silu_fwd_quant (int8) or silu_dot_fwd_bwd_quant_fuse_fp8 (E4M3) quantises.
+ *
+ *   x         bf16 or fp32 [T, D] by x_dtype (SILUQUANT_BF16 / _F32: both
+ *             output types of the products)
+ *   residual  bf16 [T, D], or NULL for none
+ *   weight    bf16 [D]
+ *   y_q       int8 or E4M3 codes [T, D] by code_format, or NULL for none
+ *   y_s       fp32 [T, ceil(D/group)], NULL together with y_q
+ *   y_bf16    bf16 [T, D] the y that is quantised, or NULL (y_q and y_bf16 may
+ *             not both be NULL)
+ *   h         bf16 [T, D] the new residual stream, or NULL; may be `residual`
+ *             itself (updated in place), no other overlap is taken
+ *   rstd      fp32 [T], or NULL: what rms_norm_bwd needs
+ *   All but y_s and rstd (4 bytes) are 16-byte aligned.
+ * Sizes: T <= 2^31, D <= 2^22, any D (the last group of a row may be short);
+ *   T == 0 or D == 0 is a no-op.  group: 128, 64 or 32.  eps: finite, >= 0 (a
+ *   row of zeros with eps == 0 gives NaN).
+ * A row that holds an infinity or a NaN gives NaN scales (or NaN codes) in the
+ * groups whose y is not finite; other rows are not affected.
+ */
+int rms_norm_quant(const void* x, int x_dtype, const void* residual, const void* weight, void* y_q, float* y_s,
+                   void* y_bf16, void* h, float* rstd, int64_t T, int64_t D, int64_t group, int code_format, float eps,
+                   hipStream_t stream);
+
+/*
+ * rms_norm_bwd -- the gradients of that norm (quantising passes the gradient
+ * through unchanged).  With n = h * rstd and g = dy * weight:
+ *
+ *   dx[t, d] = bf16(rstd[t] * (g[t, d] - n[t, d] * sum_d(g * n) / D) + d_h[t, d])
+ *   dw[d]    = sum_t dy[t, d] * n[t, d]
+ *
+ * dx is the gradient for x and for residual alike.
+ *   dy      bf16 or fp32 [T, D] by dy_dtype (the dgrad product's two outputs)
+ *   h, rstd, weight   as rms_norm_quant wrote and read them
+ *   d_h     bf16 [T, D] the gradient that reaches h by other ways (the residual
+ *           stream), or NULL; dx may be d_h itself
+ *   dx      bf16 [T, D];  dw  fp32 [D], or NULL where the weight is not trained
+ *   workspace  rms_norm_bwd_workspace_bytes(T, D) bytes, 16-byte aligned; only
+ *           looked at when dw is wanted or D > 16384.  Its contents before and
+ *           after a call mean nothing.  The sums do not depend on timing.
+ * Sizes as above; T == 0 writes zeros to dw.  A workspace that is too small
+ * returns SILUQUANT_ERR_BAD_SHAPE.
+ */
+int64_t rms_norm_bwd_workspace_bytes(int64_t T, int64_t D);
+int rms_norm_bwd(const void* dy, int dy_dtype, const void* h, const void* weight, const float* rstd, const void* d_h,
+                 void* dx, float* dw, void* workspace, int64_t workspace_bytes, int64_t T, int64_t D,
+                 hipStream_t stream);
+
+/*
+ * mxfp4_quant -- bf16 rows as microscaled 4-bit codes (OCP MX, MXFP4).
+ *
+ * A block is 32 consecutive values of a row: E2M1 codes (magnitudes 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6; bit 3 the sign) and one E8M0 byte b, their common factor
+ * 2^(b - 127):
+ *   b    = max(floor(log2(amax)) - 2, -127) + 127; 127 for a block of zeros;
+ *          255 (NaN) for a block that holds an infinity or a NaN, whose codes
+ *          then mean nothing
+ *   code = E2M1(v * 2^(127 - b)), nearest, ties to the even code, at most 6 in
+ *          magnitude; a zero keeps its sign
+ * The last block of a row is filled up with zero codes, so any K will do.
+ *   x    bf16 [R, K]
+ *   q    uint8 [R, 16 * ceil(K/32)], two codes to a byte, the even column in
+ *        the low half;  s  uint8 [R, ceil(K/32)]
+ *   q_t  uint8 [K, 16 * ceil(R/32)], s_t  uint8 [K, ceil(R/32)]: the same of
+ *        x's transpose, for the products that contract over rows
+ * Either pair may be NULL; x is read once for both.  x, q, q_t 16-byte
+ * aligned.  R <= 2^31, K <= 2^22; R == 0 or K == 0 is a no-op.
+ */
+int mxfp4_quant(const void* x, void* q, void* s, void* q_t, void* s_t, int64_t R, int64_t K, hipStream_t stream);
+
+/*
+ * mxfp4_gemm -- the product of two such operands on the matrix cores:
+ *   C[m, n] = sum over blocks k of 2^(sA[m, k] - 127) * 2^(sB[n, k] - 127) *
+ *             (A[m, block k] . B[n, block k])
+ *   A uint8 [M, K/2], sA uint8 [M, K/32]; B uint8 [N, K/2], sB uint8 [N, K/32]
+ *   (16-byte aligned codes); C fp32 (4-byte aligned) or bf16 (2-byte aligned)
+ *   [M, N] by c_dtype, fully overwritten.
+ * K counts whole blocks: a multiple of 32 (mxfp4_quant's rows are filled up).
+ * Sums are fp32; bf16 output rounds them once (nearest, ties to even).  An
+ * exponent byte of 255 makes the row or column of C it belongs to NaN.
+ * Sizes: any M, N >= 0 (M == 0 or N == 0 is a no-op), K <= 2^22 (K == 0 writes
+ * zeros).  From single rows (the weight streams through once) to large tiles.
+ */
+int mxfp4_gemm(const void* A, const void* sA, const void* B, const void* sB, void* C, int64_t M, int64_t N, int64_t K,
+               int c_dtype, hipStream_t stream);
+
+/*
+ * The values that codes stand for, in bf16 (nearest, ties to even):
+ *   mxfp4_dequant  out[r, k] = code * 2^(s - 127); NaN for an exponent byte of
+ *                  255.  q, s as mxfp4_quant writes them, out bf16 [R, K].
+ *   group_dequant  out[r, k] = bf16(fl32(code * s[r, k / group])), q int8 or
+ *                  E4M3 [R, K] by code_format, s fp32 [R, ceil(K/group)]: the
+ *                  row layouts of the quantisers above (y_q_t of the backward
+ *                  pass included, with R = H, K = T).
+ * q and out 16-byte aligned; R <= 2^31, K <= 2^22 (group_dequant: 2^23).
+ */
+int mxfp4_dequant(const void* q, const void* s, void* out, int64_t R, int64_t K, hipStream_t stream);
+int group_dequant(const void* q, const float* s, void* out, int64_t R, int64_t K, int64_t group, int code_format,
+                  hipStream_t stream);
+
 /* Optional: makes the HIP runtime load the library's kernels on the current
  * device now, which it otherwise does at the first launch.  No entry point
  * needs it first.  Enqueues nothing, allocates nothing itself; safe to call

@@ -30,7 +30,8 @@ _ERRORS = {
 
 EXPORTED = ("silu_dot_fwd_bwd_quant_fuse", "silu_dot_fwd_bwd_quant_fuse_fp8", "silu_fwd_quant", "silu_fwd_quant_q8_1",
             "kquant_swiglu_q8_1_rows", "i8_gemm_group_scaled", "siluquant_prepare", "siluquant_strerror", "siluquant_algorithmic_bytes",
-            "siluquant_eval_sigmoid", "siluquant_eval_intermediates")
+            "siluquant_eval_sigmoid", "siluquant_eval_intermediates", "rms_norm_quant", "rms_norm_bwd",
+            "rms_norm_bwd_workspace_bytes", "mxfp4_quant", "mxfp4_gemm", "mxfp4_dequant", "group_dequant")
 
 _lib = None
 
@@ -62,6 +63,16 @@ def lib() -> ctypes.CDLL:
         L.kquant_swiglu_q8_1_rows.restype = ctypes.c_int
         L.i8_gemm_group_scaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_int, vp]
         L.i8_gemm_group_scaled.restype = ctypes.c_int
+        ci, cf = ctypes.c_int, ctypes.c_float
+        for fn, args in ((L.rms_norm_quant, [vp, ci, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, cf, vp]),
+                         (L.rms_norm_bwd, [vp, ci, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp]),
+                         (L.mxfp4_quant, [vp, vp, vp, vp, vp, i64, i64, vp]),
+                         (L.mxfp4_gemm, [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]),
+                         (L.mxfp4_dequant, [vp, vp, vp, i64, i64, vp]),
+                         (L.group_dequant, [vp, vp, vp, i64, i64, i64, ci, vp])):
+            fn.argtypes, fn.restype = args, ci
+        L.rms_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.rms_norm_bwd_workspace_bytes.restype = i64
         L.siluquant_eval_sigmoid.argtypes = [vp, vp, i64, vp]
         L.siluquant_eval_sigmoid.restype = ctypes.c_int
         L.siluquant_eval_intermediates.argtypes = [vp, vp, vp, vp, i64, i64, vp]
@@ -338,6 +349,213 @@ def forward_bytes(T: int, H: int, with_bf16: bool = False, with_weight: bool = F
     """Bytes the forward quantiser must move: x (4 per pair) in, codes (1) and
     one fp32 scale per `group` codes out, plus bf16 y (2) and the row weights."""
     return 5 * T * H + 4 * T * (-(-H // group)) + (2 * T * H if with_bf16 else 0) + (4 * T if with_weight else 0)
+
+
+# ---- the norm before the products, and the microscaled 4-bit format ----
+#
+# These checks are written for single-token calls, where host time is most of a
+# call: one comparison per property, no containers built unless one fails.
+
+F32, BF16 = 0, 1
+CODE_INT8, CODE_E4M3 = 0, 1
+MX_BLOCK = 32  # values per E8M0 exponent
+
+
+def _want(name, t, dtypes, shape, dev):
+    if t.dtype not in dtypes or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of %s, shape %s, on %s; got %s %s on %s"
+                         % (name, " or ".join(str(d) for d in dtypes), tuple(shape), dev, t.dtype, tuple(t.shape),
+                            t.device))
+
+
+def _rank2(name, t):
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions, got shape %s" % (name, tuple(t.shape)))
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU; %s is on %s" % (name, t.device))
+    return t.shape[0], t.shape[1], t.device
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _enqueue(fn, what, dev, *args):
+    """fn(*args, stream) on the current stream of dev, with dev current."""
+    import torch
+
+    if dev.index == torch.cuda.current_device():
+        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(code, what)
+
+
+def _code_format(name, t):
+    import torch
+
+    if t.dtype == torch.int8:
+        return CODE_INT8
+    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
+        return CODE_E4M3
+    raise ValueError("%s must be int8, or uint8 or float8_e4m3fn (E4M3); got %s" % (name, t.dtype))
+
+
+def rms_norm_quant(x, weight, y_q=None, y_s=None, residual=None, h=None, rstd=None, y_bf16=None, eps: float = 1e-6,
+                   group_size: int = GROUP):
+    """h = bf16(x + residual), y = bf16(h / rms(h) * weight), and the codes and
+    scales of y by groups of group_size channels.
+
+    x bf16 or fp32 [T, D]; weight bf16 [D]; residual bf16 [T, D].  Written where
+    given: y_q [T, D] (int8; or E4M3 as uint8 or float8_e4m3fn) together with
+    y_s fp32 [T, ceil(D/group_size)], y_bf16 [T, D], h bf16 [T, D] (may be
+    residual itself) and rstd fp32 [T].  At least one of y_q and y_bf16 is
+    needed.  Enqueued on the current stream of x's device; returns None."""
+    import torch
+
+    T, D, dev = _rank2("x", x)
+    f32, bf16 = (torch.float32,), (torch.bfloat16,)
+    if group_size not in GROUPS:
+        raise ValueError("group_size must be one of %s" % (GROUPS,))
+    _want("x", x, f32 + bf16, (T, D), dev)
+    _want("weight", weight, bf16, (D,), dev)
+    if (y_q is None) != (y_s is None) or (y_q is None and y_bf16 is None):
+        raise ValueError("y_q and y_s go together, and one of y_q and y_bf16 is needed")
+    fmt = CODE_INT8
+    if y_q is not None:
+        fmt = _code_format("y_q", y_q)
+        _want("y_q", y_q, (y_q.dtype,), (T, D), dev)
+        _want("y_s", y_s, f32, (T, -(-D // group_size)), dev)
+    if residual is not None:
+        _want("residual", residual, bf16, (T, D), dev)
+    if h is not None:
+        _want("h", h, bf16, (T, D), dev)
+    if rstd is not None:
+        _want("rstd", rstd, f32, (T,), dev)
+    if y_bf16 is not None:
+        _want("y_bf16", y_bf16, bf16, (T, D), dev)
+    _enqueue(lib().rms_norm_quant, "rms_norm_quant", dev, x.data_ptr(), F32 if x.dtype == torch.float32 else BF16,
+             _ptr(residual), weight.data_ptr(), _ptr(y_q), _ptr(y_s), _ptr(y_bf16), _ptr(h), _ptr(rstd), T, D,
+             group_size, fmt, eps)
+
+
+def rms_norm_bwd_workspace(T: int, D: int, device):
+    """A workspace tensor for rms_norm_bwd at this size (any larger one will do)."""
+    import torch
+
+    n = int(lib().rms_norm_bwd_workspace_bytes(int(T), int(D)))
+    if n < 0:
+        raise ValueError("no such size: T=%d D=%d" % (T, D))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rms_norm_bwd(dy, h, weight, rstd, dx, dw=None, d_h=None, workspace=None):
+    """Gradients of rms_norm_quant: dx bf16 [T, D] (for x and residual alike;
+    d_h bf16 [T, D], the gradient that reaches h otherwise, is added, and dx may
+    be d_h itself) and, where given, dw fp32 [D].  dy bf16 or fp32 [T, D]; h,
+    weight, rstd as in the forward call.  workspace: from
+    rms_norm_bwd_workspace, needed for dw and for D > 16384.  Enqueued on the
+    current stream of dy's device; returns None."""
+    import torch
+
+    T, D, dev = _rank2("dy", dy)
+    f32, bf16 = (torch.float32,), (torch.bfloat16,)
+    _want("dy", dy, f32 + bf16, (T, D), dev)
+    _want("h", h, bf16, (T, D), dev)
+    _want("weight", weight, bf16, (D,), dev)
+    _want("rstd", rstd, f32, (T,), dev)
+    _want("dx", dx, bf16, (T, D), dev)
+    if dw is not None:
+        _want("dw", dw, f32, (D,), dev)
+    if d_h is not None:
+        _want("d_h", d_h, bf16, (T, D), dev)
+    nbytes = 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+        nbytes = workspace.numel() * workspace.element_size()
+    _enqueue(lib().rms_norm_bwd, "rms_norm_bwd", dev, dy.data_ptr(), F32 if dy.dtype == torch.float32 else BF16,
+             h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _ptr(d_h), dx.data_ptr(), _ptr(dw), _ptr(workspace),
+             nbytes, T, D)
+
+
+def mxfp4_shapes(R: int, K: int):
+    """Shapes of (codes, exponents) of a bf16 [R, K] tensor's rows, both uint8."""
+    blocks = -(-K // MX_BLOCK)
+    return (R, 16 * blocks), (R, blocks)
+
+
+def mxfp4_quant(x, q=None, s=None, q_t=None, s_t=None):
+    """Microscaled 4-bit codes of x bf16 [R, K]: q and s by rows (mxfp4_shapes(R,
+    K)), q_t and s_t of the transpose (mxfp4_shapes(K, R)), all uint8; either
+    pair or both, from one read of x.  Enqueued on the current stream of x's
+    device; returns None."""
+    import torch
+
+    R, K, dev = _rank2("x", x)
+    u8 = (torch.uint8,)
+    _want("x", x, (torch.bfloat16,), (R, K), dev)
+    if (q is None) != (s is None) or (q_t is None) != (s_t is None) or (q is None and q_t is None):
+        raise ValueError("q and s go together, q_t and s_t too, and one of the pairs is needed")
+    if q is not None:
+        b = -(-K // MX_BLOCK)
+        _want("q", q, u8, (R, 16 * b), dev)
+        _want("s", s, u8, (R, b), dev)
+    if q_t is not None:
+        b = -(-R // MX_BLOCK)
+        _want("q_t", q_t, u8, (K, 16 * b), dev)
+        _want("s_t", s_t, u8, (K, b), dev)
+    _enqueue(lib().mxfp4_quant, "mxfp4_quant", dev, x.data_ptr(), _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t), R, K)
+
+
+def mxfp4_gemm(A, sA, B, sB, C):
+    """C = A . B^T of microscaled 4-bit operands: A uint8 [M, K/2] with exponents
+    sA uint8 [M, K/32], B uint8 [N, K/2] with sB uint8 [N, K/32] (as mxfp4_quant
+    writes them), C fp32 or bf16 [M, N], overwritten.  Enqueued on the current
+    stream of A's device; returns None."""
+    import torch
+
+    M, half, dev = _rank2("A", A)
+    N = _rank2("B", B)[0]
+    u8, blocks = (torch.uint8,), half // 16
+    _want("A", A, u8, (M, 16 * blocks), dev)
+    _want("sA", sA, u8, (M, blocks), dev)
+    _want("B", B, u8, (N, 16 * blocks), dev)
+    _want("sB", sB, u8, (N, blocks), dev)
+    _want("C", C, (torch.float32, torch.bfloat16), (M, N), dev)
+    _enqueue(lib().mxfp4_gemm, "mxfp4_gemm", dev, A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
+             C.data_ptr(), M, N, 32 * blocks, F32 if C.dtype == torch.float32 else BF16)
+
+
+def mxfp4_dequant(q, s, out):
+    """out bf16 [R, K] = the values of microscaled 4-bit codes q, s
+    (mxfp4_shapes(R, K)).  Enqueued on the current stream of q's device."""
+    import torch
+
+    R, K, dev = _rank2("out", out)
+    blocks = -(-K // MX_BLOCK)
+    _want("out", out, (torch.bfloat16,), (R, K), dev)
+    _want("q", q, (torch.uint8,), (R, 16 * blocks), dev)
+    _want("s", s, (torch.uint8,), (R, blocks), dev)
+    _enqueue(lib().mxfp4_dequant, "mxfp4_dequant", dev, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K)
+
+
+def group_dequant(q, s, out, group_size: int = GROUP):
+    """out bf16 [R, K] = code * scale of the group-quantised rows q (int8, or
+    E4M3 as uint8 or float8_e4m3fn) [R, K] and s fp32 [R, ceil(K/group_size)].
+    Enqueued on the current stream of q's device."""
+    import torch
+
+    R, K, dev = _rank2("out", out)
+    if group_size not in GROUPS:
+        raise ValueError("group_size must be one of %s" % (GROUPS,))
+    fmt = _code_format("q", q)
+    _want("out", out, (torch.bfloat16,), (R, K), dev)
+    _want("q", q, (q.dtype,), (R, K), dev)
+    _want("s", s, (torch.float32,), (R, -(-K // group_size)), dev)
+    _enqueue(lib().group_dequant, "group_dequant", dev, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K, group_size,
+             fmt)
 
 
 def empty_outputs(T: int, H: int, device, group: int = GROUP, fp8: bool = False):

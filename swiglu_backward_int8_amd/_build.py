@@ -1,8 +1,9 @@
 """Build step for libsiluquant.so (in-tree, for gfx950).
 
 sigmoid_table.py writes the kernels' sigmoid table into _build/, then hipcc
-compiles the HIP sources (the fused SwiGLU passes and the group-scaled int8
-GEMM) into one shared library next to this file.
+compiles the HIP sources (the fused SwiGLU passes, the group-scaled int8 GEMM,
+the RMS norm and the microscaled 4-bit operators) into one shared library next
+to this file.
 Flags that matter for the numbers the library produces:
   -ffp-contract=off                  no fused multiply-add: the arithmetic order
                                      is the one written in the source;
@@ -19,7 +20,7 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 GEN = os.path.join(PKG, "_build")  # generated sources (not tracked)
-SRCS = [os.path.join(PKG, "csrc", "siluquant.hip"), os.path.join(PKG, "csrc", "i8gemm.hip")]
+SRCS = [os.path.join(PKG, "csrc", n + ".hip") for n in ("siluquant", "i8gemm", "rmsnorm", "mxfp4", "mxfp4gemm")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsiluquant.so")
 ARCH = "gfx950"

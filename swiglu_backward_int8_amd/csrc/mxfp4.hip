@@ -1,0 +1,365 @@
+// Microscaled 4-bit codes (OCP MX, MXFP4) of bf16 rows, and the dequantisers
+// of every code format of the library, for gfx950.
+//
+// A block is 32 consecutive values: codes E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+// their negatives; two to a byte, the first in the low half) and one E8M0
+// exponent byte b, the values' common factor 2^(b - 127):
+//   b = max(floor(log2(amax)) - 2, -127) + 127   (127 for a block of zeros,
+//       255, NaN, for a block that holds an infinity or a NaN)
+//   code = E2M1(v * 2^(127 - b)), nearest, ties to the even code, at most 6
+// amax is a bf16 number, so floor(log2(amax)) is its exponent field, and the
+// hardware's scaled conversions do the rest exactly.
+//
+// All of it is bound by memory: every element is read once and written once.
+// Rows-only quantising and dequantising walk the tensor in pieces of eight
+// values per lane (16 bytes of bf16), four independent pieces in flight per
+// lane.  Quantising both axes reads x once: a lane holds 32 rows of eight
+// columns in registers, so that a column's block lies inside the lane (no
+// transpose through LDS) and a row's block inside four neighbouring lanes.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "rows.h"
+#include "siluquant.h"
+
+namespace {
+
+using namespace rows;
+
+constexpr int kThreads = 256;
+
+// E8M0 byte of a block from its largest magnitude (bf16 bits).
+__device__ __forceinline__ uint32_t block_exponent(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 7;
+  return e == 255u ? 255u : amax_bits == 0u ? 127u : e > 2u ? e - 2u : 0u;
+}
+// 2^(b - 127) as fp32 (2^-127 is a subnormal number).
+__device__ __forceinline__ float exponent_value(uint32_t b) {
+  return __uint_as_float(b == 0u ? 0x00400000u : b << 23);
+}
+
+// Eight bf16 values -> eight codes, the first in the low half of the low byte.
+__device__ __forceinline__ uint32_t mx_codes8(const Piece& p, float scale) {
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, p.w[0]), scale, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, p.w[1]), scale, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, p.w[2]), scale, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, p.w[3]), scale, 3);
+  return q;
+}
+__device__ __forceinline__ Piece mx_values8(uint32_t q, uint32_t b) {
+  const float scale = exponent_value(b);
+  Piece p;
+  p.w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0));
+  p.w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1));
+  p.w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2));
+  p.w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3));
+  if (b == 255u) p = {{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u}};
+  return p;
+}
+
+// ---- walking rows in pieces of eight columns ----
+//
+// A flat walk takes the tensor as one run of pieces (rows that are whole
+// groups); otherwise 2^lg lanes share a row (as many as it has pieces, 256 at
+// most) and a workgroup takes 256 >> lg rows at a time.
+struct Where {
+  int64_t row, col;
+  int n;  // columns of the piece that the row has; 0 and below: a piece of padding
+  bool live;
+};
+struct Walk {
+  int64_t rows, pieces;  // per row, padding of the last group included
+  int cols, lg;
+  int64_t units, col_units;
+};
+
+template <class Op, bool kFlat, int kUnroll>
+__global__ __launch_bounds__(kThreads) void piece_kernel(const Op op, const Walk k) {
+  for (int64_t t = blockIdx.x; t * kUnroll < k.units; t += gridDim.x) {
+    Where at[kUnroll];
+    typename Op::In in[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t unit = t * kUnroll + u;
+      if (kFlat) {
+        const int64_t p = unit * kThreads + threadIdx.x;
+        at[u] = {0, 8 * p, 8, p < k.pieces};
+      } else {
+        const int64_t rg = unit / k.col_units;
+        const int64_t p = ((unit - rg * k.col_units) << k.lg) + (threadIdx.x & ((1 << k.lg) - 1));
+        const int64_t row = rg * (kThreads >> k.lg) + (threadIdx.x >> k.lg);
+        at[u] = {row, 8 * p, (int)(k.cols - 8 * p), unit < k.units && row < k.rows && p < k.pieces};
+      }
+      in[u] = op.template load<!kFlat>(at[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) op.template finish<!kFlat>(at[u], in[u]);
+  }
+}
+
+template <class Op>
+void launch_walk(const Op& op, int64_t R, int64_t C, int64_t group, hipStream_t stream) {
+  Walk k = {};
+  const bool flat = C % group == 0;
+  if (flat) {
+    k.rows = 1;
+    k.pieces = R * C / 8;
+    k.units = (k.pieces + kThreads - 1) / kThreads;
+  } else {
+    k.rows = R;
+    k.cols = (int)C;
+    k.pieces = (C + group - 1) / group * (group / 8);
+    while (k.lg < 8 && (int64_t(1) << k.lg) < k.pieces) ++k.lg;
+    k.col_units = (k.pieces + (1 << k.lg) - 1) >> k.lg;
+    const int64_t per = kThreads >> k.lg;
+    k.units = (R + per - 1) / per * k.col_units;
+  }
+  const bool many = k.units >= 4096;  // enough for four per thread and still a few workgroups per CU
+  const int64_t groups = many ? (k.units + 3) / 4 : k.units;
+  const dim3 grid((unsigned)std::min<int64_t>(groups, 1 << 22)), block(kThreads);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, op, k); };
+  if (flat)
+    many ? go(piece_kernel<Op, true, 4>) : go(piece_kernel<Op, true, 1>);
+  else
+    many ? go(piece_kernel<Op, false, 4>) : go(piece_kernel<Op, false, 1>);
+}
+
+struct MxQuantRows {
+  const uint16_t* x;
+  uint8_t *q, *s;
+  int64_t cols, blocks;  // per row
+  using In = Piece;
+  template <bool kTail>
+  __device__ __forceinline__ In load(const Where& a) const {
+    return a.live ? load_bf16<kTail>(x + a.row * cols + a.col, a.n) : zero_piece();
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void finish(const Where& a, const In& p) const {
+    const uint32_t b = block_exponent(group_amax_bits<false>(p, 4));
+    const uint32_t c = mx_codes8(p, exponent_value(b));
+    if (a.live) {
+      const int64_t piece = a.row * blocks * 4 + (a.col >> 3);
+      __builtin_nontemporal_store(c, reinterpret_cast<uint32_t*>(q) + piece);
+      if ((threadIdx.x & 3) == 0) s[piece >> 2] = (uint8_t)b;
+    }
+  }
+};
+
+struct MxDequantRows {
+  const uint8_t *q, *s;
+  uint16_t* out;
+  int64_t cols, blocks;
+  struct In {
+    uint32_t c, b;
+  };
+  template <bool kTail>
+  __device__ __forceinline__ In load(const Where& a) const {
+    In in = {0, 127};
+    if (a.live) {
+      const int64_t piece = a.row * blocks * 4 + (a.col >> 3);
+      in.c = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(q) + piece);
+      in.b = s[piece >> 2];
+    }
+    return in;
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void finish(const Where& a, const In& in) const {
+    if (a.live) store_bf16<kTail>(out + a.row * cols + a.col, mx_values8(in.c, in.b), a.n);
+  }
+};
+
+template <bool kE4M3>
+struct GroupDequant {
+  const uint8_t* q;
+  const float* s;
+  uint16_t* out;
+  int64_t cols, groups;
+  int lg_group;  // log2 of the group's pieces
+  struct In {
+    uint32_t c[2];
+    float s;
+  };
+  template <bool kTail>
+  __device__ __forceinline__ In load(const Where& a) const {
+    In in = {{0, 0}, 0.0f};
+    if (a.live && (!kTail || a.n > 0)) {
+      const uint8_t* p = q + a.row * cols + a.col;
+      if (!kTail || a.n >= 8) {
+        const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(p));
+        in.c[0] = v.x, in.c[1] = v.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (i < a.n) in.c[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+      }
+      in.s = s[a.row * groups + (a.col >> (3 + lg_group))];
+    }
+    return in;
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void finish(const Where& a, const In& in) const {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t c = in.c[k];
+      if (kE4M3) {
+        v[4 * k] = __builtin_amdgcn_cvt_f32_fp8(c, 0), v[4 * k + 1] = __builtin_amdgcn_cvt_f32_fp8(c, 1);
+        v[4 * k + 2] = __builtin_amdgcn_cvt_f32_fp8(c, 2), v[4 * k + 3] = __builtin_amdgcn_cvt_f32_fp8(c, 3);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * k + i] = (float)(int8_t)(c >> (8 * i));
+      }
+    }
+    Piece p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.w[i] = pack_bf16(v[2 * i] * in.s, v[2 * i + 1] * in.s);
+    if (a.live) store_bf16<kTail>(out + a.row * cols + a.col, p, a.n);
+  }
+};
+
+// ---- both axes in one read ----
+
+struct BothArgs {
+  const uint16_t* x;
+  uint8_t *q, *s, *q_t, *s_t;  // q and s may be null together: columns only
+  int64_t R;
+  int K, blocks_k;
+  int64_t blocks_r;
+};
+
+constexpr int kBothWaves = 4;
+// Wave w of workgroup (bx, by): rows 32 (4 by + w) .. + 31, columns 512 bx .. + 511.
+template <bool kTail>
+__global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const BothArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = 8 * ((int)blockIdx.x * 64 + lane), n = a.K - col;
+  const bool in_block = col < 32 * a.blocks_k;  // the same for four neighbouring lanes
+  for (int64_t br = (int64_t)blockIdx.y * kBothWaves + wave; br < a.blocks_r; br += (int64_t)gridDim.y * kBothWaves) {
+    const int64_t r0 = 32 * br;
+    const int rows_here = (int)(a.R - r0 < 32 ? a.R - r0 : 32);
+    Piece x[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+      x[r] = (kTail ? n > 0 && r < rows_here : true) ? load_bf16<kTail>(a.x + (r0 + r) * a.K + col, n) : zero_piece();
+    if (a.q) {
+#pragma unroll
+      for (int r4 = 0; r4 < 8; ++r4) {
+        uint32_t keep = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 4 * r4 + j;
+          const uint32_t b = block_exponent(group_amax_bits<false>(x[r], 4));
+          const uint32_t c = mx_codes8(x[r], exponent_value(b));
+          if (in_block && r < rows_here)
+            __builtin_nontemporal_store(c, reinterpret_cast<uint32_t*>(a.q) + (r0 + r) * (4 * (int64_t)a.blocks_k) + (col >> 3));
+          keep = (lane & 3) == j ? b : keep;
+        }
+        const int r = 4 * r4 + (lane & 3);  // four rows' exponents in one store
+        if (in_block && r < rows_here) a.s[(r0 + r) * a.blocks_k + (col >> 5)] = (uint8_t)keep;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {  // columns 2h and 2h + 1 of the lane
+      uint32_t m = x[0].w[h] & 0x7fff7fffu;
+#pragma unroll
+      for (int r = 1; r < 32; ++r) m = max_u16(m, x[r].w[h] & 0x7fff7fffu);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t b = block_exponent(half ? m >> 16 : m & 0xffffu);
+        const float scale = exponent_value(b);
+        u32x4 codes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          Piece p;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * k + 2 * i;
+            p.w[i] = __builtin_amdgcn_perm(x[r + 1].w[h], x[r].w[h], half ? 0x07060302u : 0x05040100u);
+          }
+          codes[k] = mx_codes8(p, scale);
+        }
+        const int c = col + 2 * h + half;
+        if (c < a.K) {
+          *reinterpret_cast<u32x4*>(a.q_t + ((int64_t)c * a.blocks_r + br) * 16) = codes;
+          a.s_t[(int64_t)c * a.blocks_r + br] = (uint8_t)b;
+        }
+      }
+    }
+  }
+}
+
+constexpr int64_t kMaxCols = int64_t(1) << 22, kMaxRows = int64_t(1) << 31;
+
+}  // namespace
+
+extern "C" {
+
+__attribute__((visibility("default"))) int mxfp4_quant(const void* x, void* q, void* s, void* q_t, void* s_t, int64_t R,
+                                                       int64_t K, hipStream_t stream) {
+  if (R < 0 || K < 0 || R > kMaxRows || K > kMaxCols) return SILUQUANT_ERR_BAD_SHAPE;
+  if (R == 0 || K == 0) return SILUQUANT_OK;
+  if (!x || (!q && !q_t) || (q == nullptr) != (s == nullptr) || (q_t == nullptr) != (s_t == nullptr))
+    return SILUQUANT_ERR_NULL_PTR;
+  if (misaligned(x, 16) || misaligned(q, 16) || misaligned(q_t, 16)) return SILUQUANT_ERR_MISALIGNED;
+  const int64_t bk = (K + 31) / 32, br = (R + 31) / 32;
+  const Span all[5] = {{x, 2 * R * K}, {q, 16 * R * bk}, {s, R * bk}, {q_t, 16 * K * br}, {s_t, K * br}};
+  for (int i = 1; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(all[i], all[j])) return SILUQUANT_ERR_OVERLAP;
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  uint8_t *qb = static_cast<uint8_t*>(q), *sb = static_cast<uint8_t*>(s);
+  if (!q_t) {
+    launch_walk(MxQuantRows{xb, qb, sb, K, bk}, R, K, 32, stream);
+  } else {
+    const BothArgs a = {xb, qb, sb, static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(s_t), R, (int)K, (int)bk, br};
+    const dim3 grid((unsigned)((K + 511) / 512), (unsigned)std::min<int64_t>((br + kBothWaves - 1) / kBothWaves, 32768));
+    if (K % 512 != 0 || R % 32 != 0)
+      hipLaunchKernelGGL((mx_quant_both_kernel<true>), grid, dim3(64 * kBothWaves), 0, stream, a);
+    else
+      hipLaunchKernelGGL((mx_quant_both_kernel<false>), grid, dim3(64 * kBothWaves), 0, stream, a);
+  }
+  return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
+}
+
+__attribute__((visibility("default"))) int mxfp4_dequant(const void* q, const void* s, void* out, int64_t R, int64_t K,
+                                                         hipStream_t stream) {
+  if (R < 0 || K < 0 || R > kMaxRows || K > kMaxCols) return SILUQUANT_ERR_BAD_SHAPE;
+  if (R == 0 || K == 0) return SILUQUANT_OK;
+  if (!q || !s || !out) return SILUQUANT_ERR_NULL_PTR;
+  if (misaligned(q, 16) || misaligned(out, 16)) return SILUQUANT_ERR_MISALIGNED;
+  const int64_t bk = (K + 31) / 32;
+  const Span o = {out, 2 * R * K};
+  if (overlap(o, {q, 16 * R * bk}) || overlap(o, {s, R * bk})) return SILUQUANT_ERR_OVERLAP;
+  launch_walk(MxDequantRows{static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s), static_cast<uint16_t*>(out), K, bk},
+              R, K, 32, stream);
+  return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
+}
+
+__attribute__((visibility("default"))) int group_dequant(const void* q, const float* s, void* out, int64_t R, int64_t K,
+                                                         int64_t group, int code_format, hipStream_t stream) {
+  if (group != 32 && group != 64 && group != 128) return SILUQUANT_ERR_BAD_GROUP;
+  if (R < 0 || K < 0 || R > kMaxRows || K > (int64_t(1) << 23) ||
+      (code_format != SILUQUANT_CODE_INT8 && code_format != SILUQUANT_CODE_E4M3))
+    return SILUQUANT_ERR_BAD_SHAPE;
+  if (R == 0 || K == 0) return SILUQUANT_OK;
+  if (!q || !s || !out) return SILUQUANT_ERR_NULL_PTR;
+  if (misaligned(q, 16) || misaligned(s, 4) || misaligned(out, 16)) return SILUQUANT_ERR_MISALIGNED;
+  const int64_t groups = (K + group - 1) / group;
+  const Span o = {out, 2 * R * K};
+  if (overlap(o, {q, R * K}) || overlap(o, {s, 4 * R * groups})) return SILUQUANT_ERR_OVERLAP;
+  const int lg = group == 32 ? 2 : group == 64 ? 3 : 4;
+  const uint8_t* qb = static_cast<const uint8_t*>(q);
+  uint16_t* ob = static_cast<uint16_t*>(out);
+  if (code_format == SILUQUANT_CODE_E4M3)
+    launch_walk(GroupDequant<true>{qb, s, ob, K, groups, lg}, R, K, group, stream);
+  else
+    launch_walk(GroupDequant<false>{qb, s, ob, K, groups, lg}, R, K, group, stream);
+  return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
+}
+
+}  // extern "C"

@@ -1,0 +1,617 @@
+// RMS norm with the residual's addition and the group quantiser of the library
+// behind it, and its backward pass, for gfx950.
+//
+//   forward   h = bf16(x + residual);  rstd = 1 / sqrt(sum(h^2) / D + eps)
+//             y = bf16((h * rstd) * w);  codes and scales of y by group
+//   backward  n = h * rstd;  g = dy * w;  c = sum(g * n) / D
+//             dx = bf16(rstd * (g - n * c) + d_h);  dw = sum over rows of dy * n
+//
+// Both read and write every element once and compute some ten operations on
+// it: they are bound by memory.  A row stays in registers between its sum and
+// its use, so nothing is read twice.  The sums are fp32; h is rounded to bf16
+// before the statistics because that is the stream the next layer and the
+// backward pass read, and y is rounded to bf16 before quantising as everywhere
+// in this library, so that codes made here are those of the bf16 y.
+//
+// Layout: one wave per row while a row fits 64 lanes x 8 pieces of 8 columns
+// (D <= 4096), so that rows need no barrier and a lane has up to 16 loads of
+// 16 bytes in flight; four waves per row up to 16384 columns, and also for
+// shorter rows when there are too few rows to fill the chip.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "rows.h"
+#include "siluquant.h"
+
+namespace {
+
+using namespace rows;
+
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
+
+// Eight codes of the bf16 values in p.  int8: p * inv is one fp32 product, and
+// adding kMagic leaves its nearest integer in the low byte.  E4M3: the hardware
+// conversion (nearest, ties to even).  kSafe serves an inverse that overflowed:
+// products clamp to the largest code, zeros stay zeros.
+template <bool kE4M3, bool kSafe>
+__device__ __forceinline__ u32x2 codes8(const Piece& p, float inv) {
+  constexpr float kTop = kE4M3 ? 448.0f : 127.0f;
+  float v[8];
+  unpack(v, p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = v[i] * inv;
+    v[i] = !kSafe ? t : v[i] == 0.0f ? v[i] : __builtin_amdgcn_fmed3f(t, -kTop, kTop);
+  }
+  u32x2 out;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float* q = v + 4 * k;
+    if (kE4M3) {
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+      out[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+    } else {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[i] + kMagic);
+      const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
+      out[k] = lo | (hi << 16);
+    }
+  }
+  return out;
+}
+
+// Scale of a group from its largest bf16 magnitude, and the scale's inverse.
+template <bool kE4M3>
+__device__ __forceinline__ float group_scale(uint32_t amax_bits) {
+  const float amax = __uint_as_float(amax_bits << 16);
+  return amax == 0.0f ? 1.0f : amax / (kE4M3 ? 448.0f : 127.0f);
+}
+
+struct NormArgs {
+  const void* x;
+  const uint16_t* residual;  // may be null, may be h itself
+  const uint16_t* weight;
+  uint8_t* q;  // null: no codes
+  float* s;
+  uint16_t* y;  // null: no bf16 y
+  uint16_t* h;  // null: no h
+  float* rstd;  // null: no statistics
+  int64_t T;
+  int D, group_lanes, groups;  // group_lanes: lanes per group (4, 8, 16)
+  float eps;
+};
+
+// h of one piece: x + residual in fp32, rounded once.
+template <bool kXF32>
+struct XPiece;
+template <>
+struct XPiece<false> {
+  Piece v;
+  template <bool kTail>
+  __device__ __forceinline__ void load(const void* x, int64_t at, int n) {
+    v = load_bf16<kTail>(static_cast<const uint16_t*>(x) + at, n);
+  }
+  __device__ __forceinline__ Piece plus(const Piece& r) const {
+    Piece o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o.w[i] = pack_bf16(bf16_lo(v.w[i]) + bf16_lo(r.w[i]), bf16_hi(v.w[i]) + bf16_hi(r.w[i]));
+    return o;
+  }
+  __device__ __forceinline__ Piece alone() const { return v; }
+};
+template <>
+struct XPiece<true> {
+  float v[8];
+  template <bool kTail>
+  __device__ __forceinline__ void load(const void* x, int64_t at, int n) {
+    load_f32<kTail>(v, static_cast<const float*>(x) + at, n);
+  }
+  __device__ __forceinline__ Piece plus(const Piece& r) const {
+    Piece o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.w[i] = pack_bf16(v[2 * i] + bf16_lo(r.w[i]), v[2 * i + 1] + bf16_hi(r.w[i]));
+    return o;
+  }
+  __device__ __forceinline__ Piece alone() const {
+    Piece o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    return o;
+  }
+};
+
+__device__ __forceinline__ float sum_squares(float acc, const Piece& p) {
+  float v[8];
+  unpack(v, p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(v[i], v[i], acc);
+  return acc;
+}
+
+__device__ __forceinline__ float inverse_rms(float sum, int D, float eps) { return 1.0f / sqrtf(sum / (float)D + eps); }
+
+// y of one piece: (h * rstd) * w, rounded to bf16.
+__device__ __forceinline__ Piece scaled(const Piece& h, const Piece& w, float rstd) {
+  Piece o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o.w[i] = pack_bf16((bf16_lo(h.w[i]) * rstd) * bf16_lo(w.w[i]), (bf16_hi(h.w[i]) * rstd) * bf16_hi(w.w[i]));
+  return o;
+}
+
+// Codes and scale of one piece's group; every lane of the wave calls it.
+template <bool kE4M3, bool kTail>
+__device__ __forceinline__ void quantise(const NormArgs& a, const Piece& y, int64_t row, int col, int n) {
+  const uint32_t amax = group_amax_bits<true>(y, a.group_lanes);
+  const float scale = group_scale<kE4M3>(amax);
+  const float inv = 1.0f / scale;
+  u32x2 c = codes8<kE4M3, false>(y, inv);
+  if (__any(inv == __builtin_huge_valf())) c = codes8<kE4M3, true>(y, inv);
+  if (n > 0) {
+    store_codes<kTail>(a.q + row * a.D + col, c.x, c.y, n);
+    if ((threadIdx.x & (a.group_lanes - 1)) == 0) a.s[row * a.groups + col / (8 * a.group_lanes)] = scale;
+  }
+}
+
+// kWaves waves per row (1: the workgroup's four waves take a row each), each
+// lane kChunks pieces; kTail: D is not a multiple of 8 or of the row's pieces.
+template <int kWaves, int kChunks, bool kXF32, bool kTail, bool kE4M3>
+__global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void rms_norm_quant_kernel(const NormArgs a) {
+  constexpr int kRowsPerGroup = kWaves == 1 ? 4 : 1;
+  __shared__ float s_sum[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = 8 * (kWaves == 1 ? lane : (int)threadIdx.x);  // column of piece 0; pieces are kWaves * 512 apart
+  constexpr int kStep = 512 * kWaves;
+  for (int64_t row = (int64_t)blockIdx.x * kRowsPerGroup + (kWaves == 1 ? wave : 0); row < a.T;
+       row += (int64_t)gridDim.x * kRowsPerGroup) {
+    const int64_t at = row * a.D;
+    XPiece<kXF32> x[kChunks];
+    Piece h[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) x[c].template load<kTail>(a.x, at + first + c * kStep, a.D - first - c * kStep);
+    if (a.residual) {
+      Piece r[kChunks];
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        r[c] = load_bf16<kTail>(a.residual + at + first + c * kStep, a.D - first - c * kStep);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) h[c] = x[c].plus(r[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) h[c] = x[c].alone();
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) sum = sum_squares(sum, h[c]);
+    sum = wave_sum(sum);
+    if (kWaves > 1) {
+      if (lane == 0) s_sum[wave] = sum;
+      __syncthreads();
+      sum = s_sum[0];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) sum += s_sum[i];
+      __syncthreads();  // before the next row's sums
+    }
+    const float rstd = inverse_rms(sum, a.D, a.eps);
+    if (a.rstd && first == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int col = first + c * kStep, n = a.D - col;
+      if (kTail && __all(n <= 0)) break;
+      const Piece w = load_bf16<kTail>(a.weight + col, n);
+      if (a.h) store_bf16<kTail>(a.h + at + col, h[c], n);
+      const Piece y = scaled(h[c], w, rstd);
+      if (a.y) store_bf16<kTail>(a.y + at + col, y, n);
+      if (a.q) quantise<kE4M3, kTail>(a, y, row, col, n);
+    }
+  }
+}
+
+// Rows past 16384 columns: a workgroup of 1024 walks the row twice, the second
+// time from h where it is kept (a lane reads back what it wrote itself).
+constexpr int kWideThreads = 1024;
+template <bool kXF32, bool kE4M3>
+__global__ __launch_bounds__(kWideThreads) void rms_norm_quant_wide_kernel(const NormArgs a) {
+  __shared__ float s_sum[kWideThreads / 64];
+  const int tid = threadIdx.x;
+  const int steps = (a.D + 8 * kWideThreads - 1) / (8 * kWideThreads);
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const int64_t at = row * a.D;
+    auto h_piece = [&](int col) {
+      const int n = a.D - col;
+      XPiece<kXF32> x;
+      x.template load<true>(a.x, at + col, n);
+      return a.residual ? x.plus(load_bf16<true>(a.residual + at + col, n)) : x.alone();
+    };
+    float sum = 0.0f;
+    for (int i = 0; i < steps; ++i) {
+      const int col = 8 * (i * kWideThreads + tid);
+      const Piece h = h_piece(col);
+      if (a.h) store_bf16<true>(a.h + at + col, h, a.D - col);
+      sum = sum_squares(sum, h);
+    }
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
+    __syncthreads();
+    sum = s_sum[0];
+    for (int i = 1; i < kWideThreads / 64; ++i) sum += s_sum[i];
+    __syncthreads();
+    const float rstd = inverse_rms(sum, a.D, a.eps);
+    if (a.rstd && tid == 0) a.rstd[row] = rstd;
+    for (int i = 0; i < steps; ++i) {
+      const int col = 8 * (i * kWideThreads + tid), n = a.D - col;
+      const Piece h = a.h ? load_bf16<true>(a.h + at + col, n) : h_piece(col);
+      const Piece y = scaled(h, load_bf16<true>(a.weight + col, n), rstd);
+      if (a.y) store_bf16<true>(a.y + at + col, y, n);
+      if (a.q) quantise<kE4M3, true>(a, y, row, col, n);
+    }
+  }
+}
+
+// ---- backward ----
+
+struct BwdArgs {
+  const void* dy;
+  const uint16_t* h;
+  const uint16_t* weight;
+  const float* rstd;
+  const uint16_t* d_h;  // may be null, may be dx itself
+  uint16_t* dx;
+  float* part;  // [gridDim.x, D] partial sums of dw (dw itself when there is one workgroup); null: no dw
+  int64_t T;
+  int D;
+};
+
+template <bool kF32, bool kTail>
+__device__ __forceinline__ void load_grad(float (&v)[8], const void* p, int64_t at, int n) {
+  if constexpr (kF32)
+    load_f32<kTail>(v, static_cast<const float*>(p) + at, n);
+  else
+    unpack(v, load_bf16<kTail>(static_cast<const uint16_t*>(p) + at, n));
+}
+
+// kWaves == 1: each of the workgroup's waves (blockDim.x / 64 of them) walks
+// rows of its own; kWaves == 4: the workgroup's four waves share a row.  A
+// lane keeps the dw sums of its columns in registers over all its rows; the
+// waves' sums are added in LDS at the end, in wave order, so that the result
+// does not depend on timing.
+template <int kWaves, int kChunks, bool kDyF32, bool kTail>
+__global__ __launch_bounds__(kWaves == 1 ? 512 : 64 * kWaves) void rms_norm_bwd_kernel(const BwdArgs a) {
+  __shared__ float s_dw[kWaves == 1 ? 512 * kChunks : 1];
+  __shared__ float s_sum[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int first = 8 * (kWaves == 1 ? lane : (int)threadIdx.x);
+  constexpr int kStep = 512 * kWaves;
+  Piece w[kChunks];
+  float dw[kChunks][8];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    w[c] = load_bf16<kTail>(a.weight + first + c * kStep, a.D - first - c * kStep);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
+  }
+  const int64_t per_group = kWaves == 1 ? waves : 1;
+  for (int64_t row = blockIdx.x * per_group + (kWaves == 1 ? wave : 0); row < a.T; row += gridDim.x * per_group) {
+    const int64_t at = row * a.D;
+    const float rstd = a.rstd[row];
+    float dy[kChunks][8];
+    Piece h[kChunks], d[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int col = first + c * kStep, n = a.D - col;
+      load_grad<kDyF32, kTail>(dy[c], a.dy, at + col, n);
+      h[c] = load_bf16<kTail>(a.h + at + col, n);
+    }
+    if (a.d_h) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        d[c] = load_bf16<kTail>(a.d_h + at + first + c * kStep, a.D - first - c * kStep);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) d[c] = zero_piece();
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float hv[8], wv[8];
+      unpack(hv, h[c]);
+      unpack(wv, w[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = hv[i] * rstd;
+        dw[c][i] = __builtin_fmaf(dy[c][i], n, dw[c][i]);
+        sum = __builtin_fmaf(dy[c][i] * wv[i], n, sum);
+      }
+    }
+    sum = wave_sum(sum);
+    if (kWaves > 1) {
+      if (lane == 0) s_sum[wave] = sum;
+      __syncthreads();
+      sum = s_sum[0];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) sum += s_sum[i];
+      __syncthreads();
+    }
+    const float mean = sum / (float)a.D;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float hv[8], wv[8], dv[8], o[8];
+      unpack(hv, h[c]);
+      unpack(wv, w[c]);
+      unpack(dv, d[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = hv[i] * rstd, g = dy[c][i] * wv[i];
+        o[i] = __builtin_fmaf(rstd, __builtin_fmaf(-n, mean, g), dv[i]);
+      }
+      const int col = first + c * kStep;
+      const Piece out = {{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])}};
+      store_bf16<kTail>(a.dx + at + col, out, a.D - col);
+    }
+  }
+  if (!a.part) return;
+  if (kWaves == 1) {
+    // wave by wave into LDS; a lane only ever touches the places of its own columns
+    for (int turn = 0; turn < waves; ++turn) {
+      if (wave == turn) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float* p = &s_dw[(c * 8 + i) * 64 + lane];
+            if (turn > 0) dw[c][i] += *p;
+            *p = dw[c][i];
+          }
+      }
+      __syncthreads();
+    }
+    if (wave != waves - 1) return;
+  }
+  float* out = a.part + (int64_t)blockIdx.x * a.D;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int col = first + c * kStep + i;
+      if (col < a.D) out[col] = dw[c][i];
+    }
+}
+
+// dw[d] = the sum of the partial rows, in row order within each of 16 strips
+// and then in strip order: 64 columns per workgroup.
+constexpr int kSumStrips = 16;
+__global__ __launch_bounds__(64 * kSumStrips) void rms_norm_dw_kernel(const float* part, float* dw, int parts, int D) {
+  __shared__ float s[kSumStrips][64];
+  const int lane = threadIdx.x & 63, strip = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float sum = 0.0f;
+  if (col < D)
+    for (int p = strip; p < parts; p += kSumStrips) sum += part[(int64_t)p * D + col];
+  s[strip][lane] = sum;
+  __syncthreads();
+  if (strip == 0 && col < D) {
+    for (int i = 1; i < kSumStrips; ++i) sum += s[i][lane];
+    dw[col] = sum;
+  }
+}
+
+// Rows past 16384 columns, in two launches: a workgroup per row for the mean,
+// then tiles of columns over strips of rows.
+template <bool kDyF32>
+__global__ __launch_bounds__(kWideThreads) void rms_norm_bwd_mean_kernel(const BwdArgs a, float* mean) {
+  __shared__ float s_sum[kWideThreads / 64];
+  const int tid = threadIdx.x;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const float rstd = a.rstd[row];
+    float sum = 0.0f;
+    for (int col = 8 * tid; col < a.D; col += 8 * kWideThreads) {
+      float dy[8], hv[8], wv[8];
+      load_grad<kDyF32, true>(dy, a.dy, row * a.D + col, a.D - col);
+      unpack(hv, load_bf16<true>(a.h + row * a.D + col, a.D - col));
+      unpack(wv, load_bf16<true>(a.weight + col, a.D - col));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(dy[i] * wv[i], hv[i] * rstd, sum);
+    }
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      for (int i = 1; i < kWideThreads / 64; ++i) sum += s_sum[i];
+      mean[row] = sum / (float)a.D;
+    }
+    __syncthreads();
+  }
+}
+constexpr int kTileThreads = 256;
+template <bool kDyF32>
+__global__ __launch_bounds__(kTileThreads) void rms_norm_bwd_tile_kernel(const BwdArgs a, const float* mean) {
+  const int col = 8 * ((int)blockIdx.x * kTileThreads + (int)threadIdx.x), n = a.D - col;
+  if (n <= 0) return;
+  float wv[8], dw[8] = {};
+  unpack(wv, load_bf16<true>(a.weight + col, n));
+  for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
+    const float rstd = a.rstd[row], m = mean[row];
+    float dy[8], hv[8], dv[8], o[8];
+    load_grad<kDyF32, true>(dy, a.dy, row * a.D + col, n);
+    unpack(hv, load_bf16<true>(a.h + row * a.D + col, n));
+    unpack(dv, a.d_h ? load_bf16<true>(a.d_h + row * a.D + col, n) : zero_piece());
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = hv[i] * rstd;
+      dw[i] = __builtin_fmaf(dy[i], t, dw[i]);
+      o[i] = __builtin_fmaf(rstd, __builtin_fmaf(-t, m, dy[i] * wv[i]), dv[i]);
+    }
+    const Piece out = {{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])}};
+    store_bf16<true>(a.dx + row * a.D + col, out, n);
+  }
+  if (a.part) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) a.part[(int64_t)blockIdx.y * a.D + col + i] = dw[i];
+  }
+}
+
+constexpr int64_t kMaxD = int64_t(1) << 22, kMaxT = int64_t(1) << 31;
+constexpr int kRegisterD = 16384;  // rows up to here stay in registers
+constexpr int kMaxGrid = 1 << 20;  // workgroups of the forward kernels; further rows are walked
+
+// Workgroups of the backward pass, each with a partial dw row.
+int bwd_parts(int64_t T, int64_t D) { return (int)std::min<int64_t>(T, D <= 2048 ? 256 : 512); }
+
+template <int kWaves, int kChunks>
+void launch_norm(const NormArgs& a, bool f32, bool tail, bool e4m3, hipStream_t stream) {
+  const int64_t groups = kWaves == 1 ? (a.T + 3) / 4 : a.T;
+  const dim3 grid((unsigned)std::min<int64_t>(groups, kMaxGrid)), block(kWaves == 1 ? 256 : 64 * kWaves);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+  auto pick = [&](auto f, auto t) {
+    if (e4m3)
+      go(rms_norm_quant_kernel<kWaves, kChunks, decltype(f)::value, decltype(t)::value, true>);
+    else
+      go(rms_norm_quant_kernel<kWaves, kChunks, decltype(f)::value, decltype(t)::value, false>);
+  };
+  using Y = std::true_type;
+  using N = std::false_type;
+  f32 ? (tail ? pick(Y{}, Y{}) : pick(Y{}, N{})) : (tail ? pick(N{}, Y{}) : pick(N{}, N{}));
+}
+
+template <int kWaves, int kChunks>
+void launch_bwd(const BwdArgs& a, bool f32, bool tail, int grid, int threads, hipStream_t stream) {
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, stream, a); };
+  if (f32)
+    tail ? go(rms_norm_bwd_kernel<kWaves, kChunks, true, true>) : go(rms_norm_bwd_kernel<kWaves, kChunks, true, false>);
+  else
+    tail ? go(rms_norm_bwd_kernel<kWaves, kChunks, false, true>) : go(rms_norm_bwd_kernel<kWaves, kChunks, false, false>);
+}
+
+}  // namespace
+
+extern "C" {
+
+__attribute__((visibility("default"))) int rms_norm_quant(const void* x, int x_dtype, const void* residual,
+                                                          const void* weight, void* y_q, float* y_s, void* y_bf16,
+                                                          void* h, float* rstd, int64_t T, int64_t D, int64_t group,
+                                                          int code_format, float eps, hipStream_t stream) {
+  if (group != 32 && group != 64 && group != 128) return SILUQUANT_ERR_BAD_GROUP;
+  if (T < 0 || D < 0 || T > kMaxT || D > kMaxD || !(eps >= 0.0f) || eps == __builtin_huge_valf() ||
+      (x_dtype != SILUQUANT_F32 && x_dtype != SILUQUANT_BF16) ||
+      (code_format != SILUQUANT_CODE_INT8 && code_format != SILUQUANT_CODE_E4M3))
+    return SILUQUANT_ERR_BAD_SHAPE;
+  if (T == 0 || D == 0) return SILUQUANT_OK;
+  if (!x || !weight || (!y_q && !y_bf16) || (y_q == nullptr) != (y_s == nullptr)) return SILUQUANT_ERR_NULL_PTR;
+  if (misaligned(x, 16) || misaligned(residual, 16) || misaligned(weight, 16) || misaligned(y_q, 16) ||
+      misaligned(y_bf16, 16) || misaligned(h, 16) || misaligned(y_s, 4) || misaligned(rstd, 4))
+    return SILUQUANT_ERR_MISALIGNED;
+  const bool f32 = x_dtype == SILUQUANT_F32;
+  const int64_t groups = (D + group - 1) / group;
+  const Span in[3] = {{x, T * D * (f32 ? 4 : 2)}, {residual, 2 * T * D}, {weight, 2 * D}};
+  const Span out[5] = {{y_q, T * D}, {y_s, 4 * T * groups}, {y_bf16, 2 * T * D}, {h, 2 * T * D}, {rstd, 4 * T}};
+  for (int o = 0; o < 5; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (overlap(out[o], in[i]) && !(o == 3 && i == 1 && h == residual)) return SILUQUANT_ERR_OVERLAP;
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o], out[i])) return SILUQUANT_ERR_OVERLAP;
+  }
+  const bool e4m3 = code_format == SILUQUANT_CODE_E4M3;
+  const NormArgs a = {x, static_cast<const uint16_t*>(residual), static_cast<const uint16_t*>(weight),
+                      static_cast<uint8_t*>(y_q), y_s, static_cast<uint16_t*>(y_bf16), static_cast<uint16_t*>(h),
+                      rstd, T, (int)D, (int)(group / 8), (int)groups, eps};
+  if (D > kRegisterD) {
+    const dim3 grid((unsigned)std::min<int64_t>(T, kMaxGrid)), block(kWideThreads);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+    if (f32)
+      e4m3 ? go(rms_norm_quant_wide_kernel<true, true>) : go(rms_norm_quant_wide_kernel<true, false>);
+    else
+      e4m3 ? go(rms_norm_quant_wide_kernel<false, true>) : go(rms_norm_quant_wide_kernel<false, false>);
+  } else {
+    const bool few = T < 2048;  // too few rows for a wave each to fill 256 CUs
+    auto tail = [&](int columns) { return D % columns != 0; };
+    if (D <= 512) launch_norm<1, 1>(a, f32, tail(512), e4m3, stream);
+    else if (few && D <= 2048) launch_norm<4, 1>(a, f32, tail(2048), e4m3, stream);
+    else if (few && D <= 4096) launch_norm<4, 2>(a, f32, tail(4096), e4m3, stream);
+    else if (D <= 1024) launch_norm<1, 2>(a, f32, tail(1024), e4m3, stream);
+    else if (D <= 2048) launch_norm<1, 4>(a, f32, tail(2048), e4m3, stream);
+    else if (D <= 4096) launch_norm<1, 8>(a, f32, tail(4096), e4m3, stream);
+    else if (D <= 8192) launch_norm<4, 4>(a, f32, tail(8192), e4m3, stream);
+    else launch_norm<4, 8>(a, f32, tail(16384), e4m3, stream);
+  }
+  return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
+}
+
+__attribute__((visibility("default"))) int64_t rms_norm_bwd_workspace_bytes(int64_t T, int64_t D) {
+  if (T < 0 || D < 0 || T > kMaxT || D > kMaxD) return -1;
+  if (T == 0 || D == 0) return 0;
+  return 4 * bwd_parts(T, D) * D + (D > kRegisterD ? 4 * T : 0);
+}
+
+__attribute__((visibility("default"))) int rms_norm_bwd(const void* dy, int dy_dtype, const void* h, const void* weight,
+                                                        const float* rstd, const void* d_h, void* dx, float* dw,
+                                                        void* workspace, int64_t workspace_bytes, int64_t T, int64_t D,
+                                                        hipStream_t stream) {
+  if (T < 0 || D < 0 || T > kMaxT || D > kMaxD || (dy_dtype != SILUQUANT_F32 && dy_dtype != SILUQUANT_BF16))
+    return SILUQUANT_ERR_BAD_SHAPE;
+  if (D == 0) return SILUQUANT_OK;
+  const int64_t need = rms_norm_bwd_workspace_bytes(T, D);
+  if (T == 0) {  // no rows: no gradient for the weight
+    if (!dw) return SILUQUANT_OK;
+    if (misaligned(dw, 4)) return SILUQUANT_ERR_MISALIGNED;
+    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((D + 63) / 64)), dim3(64 * kSumStrips), 0, stream,
+                       (const float*)nullptr, dw, 0, (int)D);
+    return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
+  }
+  const bool wide = D > kRegisterD;
+  if (!dy || !h || !weight || !rstd || !dx || ((dw || wide) && !workspace)) return SILUQUANT_ERR_NULL_PTR;
+  if (workspace_bytes < ((dw || wide) ? need : 0)) return SILUQUANT_ERR_BAD_SHAPE;
+  if (misaligned(dy, 16) || misaligned(h, 16) || misaligned(weight, 16) || misaligned(d_h, 16) || misaligned(dx, 16) ||
+      misaligned(rstd, 4) || misaligned(dw, 4) || misaligned(workspace, 16))
+    return SILUQUANT_ERR_MISALIGNED;
+  const bool f32 = dy_dtype == SILUQUANT_F32;
+  const Span in[5] = {{dy, T * D * (f32 ? 4 : 2)}, {h, 2 * T * D}, {weight, 2 * D}, {rstd, 4 * T}, {d_h, 2 * T * D}};
+  const Span out[3] = {{dx, 2 * T * D}, {dw, 4 * D}, {workspace, workspace_bytes}};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 5; ++i)
+      if (overlap(out[o], in[i]) && !(o == 0 && i == 4 && dx == d_h)) return SILUQUANT_ERR_OVERLAP;
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o], out[i])) return SILUQUANT_ERR_OVERLAP;
+  }
+  const int parts = bwd_parts(T, D);
+  float* ws = static_cast<float*>(workspace);
+  float* part = !dw ? nullptr : parts == 1 ? dw : ws;
+  const BwdArgs a = {dy, static_cast<const uint16_t*>(h), static_cast<const uint16_t*>(weight), rstd,
+                     static_cast<const uint16_t*>(d_h), static_cast<uint16_t*>(dx), part, T, (int)D};
+  if (wide) {
+    float* mean = ws + (int64_t)parts * D;
+    const dim3 rows_grid((unsigned)std::min<int64_t>(T, kMaxGrid));
+    const dim3 tiles((unsigned)((D + 8 * kTileThreads - 1) / (8 * kTileThreads)), (unsigned)parts);
+    if (f32) {
+      hipLaunchKernelGGL((rms_norm_bwd_mean_kernel<true>), rows_grid, dim3(kWideThreads), 0, stream, a, mean);
+      hipLaunchKernelGGL((rms_norm_bwd_tile_kernel<true>), tiles, dim3(kTileThreads), 0, stream, a, mean);
+    } else {
+      hipLaunchKernelGGL((rms_norm_bwd_mean_kernel<false>), rows_grid, dim3(kWideThreads), 0, stream, a, mean);
+      hipLaunchKernelGGL((rms_norm_bwd_tile_kernel<false>), tiles, dim3(kTileThreads), 0, stream, a, mean);
+    }
+  } else {
+    const int waves = (int)std::min<int64_t>((T + parts - 1) / parts, 8);
+    auto tail = [&](int columns) { return D % columns != 0; };
+    if (D <= 512) launch_bwd<1, 1>(a, f32, tail(512), parts, 64 * waves, stream);
+    else if (D <= 1024) launch_bwd<1, 2>(a, f32, tail(1024), parts, 64 * waves, stream);
+    else if (D <= 2048) launch_bwd<1, 4>(a, f32, tail(2048), parts, 64 * waves, stream);
+    else if (D <= 4096) launch_bwd<4, 2>(a, f32, tail(4096), parts, 256, stream);
+    else if (D <= 8192) launch_bwd<4, 4>(a, f32, tail(8192), parts, 256, stream);
+    else launch_bwd<4, 8>(a, f32, tail(16384), parts, 256, stream);
+  }
+  if (dw && parts > 1)
+    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((D + 63) / 64)), dim3(64 * kSumStrips), 0, stream, part, dw,
+                       parts, (int)D);
+  return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
+}
+
+}  // extern "C"
