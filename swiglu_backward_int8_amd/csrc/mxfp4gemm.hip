@@ -59,14 +59,18 @@ __device__ __forceinline__ void store4(void* C, int64_t at, const f32x4& v, int6
     if (left >= 4) {
       *reinterpret_cast<u32x2_a2*>(p) = w;
     } else {
-      for (int i = 0; i < left; ++i) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < left) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
   } else {
     float* p = static_cast<float*>(C) + at;
     if (left >= 4) {
       *reinterpret_cast<f32x4_a4*>(p) = v;
     } else {
-      for (int i = 0; i < left; ++i) p[i] = v[i];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < left) p[i] = v[i];
     }
   }
 }
@@ -177,6 +181,251 @@ __global__ __launch_bounds__(64 * kW) void mx_gemm_stream_kernel(const GemmArgs 
   }
 }
 
+// ---- many rows: tiles through LDS ----
+//
+// 256 threads, four waves in a 2 x 2 grid, a tile of 64 kF x 64 kF results; a
+// wave owns kF x kF blocks of 32 x 32.  A stage is 256 values (8 blocks, 128
+// bytes) of every row of the tile: the codes go from memory straight into LDS
+// (buffer loads with the lds flag), double buffered, the exponents into
+// registers.  Rows of 128 bytes lie in LDS as eight 16-byte chunks, chunk c of
+// row r at c ^ swz(r), so that the 16 lanes that read a chunk of consecutive
+// rows fall on distinct banks.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kStageBlocks = 8;                 // per row and stage
+constexpr int kRowBytes = 16 * kStageBlocks;    // 128
+constexpr int kTileThreads = 256;
+constexpr int kRasterRows = 4;                  // tile rows that are walked column by column together
+
+__device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+// Buffer resource words: base, 32-bit record count (loads at or past it read
+// as zeros), raw addressing.
+__device__ __forceinline__ i32x4 rsrc_words(const void* base, int bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return (i32x4){__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF),
+                 __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
+}
+
+// Each lane reads 16 bytes at voff + soff; the wave writes them, lane by lane,
+// to consecutive LDS bytes from address lds (M0) on.  Written as asm so that
+// the compiler does not wait for them before every LDS read; the kernel waits
+// itself.  The leading s_nop is the wait state between the compiler's write of
+// M0 and its use.
+__device__ __forceinline__ void lds_load16(i32x4 rs, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(voff), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                 "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+
+template <int kByte>
+__device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb, const f32x16& c) {
+  const i32x8 wa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8 wb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, wb, c, kFp4, kFp4, kByte, (int)sa, kByte, (int)sb);
+}
+
+template <int kF, bool kBf16Out>
+__global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
+  constexpr int kT = 64 * kF;                        // rows of A, and of B, per tile
+  constexpr int kOpBytes = kT * kRowBytes;           // one operand's stage
+  constexpr int kLoads = kT / 8 / 4;                 // wave-wide loads per operand and stage: 8 rows each
+  __shared__ __attribute__((aligned(16))) char s_tile[2][2 * kOpBytes];
+
+  // Each XCD takes a contiguous range of tiles, in groups of kRasterRows tile
+  // rows walked column by column, so that the tiles resident on one XCD share
+  // their operands in its L2.
+  const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if (tile >= a.tiles_m * a.tiles_n) return;
+  const int per_group = kRasterRows * a.tiles_n;
+  const int first_m = (tile / per_group) * kRasterRows;
+  const int in_group = tile % per_group;
+  const int gsz = min(a.tiles_m - first_m, kRasterRows);
+  const int64_t m0 = (int64_t)(first_m + in_group % gsz) * kT, n0 = (int64_t)(in_group / gsz) * kT;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave >> 1) * 32 * kF, wn = (wave & 1) * 32 * kF;
+  const int lrow = lane & 31, half = lane >> 5;
+  const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;
+  const int64_t row_bytes = (int64_t)a.blocks * 16;
+
+  // Rows past M or N read as zeros: the record count ends at the last row.
+  const int rows_a = a.M - m0 < kT ? (int)(a.M - m0) : kT, rows_b = a.N - n0 < kT ? (int)(a.N - n0) : kT;
+  const uint8_t *codes_a = a.A + m0 * row_bytes, *codes_b = a.B + n0 * row_bytes;
+  const int bytes_a = (int)(rows_a * row_bytes), bytes_b = (int)(rows_b * row_bytes);
+  // Load i of this wave covers rows 8 (kLoads w + i) .. + 7 of an operand: lane
+  // L writes row L / 8, physical chunk L % 8, and so reads chunk (L % 8) ^ swz.
+  uint32_t voff[kLoads], voff_last[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 8 * (kLoads * wave + i) + (lane >> 3);
+    const int c = (lane & 7) ^ swz(r);
+    voff[i] = (uint32_t)(r * row_bytes + 16 * c);
+    voff_last[i] = (stages - 1) * kStageBlocks + c < a.blocks ? voff[i] : 0x80000000u;  // past K: zeros
+  }
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(&s_tile[0][0]);
+  // Load i of stage s, A's and B's; past the last stage nothing is read (a
+  // record count of 0) and zeros land in a buffer that nobody reads.  The loop
+  // below has no branches but its own, or the compiler would gather the
+  // multiplications in one of its blocks.
+  auto issue = [&](int s, int i) {
+    const uint32_t at = lds0 + (s & 1) * 2 * kOpBytes + 8 * (kLoads * wave + i) * kRowBytes;
+    const uint32_t v = s == stages - 1 ? voff_last[i] : voff[i];
+    const int live = (s - stages) >> 31;  // all ones before the end
+    lds_load16(rsrc_words(codes_a, bytes_a & live), at, v, (uint32_t)(s * kRowBytes));
+    lds_load16(rsrc_words(codes_b, bytes_b & live), at + kOpBytes, v, (uint32_t)(s * kRowBytes));
+  };
+
+  // Exponents: lane (row, half) multiplies blocks 4 half .. 4 half + 3 of a
+  // stage, four bytes of its row.  In the stage in which K ends the word may
+  // reach into the next row, or past the last row's end (there it is read
+  // earlier and shifted): what is not the row's is replaced by 127, and the
+  // codes there are zeros.
+  const uint8_t *ea = a.sA + m0 * a.blocks, *eb = a.sB + n0 * a.blocks;
+  const uint32_t last_a = (uint32_t)(rows_a * a.blocks) - 4, last_b = (uint32_t)(rows_b * a.blocks) - 4;
+  uint32_t ra0[kF], rb0[kF];
+#pragma unroll
+  for (int i = 0; i < kF; ++i) {
+    ra0[i] = (uint32_t)(min(wm + 32 * i + lrow, rows_a - 1) * a.blocks + 4 * half);
+    rb0[i] = (uint32_t)(min(wn + 32 * i + lrow, rows_b - 1) * a.blocks + 4 * half);
+  }
+  uint32_t keep_last = 0;  // which of the last stage's bytes are the row's
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if ((stages - 1) * kStageBlocks + 4 * half + j < a.blocks) keep_last |= 0xffu << (8 * j);
+  uint32_t sa[kF], sb[kF], sa_next[kF], sb_next[kF];
+  auto exponents = [&](int s, uint32_t (&xa)[kF], uint32_t (&xb)[kF]) {
+#pragma unroll
+    for (int i = 0; i < kF; ++i) {
+      xa[i] = *reinterpret_cast<const u32_a1*>(ea + min(ra0[i] + s * kStageBlocks, last_a));
+      xb[i] = *reinterpret_cast<const u32_a1*>(eb + min(rb0[i] + s * kStageBlocks, last_b));
+    }
+  };
+  auto finish_exponents = [&](int s, uint32_t (&xa)[kF], uint32_t (&xb)[kF]) {
+    const uint32_t keep = s == stages - 1 ? keep_last : ~0u;
+#pragma unroll
+    for (int i = 0; i < kF; ++i) {
+      const uint32_t oa = ra0[i] + s * kStageBlocks, ob = rb0[i] + s * kStageBlocks;
+      xa[i] = ((xa[i] >> (8 * ((oa - min(oa, last_a)) & 3))) & keep) | (0x7f7f7f7fu & ~keep);
+      xb[i] = ((xb[i] >> (8 * ((ob - min(ob, last_b)) & 3))) & keep) | (0x7f7f7f7fu & ~keep);
+    }
+  };
+
+  // Step j of a stage reads chunk 4 half + j of the wave's rows; block i's row
+  // is 32 i further, which flips bit 2 of the chunk for odd i.
+  const int base_a = (wm + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(wm + lrow));
+  const int base_b = kOpBytes + (wn + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(wn + lrow));
+  u32x4 fa[2][kF], fb[2][kF];
+  auto read = [&](int s, int j, int i) {
+    const char* t = s_tile[s & 1];
+    fa[j & 1][i] = *reinterpret_cast<const u32x4*>(t + (base_a ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
+    fb[j & 1][i] = *reinterpret_cast<const u32x4*>(t + (base_b ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
+  };
+
+  f32x16 acc[kF][kF];
+#pragma unroll
+  for (int i = 0; i < kF; ++i)
+#pragma unroll
+    for (int j = 0; j < kF; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  // Step j of a stage: row by row of its blocks, kF multiplications and then
+  // the reads of the next step's operands (and loads of a later stage), in the
+  // order written, so that the matrix cores never wait for an issue.
+  auto step = [&](auto which, auto&& between) {
+    constexpr int j = decltype(which)::value;
+#pragma unroll
+    for (int i = 0; i < kF; ++i) {
+#pragma unroll
+      for (int k = 0; k < kF; ++k) acc[i][k] = mfma32<j>(fb[j & 1][k], sb[k], fa[j & 1][i], sa[i], acc[i][k]);
+      between(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using std::integral_constant;
+
+  // Before the last step of a stage every wave has read all of it: there the
+  // next stage's loads are waited for, and after the barrier the loads of the
+  // stage after it go into the buffer that has just been read, spread over
+  // that last step and the first one of the next stage.
+  if (stages > 0) {
+    constexpr int kPerRow = kLoads / kF / 2;  // loads after each row of blocks of the two steps
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) issue(0, i);
+    exponents(0, sa, sb);
+    finish_exponents(0, sa, sb);
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kLoads / 2; ++i) issue(1, i);
+#pragma unroll
+    for (int i = 0; i < kF; ++i) read(0, 0, i);
+#pragma unroll 1
+    for (int s = 0; s < stages; ++s) {
+      exponents(s + 1, sa_next, sb_next);
+      __builtin_amdgcn_sched_barrier(0);
+      step(integral_constant<int, 0>{}, [&](int i) {
+        read(s, 1, i);
+#pragma unroll
+        for (int l = 0; l < kPerRow; ++l) issue(s + 1, kLoads / 2 + kPerRow * i + l);
+      });
+      step(integral_constant<int, 1>{}, [&](int i) { read(s, 2, i); });
+      step(integral_constant<int, 2>{}, [&](int i) { read(s, 3, i); });
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+      // the exponents are used here, so that the compiler's own wait for them
+      // comes before the next loads and not after
+      finish_exponents(s + 1, sa_next, sb_next);
+#pragma unroll
+      for (int i = 0; i < kF; ++i) asm volatile("" : "+v"(sa_next[i]), "+v"(sb_next[i]));
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+      step(integral_constant<int, 3>{}, [&](int i) {
+        read(s + 1, 0, i);
+#pragma unroll
+        for (int l = 0; l < kPerRow; ++l) issue(s + 2, kPerRow * i + l);
+      });
+#pragma unroll
+      for (int i = 0; i < kF; ++i) sa[i] = sa_next[i], sb[i] = sb_next[i];
+    }
+    // the loads past the last stage write LDS: they end before the workgroup does
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  }
+
+  // The B rows come first in the instruction, so that a lane holds four
+  // consecutive columns: D[row 8 q + 4 half + e][column lrow], q = r / 4, e = r % 4.
+#pragma unroll
+  for (int i = 0; i < kF; ++i) {
+    const int64_t m = m0 + wm + 32 * i + lrow;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int k = 0; k < kF; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = n0 + wn + 32 * k + 8 * q + 4 * half;
+        const f32x4 v = {acc[i][k][4 * q], acc[i][k][4 * q + 1], acc[i][k][4 * q + 2], acc[i][k][4 * q + 3]};
+        if (n < a.N) store4<kBf16Out>(a.C, m * a.N + n, v, a.N - n);
+      }
+  }
+}
+
+template <int kF>
+void launch_tile(GemmArgs a, bool bf16, hipStream_t stream) {
+  a.tiles_m = (int)((a.M + 64 * kF - 1) / (64 * kF));
+  a.tiles_n = (int)((a.N + 64 * kF - 1) / (64 * kF));
+  const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
+  const dim3 grid(8 * per_xcd), block(kTileThreads);
+  if (bf16)
+    hipLaunchKernelGGL((mx_gemm_tile_kernel<kF, true>), grid, block, 0, stream, a, per_xcd);
+  else
+    hipLaunchKernelGGL((mx_gemm_tile_kernel<kF, false>), grid, block, 0, stream, a, per_xcd);
+}
+
 template <int kM, int kN, int kW>
 void launch_stream(GemmArgs a, bool bf16, hipStream_t stream) {
   a.tiles_m = (int)((a.M + 16 * kM - 1) / (16 * kM));
@@ -214,8 +463,10 @@ __attribute__((visibility("default"))) int mxfp4_gemm(const void* A, const void*
     launch_stream<1, 1, 8>(a, bf16, stream);
   else if (M <= 64)
     launch_stream<2, 2, 8>(a, bf16, stream);
+  else if (((M + 255) / 256) * ((N + 255) / 256) >= 128)
+    launch_tile<4>(a, bf16, stream);
   else
-    launch_stream<4, 4, 4>(a, bf16, stream);
+    launch_tile<2>(a, bf16, stream);
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }
 
