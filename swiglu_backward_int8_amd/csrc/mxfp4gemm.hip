@@ -75,6 +75,30 @@ __device__ __forceinline__ void store4(void* C, int64_t at, const f32x4& v, int6
   }
 }
 
+// A 16-byte chunk of a row of C, `left` columns of which exist at the least.
+template <bool kBf16Out>
+__device__ __forceinline__ void store_chunk(void* C, int64_t at, const u32x4& v, int64_t left) {
+  if constexpr (kBf16Out) {
+    uint16_t* p = static_cast<uint16_t*>(C) + at;
+    if (left >= 8) {
+      *reinterpret_cast<u32x4_a2*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < left) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    uint32_t* p = static_cast<uint32_t*>(C) + at;
+    if (left >= 4) {
+      *reinterpret_cast<u32x4_a4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  }
+}
+
 // ---- few rows: operands straight from memory into registers ----
 //
 // A workgroup owns 16 kM rows of A by 16 kN rows of B; its kW waves split K in
@@ -209,8 +233,9 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* base, int bytes) {
                  __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
 
-// Each lane reads 16 bytes at voff + soff; the wave writes them, lane by lane,
-// to consecutive LDS bytes from address lds (M0) on.  Written as asm so that
+// Each lane reads 16 (or 4) bytes at voff + soff (voff is checked against the
+// record count); the wave writes them, lane by lane, to consecutive LDS bytes
+// from address lds (M0) on.  Written as asm so that
 // the compiler does not wait for them before every LDS read; the kernel waits
 // itself.  The leading s_nop is the wait state between the compiler's write of
 // M0 and its use.
@@ -222,6 +247,13 @@ __device__ __forceinline__ void lds_load16(i32x4 rs, uint32_t lds, uint32_t voff
                : "memory");
 }
 
+__device__ __forceinline__ void lds_load4(i32x4 rs, uint32_t lds, uint32_t voff) {
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(rs), "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+
 template <int kByte>
 __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb, const f32x16& c) {
   const i32x8 wa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
@@ -229,12 +261,20 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, wb, c, kFp4, kFp4, kByte, (int)sa, kByte, (int)sb);
 }
 
-template <int kF, bool kBf16Out>
+// kWords: rows of exponents start on 4 bytes (K is a multiple of 128).  They
+// then go into LDS too, 32 blocks of every row at a time, a quarter of the next
+// 32 with each stage: read from memory by every wave in every stage, 4 bytes a
+// row, they doubled the requests to L2 and cost a quarter of the time.
+template <int kF, bool kWords, bool kBf16Out>
 __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   constexpr int kT = 64 * kF;                        // rows of A, and of B, per tile
   constexpr int kOpBytes = kT * kRowBytes;           // one operand's stage
   constexpr int kLoads = kT / 8 / 4;                 // wave-wide loads per operand and stage: 8 rows each
-  __shared__ __attribute__((aligned(16))) char s_tile[2][2 * kOpBytes];
+  constexpr int kSpanBytes = 32;                     // exponents of a row that are loaded together: four stages
+  constexpr int kSpan = 2 * kT * kSpanBytes;         // of all rows, A's and then B's
+  constexpr int kPatch = 32 * kF * kF * 32 * 2;      // a wave's block of results as bf16
+  static_assert(4 * kPatch <= 4 * kOpBytes, "the results go through the stages' LDS");
+  __shared__ __attribute__((aligned(16))) char s_tile[4 * kOpBytes + (kWords ? 2 * kSpan : 0)];
 
   // Each XCD takes a contiguous range of tiles, in groups of kRasterRows tile
   // rows walked column by column, so that the tiles resident on one XCD share
@@ -268,7 +308,7 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
     voff[i] = (uint32_t)(r * row_bytes + 16 * c);
     voff_last[i] = (stages - 1) * kStageBlocks + c < a.blocks ? voff[i] : 0x80000000u;  // past K: zeros
   }
-  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(&s_tile[0][0]);
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(&s_tile[0]);
   // Load i of stage s, A's and B's; past the last stage nothing is read (a
   // record count of 0) and zeros land in a buffer that nobody reads.  The loop
   // below has no branches but its own, or the compiler would gather the
@@ -299,20 +339,40 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
   for (int j = 0; j < 4; ++j)
     if ((stages - 1) * kStageBlocks + 4 * half + j < a.blocks) keep_last |= 0xffu << (8 * j);
   uint32_t sa[kF], sb[kF], sa_next[kF], sb_next[kF];
+  // Piece p (one of 4 kF) of exponent span c: eight rows, eight lanes to a row.
+  auto issue_span = [&](int c, int p) {
+    const int r = 8 * (4 * p + wave);  // of A's and B's rows in turn
+    const bool of_b = r >= kT;
+    const int live = (4 * c - stages) >> 31;
+    const int bytes = (of_b ? rows_b : rows_a) * a.blocks;
+    lds_load4(rsrc_words(of_b ? eb : ea, bytes & live), lds0 + 4 * kOpBytes + (c & 1) * kSpan + r * kSpanBytes,
+              (uint32_t)((r - (of_b ? kT : 0) + (lane >> 3)) * a.blocks + kSpanBytes * c + 4 * (lane & 7)));
+  };
+  // The exponents of stage s: from LDS, or asked for in memory one stage ahead.
   auto exponents = [&](int s, uint32_t (&xa)[kF], uint32_t (&xb)[kF]) {
 #pragma unroll
     for (int i = 0; i < kF; ++i) {
-      xa[i] = *reinterpret_cast<const u32_a1*>(ea + min(ra0[i] + s * kStageBlocks, last_a));
-      xb[i] = *reinterpret_cast<const u32_a1*>(eb + min(rb0[i] + s * kStageBlocks, last_b));
+      if (kWords) {
+        const char* t = s_tile + 4 * kOpBytes + ((s >> 2) & 1) * kSpan + (s & 3) * kStageBlocks + 4 * half;
+        xa[i] = *reinterpret_cast<const uint32_t*>(t + (wm + 32 * i + lrow) * kSpanBytes);
+        xb[i] = *reinterpret_cast<const uint32_t*>(t + (kT + wn + 32 * i + lrow) * kSpanBytes);
+      } else {
+        xa[i] = *reinterpret_cast<const u32_a1*>(ea + min(ra0[i] + s * kStageBlocks, last_a));
+        xb[i] = *reinterpret_cast<const u32_a1*>(eb + min(rb0[i] + s * kStageBlocks, last_b));
+      }
     }
   };
   auto finish_exponents = [&](int s, uint32_t (&xa)[kF], uint32_t (&xb)[kF]) {
     const uint32_t keep = s == stages - 1 ? keep_last : ~0u;
 #pragma unroll
     for (int i = 0; i < kF; ++i) {
-      const uint32_t oa = ra0[i] + s * kStageBlocks, ob = rb0[i] + s * kStageBlocks;
-      xa[i] = ((xa[i] >> (8 * ((oa - min(oa, last_a)) & 3))) & keep) | (0x7f7f7f7fu & ~keep);
-      xb[i] = ((xb[i] >> (8 * ((ob - min(ob, last_b)) & 3))) & keep) | (0x7f7f7f7fu & ~keep);
+      if (!kWords) {
+        const uint32_t oa = ra0[i] + s * kStageBlocks, ob = rb0[i] + s * kStageBlocks;
+        xa[i] >>= 8 * ((oa - min(oa, last_a)) & 3);
+        xb[i] >>= 8 * ((ob - min(ob, last_b)) & 3);
+      }
+      xa[i] = (xa[i] & keep) | (0x7f7f7f7fu & ~keep);
+      xb[i] = (xb[i] & keep) | (0x7f7f7f7fu & ~keep);
     }
   };
 
@@ -322,7 +382,7 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
   const int base_b = kOpBytes + (wn + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(wn + lrow));
   u32x4 fa[2][kF], fb[2][kF];
   auto read = [&](int s, int j, int i) {
-    const char* t = s_tile[s & 1];
+    const char* t = s_tile + (s & 1) * 2 * kOpBytes;
     fa[j & 1][i] = *reinterpret_cast<const u32x4*>(t + (base_a ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
     fb[j & 1][i] = *reinterpret_cast<const u32x4*>(t + (base_b ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
   };
@@ -358,59 +418,102 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
     constexpr int kPerRow = kLoads / kF / 2;  // loads after each row of blocks of the two steps
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) issue(0, i);
-    exponents(0, sa, sb);
-    finish_exponents(0, sa, sb);
+    if (kWords) {
+#pragma unroll
+      for (int p = 0; p < 4 * kF; ++p) issue_span(0, p);
+    } else {
+      exponents(0, sa, sb);
+    }
     asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    if (!kWords) finish_exponents(0, sa, sb);
     __syncthreads();
+    if (kWords) {
+      exponents(0, sa, sb);
+      finish_exponents(0, sa, sb);
+    }
 #pragma unroll
     for (int i = 0; i < kLoads / 2; ++i) issue(1, i);
 #pragma unroll
     for (int i = 0; i < kF; ++i) read(0, 0, i);
 #pragma unroll 1
     for (int s = 0; s < stages; ++s) {
-      exponents(s + 1, sa_next, sb_next);
+      if (!kWords) exponents(s + 1, sa_next, sb_next);
       __builtin_amdgcn_sched_barrier(0);
       step(integral_constant<int, 0>{}, [&](int i) {
         read(s, 1, i);
 #pragma unroll
         for (int l = 0; l < kPerRow; ++l) issue(s + 1, kLoads / 2 + kPerRow * i + l);
       });
-      step(integral_constant<int, 1>{}, [&](int i) { read(s, 2, i); });
+      step(integral_constant<int, 1>{}, [&](int i) {
+        read(s, 2, i);
+        if (kWords) issue_span((s >> 2) + 1, kF * (s & 3) + i);
+      });
       step(integral_constant<int, 2>{}, [&](int i) { read(s, 3, i); });
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
-      // the exponents are used here, so that the compiler's own wait for them
-      // comes before the next loads and not after
-      finish_exponents(s + 1, sa_next, sb_next);
+      if (!kWords) {
+        // the exponents are used here, so that the compiler's own wait for
+        // them comes before the next loads and not after
+        finish_exponents(s + 1, sa_next, sb_next);
 #pragma unroll
-      for (int i = 0; i < kF; ++i) asm volatile("" : "+v"(sa_next[i]), "+v"(sb_next[i]));
+        for (int i = 0; i < kF; ++i) asm volatile("" : "+v"(sa_next[i]), "+v"(sb_next[i]));
+      }
       __syncthreads();
+      if (kWords) exponents(s + 1, sa_next, sb_next);
       __builtin_amdgcn_sched_barrier(0);
       step(integral_constant<int, 3>{}, [&](int i) {
         read(s + 1, 0, i);
 #pragma unroll
         for (int l = 0; l < kPerRow; ++l) issue(s + 2, kPerRow * i + l);
       });
+      if (kWords) finish_exponents(s + 1, sa_next, sb_next);
 #pragma unroll
       for (int i = 0; i < kF; ++i) sa[i] = sa_next[i], sb[i] = sb_next[i];
     }
-    // the loads past the last stage write LDS: they end before the workgroup does
+    // the loads past the last stage write LDS: they end before it is used again
     asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   }
+  __syncthreads();
 
   // The B rows come first in the instruction, so that a lane holds four
   // consecutive columns: D[row 8 q + 4 half + e][column lrow], q = r / 4, e = r % 4.
+  // Stored from there, a wave's store touches 32 rows with 16 bytes each (10 us
+  // for a tile of 256 x 256).  Through LDS a row of the wave's block leaves in
+  // one piece: rows of 64 kF bytes, 16-byte chunk c of row r at c ^ r (mod the
+  // chunks of a row), half of the columns at a time for fp32.
+  constexpr int kParts = kBf16Out ? 1 : 2;             // runs of columns that take turns in LDS
+  constexpr int kPatchRow = 64 * kF;                   // bytes
+  constexpr int kChunks = kPatchRow / 16;
+  constexpr int kRowsPerStore = 64 / kChunks;
+  constexpr int kPer = kBf16Out ? 8 : 4;               // columns per chunk
+  char* patch = s_tile + wave * kPatch;
 #pragma unroll
-  for (int i = 0; i < kF; ++i) {
-    const int64_t m = m0 + wm + 32 * i + lrow;
-    if (m >= a.M) continue;
+  for (int part = 0; part < kParts; ++part) {
 #pragma unroll
-    for (int k = 0; k < kF; ++k)
+    for (int i = 0; i < kF; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + wn + 32 * k + 8 * q + 4 * half;
-        const f32x4 v = {acc[i][k][4 * q], acc[i][k][4 * q + 1], acc[i][k][4 * q + 2], acc[i][k][4 * q + 3]};
-        if (n < a.N) store4<kBf16Out>(a.C, m * a.N + n, v, a.N - n);
-      }
+      for (int k = 0; k < kF / kParts; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& d = acc[i][part * (kF / kParts) + k];
+          const int row = 32 * i + lrow, col = 32 * k + 8 * q + 4 * half;
+          char* to = patch + row * kPatchRow;
+          if (kBf16Out)
+            *reinterpret_cast<u32x2*>(to + 16 * (((col >> 3) ^ row) & (kChunks - 1)) + 8 * half) =
+                (u32x2){pack_bf16(d[4 * q], d[4 * q + 1]), pack_bf16(d[4 * q + 2], d[4 * q + 3])};
+          else
+            *reinterpret_cast<f32x4*>(to + 16 * (((col >> 2) ^ row) & (kChunks - 1))) =
+                (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+        }
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the wave's own writes: no other wave touches its patch
+    const int64_t n = n0 + wn + part * 16 * kF + kPer * (lane % kChunks);
+#pragma unroll
+    for (int r0 = 0; r0 < 32 * kF; r0 += kRowsPerStore) {
+      const int row = r0 + lane / kChunks;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(patch + row * kPatchRow + 16 * (((lane % kChunks) ^ row) & (kChunks - 1)));
+      const int64_t m = m0 + wm + row;
+      if (m < a.M && n < a.N) store_chunk<kBf16Out>(a.C, m * a.N + n, v, a.N - n);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
   }
 }
 
@@ -420,10 +523,11 @@ void launch_tile(GemmArgs a, bool bf16, hipStream_t stream) {
   a.tiles_n = (int)((a.N + 64 * kF - 1) / (64 * kF));
   const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
   const dim3 grid(8 * per_xcd), block(kTileThreads);
-  if (bf16)
-    hipLaunchKernelGGL((mx_gemm_tile_kernel<kF, true>), grid, block, 0, stream, a, per_xcd);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, per_xcd); };
+  if (a.blocks % 4 == 0)
+    bf16 ? go(mx_gemm_tile_kernel<kF, true, true>) : go(mx_gemm_tile_kernel<kF, true, false>);
   else
-    hipLaunchKernelGGL((mx_gemm_tile_kernel<kF, false>), grid, block, 0, stream, a, per_xcd);
+    bf16 ? go(mx_gemm_tile_kernel<kF, false, true>) : go(mx_gemm_tile_kernel<kF, false, false>);
 }
 
 template <int kM, int kN, int kW>
