@@ -265,6 +265,10 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x
 // then go into LDS too, 32 blocks of every row at a time, a quarter of the next
 // 32 with each stage: read from memory by every wave in every stage, 4 bytes a
 // row, they doubled the requests to L2 and cost a quarter of the time.
+//
+// Workgroups are persistent (one per CU for 256 x 256, two for 128 x 128): the
+// next tile's first stage is asked for before the present one's results are
+// stored, and the stores drain behind its first stage.
 template <int kF, bool kWords, bool kBf16Out>
 __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   constexpr int kT = 64 * kF;                        // rows of A, and of B, per tile
@@ -272,20 +276,7 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
   constexpr int kLoads = kT / 8 / 4;                 // wave-wide loads per operand and stage: 8 rows each
   constexpr int kSpanBytes = 32;                     // exponents of a row that are loaded together: four stages
   constexpr int kSpan = 2 * kT * kSpanBytes;         // of all rows, A's and then B's
-  constexpr int kPatch = 32 * kF * kF * 32 * 2;      // a wave's block of results as bf16
-  static_assert(4 * kPatch <= 4 * kOpBytes, "the results go through the stages' LDS");
   __shared__ __attribute__((aligned(16))) char s_tile[4 * kOpBytes + (kWords ? 2 * kSpan : 0)];
-
-  // Each XCD takes a contiguous range of tiles, in groups of kRasterRows tile
-  // rows walked column by column, so that the tiles resident on one XCD share
-  // their operands in its L2.
-  const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if (tile >= a.tiles_m * a.tiles_n) return;
-  const int per_group = kRasterRows * a.tiles_n;
-  const int first_m = (tile / per_group) * kRasterRows;
-  const int in_group = tile % per_group;
-  const int gsz = min(a.tiles_m - first_m, kRasterRows);
-  const int64_t m0 = (int64_t)(first_m + in_group % gsz) * kT, n0 = (int64_t)(in_group / gsz) * kT;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -294,10 +285,33 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
   const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;
   const int64_t row_bytes = (int64_t)a.blocks * 16;
 
-  // Rows past M or N read as zeros: the record count ends at the last row.
-  const int rows_a = a.M - m0 < kT ? (int)(a.M - m0) : kT, rows_b = a.N - n0 < kT ? (int)(a.N - n0) : kT;
-  const uint8_t *codes_a = a.A + m0 * row_bytes, *codes_b = a.B + n0 * row_bytes;
-  const int bytes_a = (int)(rows_a * row_bytes), bytes_b = (int)(rows_b * row_bytes);
+  // Each XCD takes a contiguous range of tiles, in groups of kRasterRows tile
+  // rows walked column by column, so that the tiles resident on one XCD share
+  // their operands in its L2.  Rows past M or N read as zeros: the record
+  // count ends at the last row.
+  struct Tile {
+    int64_t m0, n0;
+    const uint8_t *a, *b, *ea, *eb;
+    int rows_a, rows_b;
+  };
+  auto tile_at = [&](int t) {
+    const int per_group = kRasterRows * a.tiles_n;
+    const int first_m = (t / per_group) * kRasterRows;
+    const int in_group = t % per_group;
+    const int gsz = min(a.tiles_m - first_m, kRasterRows);
+    Tile o;
+    o.m0 = (int64_t)(first_m + in_group % gsz) * kT, o.n0 = (int64_t)(in_group / gsz) * kT;
+    o.rows_a = a.M - o.m0 < kT ? (int)(a.M - o.m0) : kT, o.rows_b = a.N - o.n0 < kT ? (int)(a.N - o.n0) : kT;
+    o.a = a.A + o.m0 * row_bytes, o.b = a.B + o.n0 * row_bytes;
+    o.ea = a.sA + o.m0 * a.blocks, o.eb = a.sB + o.n0 * a.blocks;
+    return o;
+  };
+  const int slots = gridDim.x >> 3, first_tile = (blockIdx.x & 7) * per_xcd;
+  const int end_tile = min(first_tile + per_xcd, a.tiles_m * a.tiles_n);
+  int at_tile = first_tile + (blockIdx.x >> 3);
+  if (at_tile >= end_tile) return;
+  Tile tile = tile_at(at_tile);
+
   // Load i of this wave covers rows 8 (kLoads w + i) .. + 7 of an operand: lane
   // L writes row L / 8, physical chunk L % 8, and so reads chunk (L % 8) ^ swz.
   uint32_t voff[kLoads], voff_last[kLoads];
@@ -317,23 +331,14 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
     const uint32_t at = lds0 + (s & 1) * 2 * kOpBytes + 8 * (kLoads * wave + i) * kRowBytes;
     const uint32_t v = s == stages - 1 ? voff_last[i] : voff[i];
     const int live = (s - stages) >> 31;  // all ones before the end
-    lds_load16(rsrc_words(codes_a, bytes_a & live), at, v, (uint32_t)(s * kRowBytes));
-    lds_load16(rsrc_words(codes_b, bytes_b & live), at + kOpBytes, v, (uint32_t)(s * kRowBytes));
+    lds_load16(rsrc_words(tile.a, (int)(tile.rows_a * row_bytes) & live), at, v, (uint32_t)(s * kRowBytes));
+    lds_load16(rsrc_words(tile.b, (int)(tile.rows_b * row_bytes) & live), at + kOpBytes, v, (uint32_t)(s * kRowBytes));
   };
 
   // Exponents: lane (row, half) multiplies blocks 4 half .. 4 half + 3 of a
   // stage, four bytes of its row.  In the stage in which K ends the word may
-  // reach into the next row, or past the last row's end (there it is read
-  // earlier and shifted): what is not the row's is replaced by 127, and the
-  // codes there are zeros.
-  const uint8_t *ea = a.sA + m0 * a.blocks, *eb = a.sB + n0 * a.blocks;
-  const uint32_t last_a = (uint32_t)(rows_a * a.blocks) - 4, last_b = (uint32_t)(rows_b * a.blocks) - 4;
-  uint32_t ra0[kF], rb0[kF];
-#pragma unroll
-  for (int i = 0; i < kF; ++i) {
-    ra0[i] = (uint32_t)(min(wm + 32 * i + lrow, rows_a - 1) * a.blocks + 4 * half);
-    rb0[i] = (uint32_t)(min(wn + 32 * i + lrow, rows_b - 1) * a.blocks + 4 * half);
-  }
+  // reach past the row: what is not the row's is replaced by 127, and the codes
+  // there are zeros.
   uint32_t keep_last = 0;  // which of the last stage's bytes are the row's
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -344,11 +349,14 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
     const int r = 8 * (4 * p + wave);  // of A's and B's rows in turn
     const bool of_b = r >= kT;
     const int live = (4 * c - stages) >> 31;
-    const int bytes = (of_b ? rows_b : rows_a) * a.blocks;
-    lds_load4(rsrc_words(of_b ? eb : ea, bytes & live), lds0 + 4 * kOpBytes + (c & 1) * kSpan + r * kSpanBytes,
+    const int bytes = (of_b ? tile.rows_b : tile.rows_a) * a.blocks;
+    lds_load4(rsrc_words(of_b ? tile.eb : tile.ea, bytes & live),
+              lds0 + 4 * kOpBytes + (c & 1) * kSpan + r * kSpanBytes,
               (uint32_t)((r - (of_b ? kT : 0) + (lane >> 3)) * a.blocks + kSpanBytes * c + 4 * (lane & 7)));
   };
-  // The exponents of stage s: from LDS, or asked for in memory one stage ahead.
+  // The exponents of stage s: from LDS, or (rows that start anywhere) asked for
+  // in memory one stage ahead; a word that would pass the last row's end is
+  // read earlier and shifted (both operands have at least four exponents).
   auto exponents = [&](int s, uint32_t (&xa)[kF], uint32_t (&xb)[kF]) {
 #pragma unroll
     for (int i = 0; i < kF; ++i) {
@@ -357,8 +365,10 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
         xa[i] = *reinterpret_cast<const uint32_t*>(t + (wm + 32 * i + lrow) * kSpanBytes);
         xb[i] = *reinterpret_cast<const uint32_t*>(t + (kT + wn + 32 * i + lrow) * kSpanBytes);
       } else {
-        xa[i] = *reinterpret_cast<const u32_a1*>(ea + min(ra0[i] + s * kStageBlocks, last_a));
-        xb[i] = *reinterpret_cast<const u32_a1*>(eb + min(rb0[i] + s * kStageBlocks, last_b));
+        const int oa = min(wm + 32 * i + lrow, tile.rows_a - 1) * a.blocks + 4 * half + s * kStageBlocks;
+        const int ob = min(wn + 32 * i + lrow, tile.rows_b - 1) * a.blocks + 4 * half + s * kStageBlocks;
+        xa[i] = *reinterpret_cast<const u32_a1*>(tile.ea + min(oa, tile.rows_a * a.blocks - 4));
+        xb[i] = *reinterpret_cast<const u32_a1*>(tile.eb + min(ob, tile.rows_b * a.blocks - 4));
       }
     }
   };
@@ -367,9 +377,10 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
 #pragma unroll
     for (int i = 0; i < kF; ++i) {
       if (!kWords) {
-        const uint32_t oa = ra0[i] + s * kStageBlocks, ob = rb0[i] + s * kStageBlocks;
-        xa[i] >>= 8 * ((oa - min(oa, last_a)) & 3);
-        xb[i] >>= 8 * ((ob - min(ob, last_b)) & 3);
+        const int oa = min(wm + 32 * i + lrow, tile.rows_a - 1) * a.blocks + 4 * half + s * kStageBlocks;
+        const int ob = min(wn + 32 * i + lrow, tile.rows_b - 1) * a.blocks + 4 * half + s * kStageBlocks;
+        xa[i] >>= 8 * (max(oa - (tile.rows_a * a.blocks - 4), 0) & 3);
+        xb[i] >>= 8 * (max(ob - (tile.rows_b * a.blocks - 4), 0) & 3);
       }
       xa[i] = (xa[i] & keep) | (0x7f7f7f7fu & ~keep);
       xb[i] = (xb[i] & keep) | (0x7f7f7f7fu & ~keep);
@@ -388,12 +399,6 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
   };
 
   f32x16 acc[kF][kF];
-#pragma unroll
-  for (int i = 0; i < kF; ++i)
-#pragma unroll
-    for (int j = 0; j < kF; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   // Step j of a stage: row by row of its blocks, kF multiplications and then
   // the reads of the next step's operands (and loads of a later stage), in the
@@ -410,119 +415,150 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
   };
   using std::integral_constant;
 
-  // Before the last step of a stage every wave has read all of it: there the
-  // next stage's loads are waited for, and after the barrier the loads of the
-  // stage after it go into the buffer that has just been read, spread over
-  // that last step and the first one of the next stage.
-  if (stages > 0) {
-    constexpr int kPerRow = kLoads / kF / 2;  // loads after each row of blocks of the two steps
+  auto start = [&] {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) issue(0, i);
     if (kWords) {
 #pragma unroll
       for (int p = 0; p < 4 * kF; ++p) issue_span(0, p);
-    } else {
-      exponents(0, sa, sb);
     }
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
-    if (!kWords) finish_exponents(0, sa, sb);
-    __syncthreads();
-    if (kWords) {
-      exponents(0, sa, sb);
-      finish_exponents(0, sa, sb);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads / 2; ++i) issue(1, i);
-#pragma unroll
-    for (int i = 0; i < kF; ++i) read(0, 0, i);
-#pragma unroll 1
-    for (int s = 0; s < stages; ++s) {
-      if (!kWords) exponents(s + 1, sa_next, sb_next);
-      __builtin_amdgcn_sched_barrier(0);
-      step(integral_constant<int, 0>{}, [&](int i) {
-        read(s, 1, i);
-#pragma unroll
-        for (int l = 0; l < kPerRow; ++l) issue(s + 1, kLoads / 2 + kPerRow * i + l);
-      });
-      step(integral_constant<int, 1>{}, [&](int i) {
-        read(s, 2, i);
-        if (kWords) issue_span((s >> 2) + 1, kF * (s & 3) + i);
-      });
-      step(integral_constant<int, 2>{}, [&](int i) { read(s, 3, i); });
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
-      if (!kWords) {
-        // the exponents are used here, so that the compiler's own wait for
-        // them comes before the next loads and not after
-        finish_exponents(s + 1, sa_next, sb_next);
-#pragma unroll
-        for (int i = 0; i < kF; ++i) asm volatile("" : "+v"(sa_next[i]), "+v"(sb_next[i]));
-      }
-      __syncthreads();
-      if (kWords) exponents(s + 1, sa_next, sb_next);
-      __builtin_amdgcn_sched_barrier(0);
-      step(integral_constant<int, 3>{}, [&](int i) {
-        read(s + 1, 0, i);
-#pragma unroll
-        for (int l = 0; l < kPerRow; ++l) issue(s + 2, kPerRow * i + l);
-      });
-      if (kWords) finish_exponents(s + 1, sa_next, sb_next);
-#pragma unroll
-      for (int i = 0; i < kF; ++i) sa[i] = sa_next[i], sb[i] = sb_next[i];
-    }
-    // the loads past the last stage write LDS: they end before it is used again
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
-  }
-  __syncthreads();
+  };
 
-  // The B rows come first in the instruction, so that a lane holds four
-  // consecutive columns: D[row 8 q + 4 half + e][column lrow], q = r / 4, e = r % 4.
-  // Stored from there, a wave's store touches 32 rows with 16 bytes each (10 us
-  // for a tile of 256 x 256).  Through LDS a row of the wave's block leaves in
-  // one piece: rows of 64 kF bytes, 16-byte chunk c of row r at c ^ r (mod the
-  // chunks of a row), half of the columns at a time for fp32.
-  constexpr int kParts = kBf16Out ? 1 : 2;             // runs of columns that take turns in LDS
-  constexpr int kPatchRow = 64 * kF;                   // bytes
-  constexpr int kChunks = kPatchRow / 16;
-  constexpr int kRowsPerStore = 64 / kChunks;
-  constexpr int kPer = kBf16Out ? 8 : 4;               // columns per chunk
-  char* patch = s_tile + wave * kPatch;
-#pragma unroll
-  for (int part = 0; part < kParts; ++part) {
+  // The results of a wave leave through a patch of LDS (the second stage's),
+  // 128 bytes of each of its rows at a time: 16-byte chunk c of row r at c ^ r
+  // (mod 8), the halves of a chunk swapped for rows with bit 4.
+  constexpr int kPer = kBf16Out ? 8 : 4;             // columns per chunk
+  constexpr int kParts = 32 * kF / (8 * kPer);
+  constexpr int kStores = kParts * 4 * kF;           // a wave's stores of a whole tile
+  char* patch = s_tile + 2 * kOpBytes + wave * 32 * kF * 128;
+
+  start();
+  bool whole_before = false;  // the stores of a whole tile are on their way behind this one's loads
+  constexpr int kPerRow = kLoads / kF / 2;  // loads after each row of blocks of the two steps
+  for (;;) {
 #pragma unroll
     for (int i = 0; i < kF; ++i)
 #pragma unroll
-      for (int k = 0; k < kF / kParts; ++k)
+      for (int j = 0; j < kF; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16& d = acc[i][part * (kF / kParts) + k];
-          const int row = 32 * i + lrow, col = 32 * k + 8 * q + 4 * half;
-          char* to = patch + row * kPatchRow;
-          if (kBf16Out)
-            *reinterpret_cast<u32x2*>(to + 16 * (((col >> 3) ^ row) & (kChunks - 1)) + 8 * half) =
-                (u32x2){pack_bf16(d[4 * q], d[4 * q + 1]), pack_bf16(d[4 * q + 2], d[4 * q + 3])};
-          else
-            *reinterpret_cast<f32x4*>(to + 16 * (((col >> 2) ^ row) & (kChunks - 1))) =
-                (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    if (!kWords && stages > 0) exponents(0, sa, sb);
+    // memory operations of a wave end in the order of their issue: the loads are
+    // done when only the stores are left
+    if (whole_before)
+      asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kStores < 63 ? kStores : 63) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    if (!kWords && stages > 0) finish_exponents(0, sa, sb);
+    __syncthreads();
+    // Before the last step of a stage every wave has read all of it: there the
+    // next stage's loads are waited for, and after the barrier the loads of the
+    // stage after it go into the buffer that has just been read, spread over
+    // that last step and the first one of the next stage.
+    if (stages > 0) {
+      if (kWords) {
+        exponents(0, sa, sb);
+        finish_exponents(0, sa, sb);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads / 2; ++i) issue(1, i);
+#pragma unroll
+      for (int i = 0; i < kF; ++i) read(0, 0, i);
+#pragma unroll 1
+      for (int s = 0; s < stages; ++s) {
+        if (!kWords) exponents(s + 1, sa_next, sb_next);
+        __builtin_amdgcn_sched_barrier(0);
+        step(integral_constant<int, 0>{}, [&](int i) {
+          read(s, 1, i);
+#pragma unroll
+          for (int l = 0; l < kPerRow; ++l) issue(s + 1, kLoads / 2 + kPerRow * i + l);
+        });
+        step(integral_constant<int, 1>{}, [&](int i) {
+          read(s, 2, i);
+          if (kWords) issue_span((s >> 2) + 1, kF * (s & 3) + i);
+        });
+        step(integral_constant<int, 2>{}, [&](int i) { read(s, 3, i); });
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+        if (!kWords) {
+          // the exponents are used here, so that the compiler's own wait for
+          // them comes before the next loads and not after
+          finish_exponents(s + 1, sa_next, sb_next);
+#pragma unroll
+          for (int i = 0; i < kF; ++i) asm volatile("" : "+v"(sa_next[i]), "+v"(sb_next[i]));
         }
-    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the wave's own writes: no other wave touches its patch
-    const int64_t n = n0 + wn + part * 16 * kF + kPer * (lane % kChunks);
+        __syncthreads();
+        if (kWords) exponents(s + 1, sa_next, sb_next);
+        __builtin_amdgcn_sched_barrier(0);
+        step(integral_constant<int, 3>{}, [&](int i) {
+          read(s + 1, 0, i);
 #pragma unroll
-    for (int r0 = 0; r0 < 32 * kF; r0 += kRowsPerStore) {
-      const int row = r0 + lane / kChunks;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(patch + row * kPatchRow + 16 * (((lane % kChunks) ^ row) & (kChunks - 1)));
-      const int64_t m = m0 + wm + row;
-      if (m < a.M && n < a.N) store_chunk<kBf16Out>(a.C, m * a.N + n, v, a.N - n);
+          for (int l = 0; l < kPerRow; ++l) issue(s + 2, kPerRow * i + l);
+        });
+        if (kWords) finish_exponents(s + 1, sa_next, sb_next);
+#pragma unroll
+        for (int i = 0; i < kF; ++i) sa[i] = sa_next[i], sb[i] = sb_next[i];
+      }
+      // the loads past the last stage write LDS: they end before it is used again
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    __syncthreads();
+    const int64_t m0 = tile.m0 + wm, n0 = tile.n0 + wn;
+    const bool whole = tile.rows_a == kT && tile.rows_b == kT;
+    at_tile += slots;
+    const bool more = at_tile < end_tile;
+    if (more) {
+      tile = tile_at(at_tile);
+      start();
+    }
+
+    // The B rows come first in the instruction, so that a lane holds four
+    // consecutive columns: D[row 8 q + 4 half + e][column lrow], q = r / 4, e =
+    // r % 4.  Stored from there, a store would touch 32 rows with 16 bytes each
+    // (10 us for a tile of 256 x 256); out of the patch it is 8 rows of 128.
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+#pragma unroll
+      for (int i = 0; i < kF; ++i)
+#pragma unroll
+        for (int k = 0; k < kPer / 4; ++k)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& d = acc[i][part * (kPer / 4) + k];
+            const int row = 32 * i + lrow;
+            char* to = patch + row * 128;
+            if constexpr (kBf16Out)
+              *reinterpret_cast<u32x2*>(to + 16 * (((4 * k + q) ^ row) & 7) + 8 * (half ^ ((row >> 4) & 1))) =
+                  (u32x2){pack_bf16(d[4 * q], d[4 * q + 1]), pack_bf16(d[4 * q + 2], d[4 * q + 3])};
+            else
+              *reinterpret_cast<f32x4*>(to + 16 * (((2 * q + half) ^ row) & 7)) =
+                  (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+          }
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the wave's own writes: no other wave touches its patch
+      const int64_t n = n0 + 8 * kPer * part + kPer * (lane & 7);
+#pragma unroll
+      for (int r0 = 0; r0 < 32 * kF; r0 += 8) {
+        const int row = r0 + (lane >> 3);
+        u32x4 v = *reinterpret_cast<const u32x4*>(patch + row * 128 + 16 * ((lane ^ row) & 7));
+        if (kBf16Out && (r0 & 16)) v = (u32x4){v.z, v.w, v.x, v.y};
+        const int64_t m = m0 + row;
+        if (whole)
+          store_chunk<kBf16Out>(a.C, m * a.N + n, v, kPer);
+        else if (m < a.M && n < a.N)
+          store_chunk<kBf16Out>(a.C, m * a.N + n, v, a.N - n);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    }
+    if (!more) break;
+    whole_before = whole;
   }
 }
 
 template <int kF>
-void launch_tile(GemmArgs a, bool bf16, hipStream_t stream) {
+void launch_tile(GemmArgs a, bool bf16, int cus, hipStream_t stream) {
   a.tiles_m = (int)((a.M + 64 * kF - 1) / (64 * kF));
   a.tiles_n = (int)((a.N + 64 * kF - 1) / (64 * kF));
   const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
-  const dim3 grid(8 * per_xcd), block(kTileThreads);
+  const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * (kF == 4 ? 1 : 2))), block(kTileThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, per_xcd); };
   if (a.blocks % 4 == 0)
     bf16 ? go(mx_gemm_tile_kernel<kF, true, true>) : go(mx_gemm_tile_kernel<kF, true, false>);
@@ -563,14 +599,20 @@ __attribute__((visibility("default"))) int mxfp4_gemm(const void* A, const void*
     return SILUQUANT_ERR_OVERLAP;
   const GemmArgs a = {static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(sA), static_cast<const uint8_t*>(B),
                       static_cast<const uint8_t*>(sB), C, M, N, (int)(K / 32), 0, 0};
+  int dev = 0, cus = 0;  // asked on every call (the runtime answers from its cached properties): no state is kept
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    return SILUQUANT_ERR_DEVICE;
   if (M <= 16)
     launch_stream<1, 1, 8>(a, bf16, stream);
   else if (M <= 64)
     launch_stream<2, 2, 8>(a, bf16, stream);
+  else if (N * (K / 32) < 4)
+    launch_stream<2, 2, 8>(a, bf16, stream);
   else if (((M + 255) / 256) * ((N + 255) / 256) >= 128)
-    launch_tile<4>(a, bf16, stream);
+    launch_tile<4>(a, bf16, cus, stream);
   else
-    launch_tile<2>(a, bf16, stream);
+    launch_tile<2>(a, bf16, cus, stream);
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }
 
