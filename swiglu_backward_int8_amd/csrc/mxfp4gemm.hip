@@ -207,8 +207,8 @@ __global__ __launch_bounds__(64 * kW) void mx_gemm_stream_kernel(const GemmArgs 
 
 // ---- many rows: tiles through LDS ----
 //
-// 256 threads, four waves in a 2 x 2 grid, a tile of 64 kF x 64 kF results; a
-// wave owns kF x kF blocks of 32 x 32.  A stage is 256 values (8 blocks, 128
+// A workgroup owns a tile of kTileA x kTileB results, its waves (2 x kWavesB)
+// kFA x kFB blocks of 32 x 32 each.  A stage is 256 values (8 blocks, 128
 // bytes) of every row of the tile: the codes go from memory straight into LDS
 // (buffer loads with the lds flag), double buffered, the exponents into
 // registers.  Rows of 128 bytes lie in LDS as eight 16-byte chunks, chunk c of
@@ -219,7 +219,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kStageBlocks = 8;                 // per row and stage
 constexpr int kRowBytes = 16 * kStageBlocks;    // 128
-constexpr int kTileThreads = 256;
 constexpr int kRasterRows = 4;                  // tile rows that are walked column by column together
 
 __device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
@@ -233,25 +232,30 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* base, int bytes) {
                  __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
 
-// Each lane reads 16 (or 4) bytes at voff + soff (voff is checked against the
-// record count); the wave writes them, lane by lane, to consecutive LDS bytes
-// from address lds (M0) on.  Written as asm so that
-// the compiler does not wait for them before every LDS read; the kernel waits
-// itself.  The leading s_nop is the wait state between the compiler's write of
-// M0 and its use.
+// Each lane reads 16 bytes at voff + soff (voff is checked against the record
+// count, each 4 bytes for themselves); the wave writes them, lane by lane, to
+// consecutive LDS bytes from address lds (M0) on.  Written as asm so that the
+// compiler does not wait for them before every LDS read; the kernel waits
+// itself.  The leading s_nop gives the wait states that the compiler cannot,
+// since it does not look inside: one between the write of M0 and its use; and,
+// with kSlow, five between a vector instruction's write of a scalar register
+// (a scalar that was spilled to lanes comes back that way) and a load that
+// reads it.  In the main loop the scalars stay in their registers, which the
+// instruction checks of the tests hold it to, and 20 cycles a load would show.
+template <bool kSlow>
 __device__ __forceinline__ void lds_load16(i32x4 rs, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :
-               : "v"(voff), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(soff)),
-                 "{m0}"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory");
-}
-
-__device__ __forceinline__ void lds_load4(i32x4 rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(rs), "{m0}"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory");
+  if (kSlow)
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                   "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory");
+  else
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                   "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory");
 }
 
 template <int kByte>
@@ -269,18 +273,29 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x
 // Workgroups are persistent (one per CU for 256 x 256, two for 128 x 128): the
 // next tile's first stage is asked for before the present one's results are
 // stored, and the stores drain behind its first stage.
-template <int kF, bool kWords, bool kBf16Out>
-__global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
-  constexpr int kT = 64 * kF;                        // rows of A, and of B, per tile
-  constexpr int kOpBytes = kT * kRowBytes;           // one operand's stage
-  constexpr int kLoads = kT / 8 / 4;                 // wave-wide loads per operand and stage: 8 rows each
-  constexpr int kSpanBytes = 32;                     // exponents of a row that are loaded together: four stages
-  constexpr int kSpan = 2 * kT * kSpanBytes;         // of all rows, A's and then B's
-  __shared__ __attribute__((aligned(16))) char s_tile[4 * kOpBytes + (kWords ? 2 * kSpan : 0)];
+template <int kFA, int kFB, int kWavesB>
+struct TileShape {
+  static constexpr int kWaves = 2 * kWavesB, kThreads = 64 * kWaves;
+  static constexpr int kTileA = 64 * kFA, kTileB = 32 * kWavesB * kFB;  // rows of A and of B
+  static constexpr int kPerCu = kFA * kFB * kWavesB > 8 ? 1 : 2;        // workgroups that fit a CU's LDS
+};
+template <int kFA, int kFB, int kWavesB, bool kWords, bool kBf16Out>
+__global__ __launch_bounds__(128 * kWavesB, (kFA * kFB * kWavesB > 8 ? 1 : 2) * kWavesB / 2) void
+mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
+  using Shape = TileShape<kFA, kFB, kWavesB>;
+  constexpr int kWaves = Shape::kWaves, kTileA = Shape::kTileA, kTileB = Shape::kTileB;
+  constexpr int kStage = (kTileA + kTileB) * kRowBytes;     // A's rows, then B's
+  constexpr int kLoadsA = kTileA / 8 / kWaves, kLoadsB = kTileB / 8 / kWaves;  // wave-wide loads per stage: 8 rows each
+  constexpr int kLoads = kLoadsA + kLoadsB;
+  constexpr int kSpanBytes = 32;                            // exponents of a row that are loaded together: four stages
+  constexpr int kSpan = (kTileA + kTileB) * kSpanBytes;
+  constexpr int kSpanLoads = (kTileA + kTileB) / 32;        // 32 rows each
+  constexpr int kSpanPerWave = kSpanLoads / kWaves;         // of a span, one a stage
+  __shared__ __attribute__((aligned(16))) char s_tile[2 * kStage + (kWords ? 2 * kSpan : 0)];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = (wave >> 1) * 32 * kF, wn = (wave & 1) * 32 * kF;
+  const int wm = (wave / kWavesB) * 32 * kFA, wn = (wave % kWavesB) * 32 * kFB;
   const int lrow = lane & 31, half = lane >> 5;
   const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;
   const int64_t row_bytes = (int64_t)a.blocks * 16;
@@ -291,48 +306,57 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
   // count ends at the last row.
   struct Tile {
     int64_t m0, n0;
-    const uint8_t *a, *b, *ea, *eb;
+    i32x4 a, b, ea, eb;  // buffer resources of its rows' codes and exponents
     int rows_a, rows_b;
   };
-  auto tile_at = [&](int t) {
-    const int per_group = kRasterRows * a.tiles_n;
-    const int first_m = (t / per_group) * kRasterRows;
-    const int in_group = t % per_group;
+  auto tile_at = [&](int group, int in_group) {
+    const int first_m = group * kRasterRows;
     const int gsz = min(a.tiles_m - first_m, kRasterRows);
+    const int tn = gsz == 4 ? in_group >> 2 : gsz == 2 ? in_group >> 1 : gsz == 1 ? in_group : in_group / 3;
     Tile o;
-    o.m0 = (int64_t)(first_m + in_group % gsz) * kT, o.n0 = (int64_t)(in_group / gsz) * kT;
-    o.rows_a = a.M - o.m0 < kT ? (int)(a.M - o.m0) : kT, o.rows_b = a.N - o.n0 < kT ? (int)(a.N - o.n0) : kT;
-    o.a = a.A + o.m0 * row_bytes, o.b = a.B + o.n0 * row_bytes;
-    o.ea = a.sA + o.m0 * a.blocks, o.eb = a.sB + o.n0 * a.blocks;
+    o.m0 = (int64_t)(first_m + in_group - tn * gsz) * kTileA, o.n0 = (int64_t)tn * kTileB;
+    o.rows_a = a.M - o.m0 < kTileA ? (int)(a.M - o.m0) : kTileA;
+    o.rows_b = a.N - o.n0 < kTileB ? (int)(a.N - o.n0) : kTileB;
+    o.a = rsrc_words(a.A + o.m0 * row_bytes, (int)(o.rows_a * row_bytes));
+    o.b = rsrc_words(a.B + o.n0 * row_bytes, (int)(o.rows_b * row_bytes));
+    o.ea = rsrc_words(a.sA + o.m0 * a.blocks, o.rows_a * a.blocks);
+    o.eb = rsrc_words(a.sB + o.n0 * a.blocks, o.rows_b * a.blocks);
     return o;
   };
+  static_assert(kRasterRows == 4, "tile_at divides by 1 to 4");
   const int slots = gridDim.x >> 3, first_tile = (blockIdx.x & 7) * per_xcd;
   const int end_tile = min(first_tile + per_xcd, a.tiles_m * a.tiles_n);
   int at_tile = first_tile + (blockIdx.x >> 3);
   if (at_tile >= end_tile) return;
-  Tile tile = tile_at(at_tile);
+  const int per_group = kRasterRows * a.tiles_n;
+  int group = at_tile / per_group, in_group = at_tile - group * per_group;
+  Tile tile = tile_at(group, in_group);
 
   // Load i of this wave covers rows 8 (kLoads w + i) .. + 7 of an operand: lane
   // L writes row L / 8, physical chunk L % 8, and so reads chunk (L % 8) ^ swz.
-  uint32_t voff[kLoads], voff_last[kLoads];
+  constexpr int kMostLoads = kLoadsA > kLoadsB ? kLoadsA : kLoadsB;
+  static_assert(kLoadsA == kLoadsB, "A's and B's loads share their offsets");
+  uint32_t voff[kMostLoads], past_k = 0;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int r = 8 * (kLoads * wave + i) + (lane >> 3);
+  for (int i = 0; i < kMostLoads; ++i) {
+    const int r = 8 * (kMostLoads * wave + i) + (lane >> 3);
     const int c = (lane & 7) ^ swz(r);
     voff[i] = (uint32_t)(r * row_bytes + 16 * c);
-    voff_last[i] = (stages - 1) * kStageBlocks + c < a.blocks ? voff[i] : 0x80000000u;  // past K: zeros
+    past_k |= (uint32_t)((stages - 1) * kStageBlocks + c >= a.blocks) << i;  // in the last stage
   }
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(&s_tile[0]);
-  // Load i of stage s, A's and B's; past the last stage nothing is read (a
-  // record count of 0) and zeros land in a buffer that nobody reads.  The loop
-  // below has no branches but its own, or the compiler would gather the
-  // multiplications in one of its blocks.
-  auto issue = [&](int s, int i) {
-    const uint32_t at = lds0 + (s & 1) * 2 * kOpBytes + 8 * (kLoads * wave + i) * kRowBytes;
-    const uint32_t v = s == stages - 1 ? voff_last[i] : voff[i];
-    const int live = (s - stages) >> 31;  // all ones before the end
-    lds_load16(rsrc_words(tile.a, (int)(tile.rows_a * row_bytes) & live), at, v, (uint32_t)(s * kRowBytes));
-    lds_load16(rsrc_words(tile.b, (int)(tile.rows_b * row_bytes) & live), at + kOpBytes, v, (uint32_t)(s * kRowBytes));
+  // Load l of stage s (even: of A, odd: of B).  Bit i of `past` sends load i of
+  // either past the record count, where zeros are read: chunks past K, and all
+  // of a stage past the last one (its zeros land in a buffer that nobody reads;
+  // the loop below has no branches but its own, or the compiler would gather
+  // the multiplications in one of its blocks).
+  auto past = [&](int s) { return s < stages - 1 ? 0u : s == stages - 1 ? past_k : ~0u; };
+  auto issue = [&](auto slow, int s, uint32_t past, int l) {
+    const bool of_b = l & 1;
+    const int i = l >> 1;
+    const uint32_t at = lds0 + (s & 1) * kStage + (of_b ? kTileA * kRowBytes : 0) + 8 * (kMostLoads * wave + i) * kRowBytes;
+    lds_load16<decltype(slow)::value>(of_b ? tile.b : tile.a, at, voff[i] | ((past << (31 - i)) & 0x80000000u),
+                                      (uint32_t)(s * kRowBytes));
   };
 
   // Exponents: lane (row, half) multiplies blocks 4 half .. 4 half + 3 of a
@@ -343,112 +367,120 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if ((stages - 1) * kStageBlocks + 4 * half + j < a.blocks) keep_last |= 0xffu << (8 * j);
-  uint32_t sa[kF], sb[kF], sa_next[kF], sb_next[kF];
-  // Piece p (one of 4 kF) of exponent span c: eight rows, eight lanes to a row.
-  auto issue_span = [&](int c, int p) {
-    const int r = 8 * (4 * p + wave);  // of A's and B's rows in turn
-    const bool of_b = r >= kT;
-    const int live = (4 * c - stages) >> 31;
-    const int bytes = (of_b ? tile.rows_b : tile.rows_a) * a.blocks;
-    lds_load4(rsrc_words(of_b ? tile.eb : tile.ea, bytes & live),
-              lds0 + 4 * kOpBytes + (c & 1) * kSpan + r * kSpanBytes,
-              (uint32_t)((r - (of_b ? kT : 0) + (lane >> 3)) * a.blocks + kSpanBytes * c + 4 * (lane & 7)));
+  uint32_t sa[kFA], sb[kFB], sa_next[kFA], sb_next[kFB];
+  // Load p (one of kSpanPerWave) of this wave of exponent span c: 32 rows, two
+  // lanes to a row; spans past K are not read.
+  auto issue_span = [&](auto slow, int c, int p) {
+    const int r = 32 * (kWaves * p + wave);  // of A's and B's rows in turn
+    const bool of_b = r >= kTileA;
+    const uint32_t at = (uint32_t)((r - (of_b ? kTileA : 0) + (lane >> 1)) * a.blocks + kSpanBytes * c + 16 * (lane & 1));
+    const uint32_t none = 4 * c < stages ? 0u : 0x80000000u;
+    i32x4 rs;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) rs[w] = of_b ? tile.eb[w] : tile.ea[w];
+    lds_load16<decltype(slow)::value>(rs, lds0 + 2 * kStage + (c & 1) * kSpan + r * kSpanBytes, at | none, 0);
   };
   // The exponents of stage s: from LDS, or (rows that start anywhere) asked for
   // in memory one stage ahead; a word that would pass the last row's end is
   // read earlier and shifted (both operands have at least four exponents).
-  auto exponents = [&](int s, uint32_t (&xa)[kF], uint32_t (&xb)[kF]) {
-#pragma unroll
-    for (int i = 0; i < kF; ++i) {
-      if (kWords) {
-        const char* t = s_tile + 4 * kOpBytes + ((s >> 2) & 1) * kSpan + (s & 3) * kStageBlocks + 4 * half;
-        xa[i] = *reinterpret_cast<const uint32_t*>(t + (wm + 32 * i + lrow) * kSpanBytes);
-        xb[i] = *reinterpret_cast<const uint32_t*>(t + (kT + wn + 32 * i + lrow) * kSpanBytes);
-      } else {
-        const int oa = min(wm + 32 * i + lrow, tile.rows_a - 1) * a.blocks + 4 * half + s * kStageBlocks;
-        const int ob = min(wn + 32 * i + lrow, tile.rows_b - 1) * a.blocks + 4 * half + s * kStageBlocks;
-        xa[i] = *reinterpret_cast<const u32_a1*>(tile.ea + min(oa, tile.rows_a * a.blocks - 4));
-        xb[i] = *reinterpret_cast<const u32_a1*>(tile.eb + min(ob, tile.rows_b * a.blocks - 4));
-      }
-    }
+  auto word_at = [&](int s, int row, int rows) { return min(row, rows - 1) * a.blocks + 4 * half + s * kStageBlocks; };
+  auto word = [&](const uint8_t* e, int s, int row, int rows) {
+    return *reinterpret_cast<const u32_a1*>(e + min(word_at(s, row, rows), rows * a.blocks - 4));
   };
-  auto finish_exponents = [&](int s, uint32_t (&xa)[kF], uint32_t (&xb)[kF]) {
-    const uint32_t keep = s == stages - 1 ? keep_last : ~0u;
+  auto exponents_of = [&](const uint8_t* e, int64_t row) { return e + row * a.blocks; };
+  auto exponents = [&](int s, uint32_t (&xa)[kFA], uint32_t (&xb)[kFB]) {
+    const char* t = s_tile + 2 * kStage + ((s >> 2) & 1) * kSpan + (s & 3) * kStageBlocks + 4 * half;
 #pragma unroll
-    for (int i = 0; i < kF; ++i) {
-      if (!kWords) {
-        const int oa = min(wm + 32 * i + lrow, tile.rows_a - 1) * a.blocks + 4 * half + s * kStageBlocks;
-        const int ob = min(wn + 32 * i + lrow, tile.rows_b - 1) * a.blocks + 4 * half + s * kStageBlocks;
-        xa[i] >>= 8 * (max(oa - (tile.rows_a * a.blocks - 4), 0) & 3);
-        xb[i] >>= 8 * (max(ob - (tile.rows_b * a.blocks - 4), 0) & 3);
-      }
-      xa[i] = (xa[i] & keep) | (0x7f7f7f7fu & ~keep);
-      xb[i] = (xb[i] & keep) | (0x7f7f7f7fu & ~keep);
-    }
+    for (int i = 0; i < kFA; ++i)
+      xa[i] = kWords ? *reinterpret_cast<const uint32_t*>(t + (wm + 32 * i + lrow) * kSpanBytes)
+                     : word(exponents_of(a.sA, tile.m0), s, wm + 32 * i + lrow, tile.rows_a);
+#pragma unroll
+    for (int i = 0; i < kFB; ++i)
+      xb[i] = kWords ? *reinterpret_cast<const uint32_t*>(t + (kTileA + wn + 32 * i + lrow) * kSpanBytes)
+                     : word(exponents_of(a.sB, tile.n0), s, wn + 32 * i + lrow, tile.rows_b);
+  };
+  auto finish_exponents = [&](int s, uint32_t (&xa)[kFA], uint32_t (&xb)[kFB]) {
+    const uint32_t keep = s == stages - 1 ? keep_last : ~0u;
+    auto finish = [&](uint32_t& x, int row, int rows) {
+      if (!kWords) x >>= 8 * (max(word_at(s, row, rows) - (rows * a.blocks - 4), 0) & 3);
+      x = (x & keep) | (0x7f7f7f7fu & ~keep);
+    };
+#pragma unroll
+    for (int i = 0; i < kFA; ++i) finish(xa[i], wm + 32 * i + lrow, tile.rows_a);
+#pragma unroll
+    for (int i = 0; i < kFB; ++i) finish(xb[i], wn + 32 * i + lrow, tile.rows_b);
   };
 
   // Step j of a stage reads chunk 4 half + j of the wave's rows; block i's row
   // is 32 i further, which flips bit 2 of the chunk for odd i.
   const int base_a = (wm + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(wm + lrow));
-  const int base_b = kOpBytes + (wn + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(wn + lrow));
-  u32x4 fa[2][kF], fb[2][kF];
-  auto read = [&](int s, int j, int i) {
-    const char* t = s_tile + (s & 1) * 2 * kOpBytes;
-    fa[j & 1][i] = *reinterpret_cast<const u32x4*>(t + (base_a ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
-    fb[j & 1][i] = *reinterpret_cast<const u32x4*>(t + (base_b ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
+  const int base_b = kTileA * kRowBytes + (wn + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(wn + lrow));
+  u32x4 fa[2][kFA], fb[2][kFB];
+  // Read n of a step's operands, in the order in which they are needed.
+  constexpr int kReads = kFA + kFB;
+  auto read = [&](int s, int j, int n) {
+    const char* t = s_tile + (s & 1) * kStage;
+    const bool of_b = n != 1 && n <= kFB;
+    const int i = n == 0 || n == 1 ? 0 : of_b ? n - 1 : n - kFB;
+    u32x4& to = of_b ? fb[j & 1][i] : fa[j & 1][i];
+    to = *reinterpret_cast<const u32x4*>(t + ((of_b ? base_b : base_a) ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
   };
 
-  f32x16 acc[kF][kF];
+  f32x16 acc[kFA][kFB];
 
-  // Step j of a stage: row by row of its blocks, kF multiplications and then
-  // the reads of the next step's operands (and loads of a later stage), in the
-  // order written, so that the matrix cores never wait for an issue.
+  // Step j of a stage: its multiplications, and after each of them (32 cycles of
+  // the matrix core, 8 issues of the one wave that feeds it) a little of
+  // everything else, in the order written: reads of the next step's operands,
+  // loads of a later stage.
+  constexpr int kSlots = kFA * kFB;
   auto step = [&](auto which, auto&& between) {
     constexpr int j = decltype(which)::value;
 #pragma unroll
-    for (int i = 0; i < kF; ++i) {
-#pragma unroll
-      for (int k = 0; k < kF; ++k) acc[i][k] = mfma32<j>(fb[j & 1][k], sb[k], fa[j & 1][i], sa[i], acc[i][k]);
-      between(i);
+    for (int t = 0; t < kSlots; ++t) {
+      const int i = t / kFB, k = t % kFB;
+      acc[i][k] = mfma32<j>(fb[j & 1][k], sb[k], fa[j & 1][i], sa[i], acc[i][k]);
+      between(t);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  // Part n of `of`, spread over a step's slots from slot `from` on: f(n) at its slot.
+  auto spread = [&](int t, int of, int from, auto&& f) {
+#pragma unroll
+    for (int n = 0; n < of; ++n)
+      if (t == std::min(kSlots - 1, n * kSlots / of + from)) f(n);
+  };
   using std::integral_constant;
 
-  auto start = [&] {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) issue(0, i);
-    if (kWords) {
-#pragma unroll
-      for (int p = 0; p < 4 * kF; ++p) issue_span(0, p);
-    }
+  // A tile's first loads: its first stage and the first span of exponents.
+  constexpr int kFirst = kLoads + (kWords ? kSpanPerWave : 0);
+  auto start = [&](int l) {
+    if (l < kLoads)
+      issue(std::true_type{}, 0, past(0), l);
+    else
+      issue_span(std::true_type{}, 0, l - kLoads);
   };
 
-  // The results of a wave leave through a patch of LDS (the second stage's),
-  // 128 bytes of each of its rows at a time: 16-byte chunk c of row r at c ^ r
-  // (mod 8), the halves of a chunk swapped for rows with bit 4.
-  constexpr int kPer = kBf16Out ? 8 : 4;             // columns per chunk
-  constexpr int kParts = 32 * kF / (8 * kPer);
-  constexpr int kStores = kParts * 4 * kF;           // a wave's stores of a whole tile
-  char* patch = s_tile + 2 * kOpBytes + wave * 32 * kF * 128;
+  // The results of a wave leave through a patch of LDS (in the second stage's
+  // place), 32 rows of 128 bytes at a time, two blocks in turn: 16-byte chunk c
+  // of row r at c ^ swz(r), the halves of a chunk swapped for rows with bit 4.
+  constexpr int kPer = kBf16Out ? 8 : 4;               // columns per chunk
+  constexpr int kPartsB = 32 * kFB / (8 * kPer);       // runs of columns
+  constexpr int kPieces = kPartsB * kFA;               // of 32 rows x 128 bytes
+  static_assert(kStage / kWaves >= 2 * 32 * 128, "two pieces fit");
+  char* patch = s_tile + kStage + wave * (kStage / kWaves);
+  constexpr int kPerPiece = 8;  // the next tile's first loads that go out with each piece
+  static_assert(kFirst <= kPerPiece * kPieces, "all go out");
 
-  start();
-  bool whole_before = false;  // the stores of a whole tile are on their way behind this one's loads
-  constexpr int kPerRow = kLoads / kF / 2;  // loads after each row of blocks of the two steps
+#pragma unroll
+  for (int l = 0; l < kFirst; ++l) start(l);
+  static_assert(kLoads % 2 == 0 && kSpanLoads % kWaves == 0 && (kSpanPerWave == 4 || kSpanPerWave == 2), "every load has its place");
   for (;;) {
 #pragma unroll
-    for (int i = 0; i < kF; ++i)
+    for (int i = 0; i < kFA; ++i)
 #pragma unroll
-      for (int j = 0; j < kF; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      for (int k = 0; k < kFB; ++k) acc[i][k] = (f32x16){};
     if (!kWords && stages > 0) exponents(0, sa, sb);
-    // memory operations of a wave end in the order of their issue: the loads are
-    // done when only the stores are left
-    if (whole_before)
-      asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kStores < 63 ? kStores : 63) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     if (!kWords && stages > 0) finish_exponents(0, sa, sb);
     __syncthreads();
     // Before the last step of a stage every wave has read all of it: there the
@@ -461,109 +493,146 @@ __global__ __launch_bounds__(kTileThreads, kF == 4 ? 1 : 2) void mx_gemm_tile_ke
         finish_exponents(0, sa, sb);
       }
 #pragma unroll
-      for (int i = 0; i < kLoads / 2; ++i) issue(1, i);
+      for (int l = 0; l < kLoads / 2; ++l) issue(std::true_type{}, 1, past(1), l);
 #pragma unroll
-      for (int i = 0; i < kF; ++i) read(0, 0, i);
+      for (int n = 0; n < kReads; ++n) read(0, 0, n);
 #pragma unroll 1
       for (int s = 0; s < stages; ++s) {
         if (!kWords) exponents(s + 1, sa_next, sb_next);
         __builtin_amdgcn_sched_barrier(0);
-        step(integral_constant<int, 0>{}, [&](int i) {
-          read(s, 1, i);
-#pragma unroll
-          for (int l = 0; l < kPerRow; ++l) issue(s + 1, kLoads / 2 + kPerRow * i + l);
+        const uint32_t past1 = past(s + 1), past2 = past(s + 2);
+        step(integral_constant<int, 0>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(s, 1, n); });
+          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + 1, past1, kLoads / 2 + l); });
         });
-        step(integral_constant<int, 1>{}, [&](int i) {
-          read(s, 2, i);
-          if (kWords) issue_span((s >> 2) + 1, kF * (s & 3) + i);
+        step(integral_constant<int, 1>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(s, 2, n); });
+          if (kWords && t == kSlots / 2)  // with fewer than four a span, some are loaded twice
+            issue_span(std::false_type{}, (s >> 2) + 1, s & (kSpanPerWave - 1));
         });
-        step(integral_constant<int, 2>{}, [&](int i) { read(s, 3, i); });
+        step(integral_constant<int, 2>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(s, 3, n); }); });
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
         if (!kWords) {
           // the exponents are used here, so that the compiler's own wait for
           // them comes before the next loads and not after
           finish_exponents(s + 1, sa_next, sb_next);
 #pragma unroll
-          for (int i = 0; i < kF; ++i) asm volatile("" : "+v"(sa_next[i]), "+v"(sb_next[i]));
+          for (int i = 0; i < kFA; ++i) asm volatile("" : "+v"(sa_next[i]));
+#pragma unroll
+          for (int i = 0; i < kFB; ++i) asm volatile("" : "+v"(sb_next[i]));
         }
         __syncthreads();
         if (kWords) exponents(s + 1, sa_next, sb_next);
         __builtin_amdgcn_sched_barrier(0);
-        step(integral_constant<int, 3>{}, [&](int i) {
-          read(s + 1, 0, i);
-#pragma unroll
-          for (int l = 0; l < kPerRow; ++l) issue(s + 2, kPerRow * i + l);
+        step(integral_constant<int, 3>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(s + 1, 0, n); });
+          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + 2, past2, l); });
         });
         if (kWords) finish_exponents(s + 1, sa_next, sb_next);
 #pragma unroll
-        for (int i = 0; i < kF; ++i) sa[i] = sa_next[i], sb[i] = sb_next[i];
+        for (int i = 0; i < kFA; ++i) sa[i] = sa_next[i];
+#pragma unroll
+        for (int i = 0; i < kFB; ++i) sb[i] = sb_next[i];
       }
       // the loads past the last stage write LDS: they end before it is used again
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
     }
     __syncthreads();
     const int64_t m0 = tile.m0 + wm, n0 = tile.n0 + wn;
-    const bool whole = tile.rows_a == kT && tile.rows_b == kT;
+    const bool whole = tile.rows_a == kTileA && tile.rows_b == kTileB;
     at_tile += slots;
     const bool more = at_tile < end_tile;
     if (more) {
-      tile = tile_at(at_tile);
-      start();
+      in_group += slots;
+      while (in_group >= per_group) in_group -= per_group, ++group;
+      tile = tile_at(group, in_group);
+    } else {
+      tile.a.z = tile.b.z = tile.ea.z = tile.eb.z = 0;  // the first loads of no tile read nothing
     }
 
     // The B rows come first in the instruction, so that a lane holds four
     // consecutive columns: D[row 8 q + 4 half + e][column lrow], q = r / 4, e =
     // r % 4.  Stored from there, a store would touch 32 rows with 16 bytes each
     // (10 us for a tile of 256 x 256); out of the patch it is 8 rows of 128.
+    // A wave's LDS operations are carried out in their order and its patch is
+    // its own, so nothing waits but the stores for what they store.
+    auto put = [&](int piece) {
+      const int i = piece % kFA, part = piece / kFA;
+      char* to = patch + (piece & 1) * 32 * 128 + lrow * 128;
 #pragma unroll
-    for (int part = 0; part < kParts; ++part) {
+      for (int k = 0; k < kPer / 4; ++k)
 #pragma unroll
-      for (int i = 0; i < kF; ++i)
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& d = acc[i][part * (kPer / 4) + k];
+          if constexpr (kBf16Out)
+            *reinterpret_cast<u32x2*>(to + 16 * ((4 * k + q) ^ swz(lrow)) + 8 * (half ^ (lrow >> 4))) =
+                (u32x2){pack_bf16(d[4 * q], d[4 * q + 1]), pack_bf16(d[4 * q + 2], d[4 * q + 3])};
+          else
+            *reinterpret_cast<f32x4*>(to + 16 * ((2 * q + half) ^ swz(lrow))) =
+                (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+        }
+    };
+    const int r = lane >> 3;
+    u32x4 out[2][4];
+    auto get = [&](int piece) {
 #pragma unroll
-        for (int k = 0; k < kPer / 4; ++k)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x16& d = acc[i][part * (kPer / 4) + k];
-            const int row = 32 * i + lrow;
-            char* to = patch + row * 128;
-            if constexpr (kBf16Out)
-              *reinterpret_cast<u32x2*>(to + 16 * (((4 * k + q) ^ row) & 7) + 8 * (half ^ ((row >> 4) & 1))) =
-                  (u32x2){pack_bf16(d[4 * q], d[4 * q + 1]), pack_bf16(d[4 * q + 2], d[4 * q + 3])};
-            else
-              *reinterpret_cast<f32x4*>(to + 16 * (((2 * q + half) ^ row) & 7)) =
-                  (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
-          }
-      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the wave's own writes: no other wave touches its patch
-      const int64_t n = n0 + 8 * kPer * part + kPer * (lane & 7);
-#pragma unroll
-      for (int r0 = 0; r0 < 32 * kF; r0 += 8) {
-        const int row = r0 + (lane >> 3);
-        u32x4 v = *reinterpret_cast<const u32x4*>(patch + row * 128 + 16 * ((lane ^ row) & 7));
-        if (kBf16Out && (r0 & 16)) v = (u32x4){v.z, v.w, v.x, v.y};
-        const int64_t m = m0 + row;
-        if (whole)
-          store_chunk<kBf16Out>(a.C, m * a.N + n, v, kPer);
-        else if (m < a.M && n < a.N)
-          store_chunk<kBf16Out>(a.C, m * a.N + n, v, a.N - n);
+      for (int x = 0; x < 4; ++x) {
+        const int row = 8 * x + r;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(patch + (piece & 1) * 32 * 128 + row * 128 + 16 * ((lane & 7) ^ swz(row)));
+        out[piece & 1][x] = kBf16Out && x >= 2 ? (u32x4){v.z, v.w, v.x, v.y} : v;
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    };
+    char* const to0 = static_cast<char*>(a.C) + ((m0 + r) * a.N + n0 + kPer * (lane & 7)) * (16 / kPer);
+    auto loads = [&](int t) {
+#pragma unroll
+      for (int l = kPerPiece * t; l < kPerPiece * (t + 1); ++l)
+        if (l < kFirst) start(l);
+    };
+    if (whole) {
+#pragma unroll
+      for (int t = 0; t < kPieces + 2; ++t) {
+        loads(t);
+        if (t < kPieces) put(t);
+        if (t >= 2) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<u32x4_a2*>(to0 + (32 * ((t - 2) % kFA) + 8 * x) * a.N * (16 / kPer) + 128 * ((t - 2) / kFA)) =
+                out[t & 1][x];
+        }
+        if (t >= 1 && t <= kPieces) get(t - 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < kPieces; ++t) {
+        loads(t);
+        put(t);
+        get(t);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int64_t m = m0 + 32 * (t % kFA) + 8 * x + r, n = n0 + 8 * kPer * (t / kFA) + kPer * (lane & 7);
+          if (m < a.M && n < a.N) store_chunk<kBf16Out>(a.C, m * a.N + n, out[t & 1][x], a.N - n);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     if (!more) break;
-    whole_before = whole;
   }
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // nothing writes LDS after the workgroup's end
 }
 
-template <int kF>
+template <int kFA, int kFB, int kWavesB>
 void launch_tile(GemmArgs a, bool bf16, int cus, hipStream_t stream) {
-  a.tiles_m = (int)((a.M + 64 * kF - 1) / (64 * kF));
-  a.tiles_n = (int)((a.N + 64 * kF - 1) / (64 * kF));
+  using Shape = TileShape<kFA, kFB, kWavesB>;
+  a.tiles_m = (int)((a.M + Shape::kTileA - 1) / Shape::kTileA);
+  a.tiles_n = (int)((a.N + Shape::kTileB - 1) / Shape::kTileB);
   const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
-  const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * (kF == 4 ? 1 : 2))), block(kTileThreads);
+  const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * Shape::kPerCu)), block(Shape::kThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, per_xcd); };
   if (a.blocks % 4 == 0)
-    bf16 ? go(mx_gemm_tile_kernel<kF, true, true>) : go(mx_gemm_tile_kernel<kF, true, false>);
+    bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, true, true>) : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, true, false>);
   else
-    bf16 ? go(mx_gemm_tile_kernel<kF, false, true>) : go(mx_gemm_tile_kernel<kF, false, false>);
+    bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, false, true>) : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, false, false>);
 }
 
 template <int kM, int kN, int kW>
@@ -610,9 +679,9 @@ __attribute__((visibility("default"))) int mxfp4_gemm(const void* A, const void*
   else if (N * (K / 32) < 4)
     launch_stream<2, 2, 8>(a, bf16, stream);
   else if (((M + 255) / 256) * ((N + 255) / 256) >= 128)
-    launch_tile<4>(a, bf16, cus, stream);
+    launch_tile<4, 4, 2>(a, bf16, cus, stream);
   else
-    launch_tile<2>(a, bf16, cus, stream);
+    launch_tile<2, 2, 2>(a, bf16, cus, stream);
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }
 

@@ -172,7 +172,8 @@ GEMM_SHAPES = [(1, 1, 32), (1, 16, 32), (1, 17, 64), (1, 4096, 4096), (1, 1000, 
                (33, 130, 2048), (48, 512, 2080), (64, 4096, 1024), (65, 65, 65 * 32), (100, 300, 256), (127, 129, 352),
                (128, 128, 128), (128, 1024, 4096), (200, 250, 288), (255, 257, 256), (256, 256, 512), (256, 512, 768),
                (300, 1001, 1376), (513, 511, 1056), (512, 768, 224), (777, 1001, 1376), (1024, 1024, 1024),
-               (1030, 2060, 544), (2048, 300, 96), (3000, 17, 640), (9, 3000, 32), (1500, 2100, 2048)]
+               (1030, 2060, 544), (4400, 4352, 128), (4352, 4400, 1152), (4360, 4352, 2144), (5000, 4096, 32), (200, 129, 32),
+               (2176, 2200, 640), (2048, 300, 96), (3000, 17, 640), (9, 3000, 32), (1500, 2100, 2048)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM_SHAPES)
