@@ -50,6 +50,9 @@ struct GemmArgs {
   int tiles_m, tiles_n;
 };
 
+// Whether every row's exponents start on 4 bytes, in both operands.
+bool words(const GemmArgs& a) { return a.blocks % 4 == 0 && !misaligned(a.sA, 4) && !misaligned(a.sB, 4); }
+
 // Four consecutive columns of a row of C; `left` of them exist.
 template <bool kBf16Out>
 __device__ __forceinline__ void store4(void* C, int64_t at, const f32x4& v, int64_t left) {
@@ -258,6 +261,13 @@ __device__ __forceinline__ void lds_load16(i32x4 rs, uint32_t lds, uint32_t voff
                  : "memory");
 }
 
+__device__ __forceinline__ void lds_load4(i32x4 rs, uint32_t lds, uint32_t voff) {
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(rs), "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+
 template <int kByte>
 __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x4& b, uint32_t sb, const f32x16& c) {
   const i32x8 wa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
@@ -265,7 +275,7 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, wb, c, kFp4, kFp4, kByte, (int)sa, kByte, (int)sb);
 }
 
-// kWords: rows of exponents start on 4 bytes (K is a multiple of 128).  They
+// kWords: rows of exponents start on 4 bytes (K is a multiple of 128, in aligned buffers).  They
 // then go into LDS too, 32 blocks of every row at a time, a quarter of the next
 // 32 with each stage: read from memory by every wave in every stage, 4 bytes a
 // row, they doubled the requests to L2 and cost a quarter of the time.
@@ -596,8 +606,11 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
         if (t >= 2) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<u32x4_a2*>(to0 + (32 * ((t - 2) % kFA) + 8 * x) * a.N * (16 / kPer) + 128 * ((t - 2) / kFA)) =
-                out[t & 1][x];
+            // streamed: left in L2, a round's results (4 MB an XCD) drive out the
+            // operands (16384 x 22016 x 4096: 806 us, streamed 728 us)
+            __builtin_nontemporal_store(
+                out[t & 1][x], reinterpret_cast<u32x4_a2*>(to0 + (32 * ((t - 2) % kFA) + 8 * x) * a.N * (16 / kPer) +
+                                                           128 * ((t - 2) / kFA)));
         }
         if (t >= 1 && t <= kPieces) get(t - 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -629,10 +642,187 @@ void launch_tile(GemmArgs a, bool bf16, int cus, hipStream_t stream) {
   const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
   const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * Shape::kPerCu)), block(Shape::kThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, per_xcd); };
-  if (a.blocks % 4 == 0)
+  if (words(a))
     bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, true, true>) : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, true, false>);
   else
     bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, false, true>) : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, false, false>);
+}
+
+// ---- few tiles: every wave its own slice of K ----
+//
+// With fewer tiles than CUs, or few rows, the time is that of memory's latency
+// and of the weight's way through the chip.  A workgroup owns a tile of 32 kFA x
+// 32 kFB results; its four waves take its stages (256 values, as above) in turn,
+// each through a ring of kDepth stages of LDS that is its own: a wave waits for
+// nothing but its own oldest loads, and 100 KB or more are on their way to
+// every CU.  The four sums meet in LDS at the end.
+constexpr int kSliceWaves = 4;
+
+template <int kFA, int kFB, int kDepth, bool kBf16Out>
+__global__ __launch_bounds__(64 * kSliceWaves, 1) void mx_gemm_slice_kernel(const GemmArgs a, int per_xcd) {
+  constexpr int kTileA = 32 * kFA, kTileB = 32 * kFB;
+  constexpr int kLoadsA = 4 * kFA, kLoadsB = 4 * kFB;         // 8 rows of 128 bytes each
+  constexpr int kExps = kFA + kFB;                            // 32 rows of 8 exponents each
+  constexpr int kPerStage = kLoadsA + kLoadsB + kExps;        // loads of a wave per stage
+  constexpr int kCodes = (kTileA + kTileB) * kRowBytes, kStage = kCodes + kExps * 256;
+  constexpr int kBlocks = kFA * kFB;
+  constexpr int kRing = kSliceWaves * kDepth * kStage, kSums = (kSliceWaves - 1) * kBlocks * 64 * 64;
+  static_assert(kPerStage * (kDepth - 1) <= 63, "the waits count to 63");
+  __shared__ __attribute__((aligned(16))) char s_lds[kRing > kSums ? kRing : kSums];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 31, half = lane >> 5;
+  // XCDs take contiguous ranges of tiles, down the columns: the tiles that
+  // share a piece of B are near each other
+  const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if (tile >= a.tiles_m * a.tiles_n) return;
+  const int tn = tile / a.tiles_m;
+  const int64_t m0 = (int64_t)(tile - tn * a.tiles_m) * kTileA, n0 = (int64_t)tn * kTileB;
+  const int rows_a = a.M - m0 < kTileA ? (int)(a.M - m0) : kTileA, rows_b = a.N - n0 < kTileB ? (int)(a.N - n0) : kTileB;
+  const int64_t row_bytes = (int64_t)a.blocks * 16;
+  const i32x4 ra = rsrc_words(a.A + m0 * row_bytes, (int)(rows_a * row_bytes));
+  const i32x4 rb = rsrc_words(a.B + n0 * row_bytes, (int)(rows_b * row_bytes));
+  const i32x4 rea = rsrc_words(a.sA + m0 * a.blocks, rows_a * a.blocks);
+  const i32x4 reb = rsrc_words(a.sB + n0 * a.blocks, rows_b * a.blocks);
+  const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;
+  const int mine = (stages - wave + kSliceWaves - 1) / kSliceWaves;  // stages wave, wave + 4, ...
+
+  // Load l covers rows 8 l .. + 7, lane L row L / 8, physical chunk L % 8.
+  constexpr int kMost = kLoadsA > kLoadsB ? kLoadsA : kLoadsB;
+  uint32_t voff[kMost], past_k = 0;
+#pragma unroll
+  for (int l = 0; l < kMost; ++l) {
+    const int r = 8 * l + (lane >> 3), c = (lane & 7) ^ swz(r);
+    voff[l] = (uint32_t)(r * row_bytes + 16 * c);
+    past_k |= (uint32_t)((stages - 1) * kStageBlocks + c >= a.blocks) << l;
+  }
+  const uint32_t voff_e = (uint32_t)((lane >> 1) * a.blocks + 4 * (lane & 1));
+  const bool past_k_e = (stages - 1) * kStageBlocks + 4 * (lane & 1) >= a.blocks;
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(&s_lds[0]) + wave * kDepth * kStage;
+  // This wave's stage i into slot i mod kDepth; past its last, zeros that nobody reads.
+  auto issue = [&](int i, int slot) {
+    const int s = wave + kSliceWaves * i;
+    const uint32_t past = s < stages - 1 ? 0u : s == stages - 1 ? past_k : ~0u;
+    const uint32_t none = s < stages - 1 ? 0u : (s > stages - 1 || past_k_e) ? 0x80000000u : 0u;
+    const uint32_t at = lds0 + slot * kStage;
+#pragma unroll
+    for (int l = 0; l < kMost; ++l) {
+      const uint32_t v = voff[l] | ((past << (31 - l)) & 0x80000000u);
+      if (l < kLoadsA) lds_load16<true>(ra, at + 1024 * l, v, (uint32_t)(s * kRowBytes));
+      if (l < kLoadsB) lds_load16<true>(rb, at + kTileA * kRowBytes + 1024 * l, v, (uint32_t)(s * kRowBytes));
+    }
+#pragma unroll
+    for (int e = 0; e < kExps; ++e) {
+      const int block = e < kFA ? e : e - kFA;
+      lds_load4(e < kFA ? rea : reb, at + kCodes + 256 * e,
+                (voff_e + (uint32_t)(32 * block * a.blocks + s * kStageBlocks)) | none);
+    }
+  };
+
+  f32x16 acc[kFA][kFB];
+#pragma unroll
+  for (int i = 0; i < kFA; ++i)
+#pragma unroll
+    for (int j = 0; j < kFB; ++j) acc[i][j] = (f32x16){};
+  const int base_a = lrow * kRowBytes + 16 * ((4 * half) ^ swz(lrow)), base_b = kTileA * kRowBytes + base_a;
+  auto compute = [&](int i, int slot) {
+    const char* t = s_lds + (wave * kDepth + slot) * kStage;
+    uint32_t sa[kFA], sb[kFB];
+    // in the stage in which K ends, exponents past it: 127
+    uint32_t keep = ~0u;
+    if (wave + kSliceWaves * i == stages - 1) {
+      keep = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((stages - 1) * kStageBlocks + 4 * half + j < a.blocks) keep |= 0xffu << (8 * j);
+    }
+#pragma unroll
+    for (int x = 0; x < kFA; ++x)
+      sa[x] = (*reinterpret_cast<const uint32_t*>(t + kCodes + 256 * x + 8 * lrow + 4 * half) & keep) | (0x7f7f7f7fu & ~keep);
+#pragma unroll
+    for (int x = 0; x < kFB; ++x)
+      sb[x] = (*reinterpret_cast<const uint32_t*>(t + kCodes + 256 * (kFA + x) + 8 * lrow + 4 * half) & keep) |
+              (0x7f7f7f7fu & ~keep);
+    u32x4 fa[4][kFA], fb[4][kFB];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int x = 0; x < kFA; ++x)
+        fa[j][x] = *reinterpret_cast<const u32x4*>(t + (base_a ^ (16 * j) ^ (64 * (x & 1))) + 32 * kRowBytes * x);
+#pragma unroll
+      for (int x = 0; x < kFB; ++x)
+        fb[j][x] = *reinterpret_cast<const u32x4*>(t + (base_b ^ (16 * j) ^ (64 * (x & 1))) + 32 * kRowBytes * x);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // the slot may be written again from here on
+    auto multiply = [&](auto step) {
+      constexpr int j = decltype(step)::value;
+#pragma unroll
+      for (int x = 0; x < kFA; ++x)
+#pragma unroll
+        for (int y = 0; y < kFB; ++y) acc[x][y] = mfma32<j>(fb[j][y], sb[y], fa[j][x], sa[x], acc[x][y]);
+    };
+    multiply(std::integral_constant<int, 0>{});
+    multiply(std::integral_constant<int, 1>{});
+    multiply(std::integral_constant<int, 2>{});
+    multiply(std::integral_constant<int, 3>{});
+  };
+
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) issue(i, i);
+  int slot = 0;
+#pragma unroll 1
+  for (int i = 0; i < mine; ++i) {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kPerStage * (kDepth - 1)) : "memory");
+    compute(i, slot);
+    issue(i + kDepth, slot);
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // nothing writes LDS from here on
+  __syncthreads();
+
+  // Block b of the tile is summed and stored by wave b mod 4; the others leave
+  // theirs in LDS, the sums are added in wave order.
+  f32x4* sums = reinterpret_cast<f32x4*>(s_lds);  // [block][3 others][4][lane]
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    const int owner = b % kSliceWaves;
+    if (wave == owner) continue;
+    const int place = wave - (wave > owner ? 1 : 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x16& d = acc[b / kFB][b % kFB];
+      sums[((b * (kSliceWaves - 1) + place) * 4 + q) * 64 + lane] = (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    if (wave != b % kSliceWaves) continue;
+    const int64_t m = m0 + 32 * (b / kFB) + lrow;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x16& d = acc[b / kFB][b % kFB];
+      const f32x4 own = {d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+      f32x4 v = (f32x4){0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kSliceWaves; ++w)
+        v += w == b % kSliceWaves ? own : sums[((b * (kSliceWaves - 1) + w - (w > b % kSliceWaves ? 1 : 0)) * 4 + q) * 64 + lane];
+      const int64_t n = n0 + 32 * (b % kFB) + 8 * q + 4 * half;
+      if (m < a.M && n < a.N) store4<kBf16Out>(a.C, m * a.N + n, v, a.N - n);
+    }
+  }
+}
+
+template <int kFA, int kFB, int kDepth>
+void launch_slice(GemmArgs a, bool bf16, hipStream_t stream) {
+  a.tiles_m = (int)((a.M + 32 * kFA - 1) / (32 * kFA));
+  a.tiles_n = (int)((a.N + 32 * kFB - 1) / (32 * kFB));
+  const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
+  const dim3 grid(8 * per_xcd), block(64 * kSliceWaves);
+  if (bf16)
+    hipLaunchKernelGGL((mx_gemm_slice_kernel<kFA, kFB, kDepth, true>), grid, block, 0, stream, a, per_xcd);
+  else
+    hipLaunchKernelGGL((mx_gemm_slice_kernel<kFA, kFB, kDepth, false>), grid, block, 0, stream, a, per_xcd);
 }
 
 template <int kM, int kN, int kW>
@@ -646,6 +836,46 @@ void launch_stream(GemmArgs a, bool bf16, hipStream_t stream) {
     hipLaunchKernelGGL((mx_gemm_stream_kernel<kM, kN, kW, false>), grid, block, 0, stream, a);
 }
 
+// Which kernel takes a product.  Measured at K = 4096 and N = 4096 or 22016
+// unless noted; "words" are exponents in aligned words (K a multiple of 128).
+//   * up to 16 rows: the stream, 16 columns per workgroup (1 x 4096 x 11008: 6.4
+//     us, 32 columns 9.4), 32 from about two workgroups per CU on (16 x 22016:
+//     16.6 and 13.5 us);
+//   * few tiles: the smallest slices that need no second round of workgroups (64
+//     x 4096 x 11008: 32 x 32 slices 9.4 us, 64 x 64 16.0, tiles of 128 33; 128 x
+//     4096: 64 x 32 slices 7.4 us, 32 x 32 10.6; 256 x 4096: 64 x 64 slices 8.7
+//     us, tiles of 128 15.1); up to 32 rows of more columns than that, the
+//     stream (32 x 22016: 17.5 us, slices 18.5);
+//   * tiles of 128 or of 256 by their rounds: one of 256 x 256 tiles takes 27 us,
+//     one of 128 x 128 24 us (15 us when every CU has one of them: 512 x 22016:
+//     35 us and 47 us, 2048 x 4096: 28 us and 24 us);
+//   * without words, the stream in place of the slices (777 x 1001 x 1376: 7.1
+//     us in blocks of 32 x 32 by 4 waves, 9.3 us in 64 x 64, tiles 9.8 us; 256 x
+//     4096: 20, 14 and 15 us).
+void pick_and_launch(const GemmArgs& a, bool bf16, int cus, hipStream_t stream) {
+  auto tiles = [&](int64_t tm, int64_t tn) { return ((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn); };
+  if (a.M <= 32 && a.N <= (int64_t(1) << 24)) {
+    if (a.M <= 16)
+      return tiles(16, 16) <= 2 * cus ? launch_stream<1, 1, 8>(a, bf16, stream) : launch_stream<1, 2, 8>(a, bf16, stream);
+    if (tiles(32, 64) > cus) return launch_stream<2, 2, 4>(a, bf16, stream);
+  }
+  if (words(a)) {
+    if (tiles(32, 32) <= cus) return launch_slice<1, 1, 4>(a, bf16, stream);
+    if (a.M <= 32 && tiles(32, 64) <= cus) return launch_slice<1, 2, 3>(a, bf16, stream);
+    if (tiles(64, 32) <= cus) return launch_slice<2, 1, 3>(a, bf16, stream);
+    if (tiles(64, 64) <= cus) return launch_slice<2, 2, 2>(a, bf16, stream);
+  } else {
+    if (tiles(32, 32) <= 3 * cus) return launch_stream<2, 2, 4>(a, bf16, stream);
+    if (tiles(64, 64) <= cus || a.M * a.blocks < 4 || a.N * a.blocks < 4) return launch_stream<4, 4, 4>(a, bf16, stream);
+  }
+  const int64_t small = tiles(128, 128), large = tiles(256, 256);
+  const int64_t cost_small = small <= cus ? 15 : 24 * ((small + 2 * cus - 1) / (2 * cus));
+  if (27 * ((large + cus - 1) / cus) <= cost_small)
+    launch_tile<4, 4, 2>(a, bf16, cus, stream);
+  else
+    launch_tile<2, 2, 2>(a, bf16, cus, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -657,8 +887,8 @@ __attribute__((visibility("default"))) int mxfp4_gemm(const void* A, const void*
       N > (int64_t(1) << 31) || (c_dtype != SILUQUANT_F32 && c_dtype != SILUQUANT_BF16))
     return SILUQUANT_ERR_BAD_SHAPE;
   if (M == 0 || N == 0) return SILUQUANT_OK;
-  // workgroups are counted in 32 bits, at 16 x 16 results each at the least
-  if (((M + 15) / 16) * ((N + 15) / 16) > (int64_t(1) << 30)) return SILUQUANT_ERR_BAD_SHAPE;
+  // tiles are counted in 32 bits, at 128 x 128 results each at the least
+  if (((M + 127) / 128) * ((N + 127) / 128) > (int64_t(1) << 30)) return SILUQUANT_ERR_BAD_SHAPE;
   const bool bf16 = c_dtype == SILUQUANT_BF16;
   if (!C || (K > 0 && (!A || !sA || !B || !sB))) return SILUQUANT_ERR_NULL_PTR;
   if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, bf16 ? 2 : 4)) return SILUQUANT_ERR_MISALIGNED;
@@ -672,16 +902,7 @@ __attribute__((visibility("default"))) int mxfp4_gemm(const void* A, const void*
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
     return SILUQUANT_ERR_DEVICE;
-  if (M <= 16)
-    launch_stream<1, 1, 8>(a, bf16, stream);
-  else if (M <= 64)
-    launch_stream<2, 2, 8>(a, bf16, stream);
-  else if (N * (K / 32) < 4)
-    launch_stream<2, 2, 8>(a, bf16, stream);
-  else if (((M + 255) / 256) * ((N + 255) / 256) >= 128)
-    launch_tile<4, 4, 2>(a, bf16, cus, stream);
-  else
-    launch_tile<2, 2, 2>(a, bf16, cus, stream);
+  pick_and_launch(a, bf16, cus, stream);
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }
 

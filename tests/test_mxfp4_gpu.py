@@ -172,7 +172,8 @@ GEMM_SHAPES = [(1, 1, 32), (1, 16, 32), (1, 17, 64), (1, 4096, 4096), (1, 1000, 
                (33, 130, 2048), (48, 512, 2080), (64, 4096, 1024), (65, 65, 65 * 32), (100, 300, 256), (127, 129, 352),
                (128, 128, 128), (128, 1024, 4096), (200, 250, 288), (255, 257, 256), (256, 256, 512), (256, 512, 768),
                (300, 1001, 1376), (513, 511, 1056), (512, 768, 224), (777, 1001, 1376), (1024, 1024, 1024),
-               (1030, 2060, 544), (4400, 4352, 128), (4352, 4400, 1152), (4360, 4352, 2144), (5000, 4096, 32), (200, 129, 32),
+               (1030, 2060, 544), (4400, 4352, 128), (4352, 4400, 1152), (4360, 4352, 2144), (5000, 4096, 32), (200, 129, 32), (33, 1024, 4096),
+               (60, 2000, 896), (64, 4096, 1408), (120, 4000, 1152), (250, 4000, 640), (20, 9000, 256), (300, 3, 32), (5000, 2, 64),
                (2176, 2200, 640), (2048, 300, 96), (3000, 17, 640), (9, 3000, 32), (1500, 2100, 2048)]
 
 
@@ -219,16 +220,17 @@ def test_product_over_no_values_is_zero(M, N):
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
-def test_product_into_an_unaligned_result(out):
+def test_product_of_unaligned_exponents_and_into_an_unaligned_result(out):
     # C only has to be aligned to its elements
-    ops = operands(20, 36, 320, (126, 127), 11)
-    want = rows64.mx_values(*ops[:2]) @ rows64.mx_values(*ops[2:]).T
-    for shape in ((20, 36, 320), (200, 310, 320)):
+    # and exponents to nothing: K of whole words of them, from odd addresses
+    for shape in ((20, 36, 320), (200, 310, 320), (40, 300, 1024), (1500, 1400, 384)):
         ops = operands(*shape, (126, 127), 12)
         M, N = shape[:2]
         want = torch.from_numpy((rows64.mx_values(*ops[:2]) @ rows64.mx_values(*ops[2:]).T).astype(np.float32))
         buf = torch.full((M * N + 2,), 7.0, dtype=out, device=DEV)
-        sq.mxfp4_gemm(*(torch.from_numpy(t).to(DEV) for t in ops), buf[1:1 + M * N].view(M, N))
+        A, sA, B, sB = (torch.from_numpy(t).to(DEV) for t in ops)
+        odd = lambda t: torch.cat([t.new_full((3,), 255), t.flatten()])[3:].view(t.shape)
+        sq.mxfp4_gemm(A, odd(sA), B, odd(sB), buf[1:1 + M * N].view(M, N))
         got = buf.cpu()
         assert torch.equal(got[1:-1].view(M, N), want.to(out)) and got[0] == 7 and got[-1] == 7
 
