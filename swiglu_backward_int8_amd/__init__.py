@@ -354,42 +354,63 @@ def forward_bytes(T: int, H: int, with_bf16: bool = False, with_weight: bool = F
 # ---- the norm before the products, and the microscaled 4-bit format ----
 #
 # These checks are written for single-token calls, where host time is most of a
-# call: one comparison per property, no containers built unless one fails.
+# call: one comparison per property, integers for devices, no containers.
 
 F32, BF16 = 0, 1
 CODE_INT8, CODE_E4M3 = 0, 1
 MX_BLOCK = 32  # values per E8M0 exponent
 
 
-def _want(name, t, dtypes, shape, dev):
-    if t.dtype not in dtypes or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of %s, shape %s, on %s; got %s %s on %s"
-                         % (name, " or ".join(str(d) for d in dtypes), tuple(shape), dev, t.dtype, tuple(t.shape),
-                            t.device))
+def _refuse(name, t, dtypes, shape, idx):
+    raise ValueError("%s must be a contiguous tensor of %s, shape %s, on cuda:%d; got %s %s on %s%s"
+                     % (name, dtypes, tuple(shape), idx, t.dtype, tuple(t.shape), t.device,
+                        "" if t.is_contiguous() else ", not contiguous"))
+
+
+def _want(name, t, dtype, shape, idx):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, idx)
+
+
+def _want2(name, t, dtype, other, shape, idx):
+    if (t.dtype is not dtype and t.dtype is not other) or t.shape != shape or t.get_device() != idx \
+            or not t.is_contiguous():
+        _refuse(name, t, "%s or %s" % (dtype, other), shape, idx)
 
 
 def _rank2(name, t):
-    if t.dim() != 2:
-        raise ValueError("%s must have two dimensions, got shape %s" % (name, tuple(t.shape)))
-    if t.device.type != "cuda":
+    """(rows, columns, device index) of a two-dimensional GPU tensor."""
+    if not t.is_cuda:
         raise ValueError("tensors must be on a GPU; %s is on %s" % (name, t.device))
-    return t.shape[0], t.shape[1], t.device
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must have two dimensions, got shape %s" % (name, tuple(shape)))
+    return shape[0], shape[1], t.get_device()
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _enqueue(fn, what, dev, *args):
-    """fn(*args, stream) on the current stream of dev, with dev current."""
+def _stream_of(idx):
+    """The current stream of device idx as a hipStream_t."""
     import torch
 
-    if dev.index == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # what current_stream() wraps, without the wrapping
+    return raw(idx) if raw is not None else torch.cuda.current_stream(idx).cuda_stream
+
+
+def _enqueue(fn, what, idx, *args):
+    """fn(*args, stream) on the current stream of device idx, with that device current."""
+    import torch
+
+    if idx == torch.cuda.current_device():
+        code = fn(*args, _stream_of(idx))
     else:
-        with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(code, what)
+        with torch.cuda.device(idx):
+            code = fn(*args, _stream_of(idx))
+    if code:
+        _check(code, what)
 
 
 def _code_format(name, t):
@@ -414,28 +435,28 @@ def rms_norm_quant(x, weight, y_q=None, y_s=None, residual=None, h=None, rstd=No
     needed.  Enqueued on the current stream of x's device; returns None."""
     import torch
 
-    T, D, dev = _rank2("x", x)
-    f32, bf16 = (torch.float32,), (torch.bfloat16,)
+    T, D, idx = _rank2("x", x)
+    f32, bf16 = torch.float32, torch.bfloat16
     if group_size not in GROUPS:
         raise ValueError("group_size must be one of %s" % (GROUPS,))
-    _want("x", x, f32 + bf16, (T, D), dev)
-    _want("weight", weight, bf16, (D,), dev)
+    _want2("x", x, bf16, f32, (T, D), idx)
+    _want("weight", weight, bf16, (D,), idx)
     if (y_q is None) != (y_s is None) or (y_q is None and y_bf16 is None):
         raise ValueError("y_q and y_s go together, and one of y_q and y_bf16 is needed")
     fmt = CODE_INT8
     if y_q is not None:
         fmt = _code_format("y_q", y_q)
-        _want("y_q", y_q, (y_q.dtype,), (T, D), dev)
-        _want("y_s", y_s, f32, (T, -(-D // group_size)), dev)
+        _want("y_q", y_q, y_q.dtype, (T, D), idx)
+        _want("y_s", y_s, f32, (T, -(-D // group_size)), idx)
     if residual is not None:
-        _want("residual", residual, bf16, (T, D), dev)
+        _want("residual", residual, bf16, (T, D), idx)
     if h is not None:
-        _want("h", h, bf16, (T, D), dev)
+        _want("h", h, bf16, (T, D), idx)
     if rstd is not None:
-        _want("rstd", rstd, f32, (T,), dev)
+        _want("rstd", rstd, f32, (T,), idx)
     if y_bf16 is not None:
-        _want("y_bf16", y_bf16, bf16, (T, D), dev)
-    _enqueue(lib().rms_norm_quant, "rms_norm_quant", dev, x.data_ptr(), F32 if x.dtype == torch.float32 else BF16,
+        _want("y_bf16", y_bf16, bf16, (T, D), idx)
+    _enqueue(lib().rms_norm_quant, "rms_norm_quant", idx, x.data_ptr(), F32 if x.dtype == torch.float32 else BF16,
              _ptr(residual), weight.data_ptr(), _ptr(y_q), _ptr(y_s), _ptr(y_bf16), _ptr(h), _ptr(rstd), T, D,
              group_size, fmt, eps)
 
@@ -459,23 +480,23 @@ def rms_norm_bwd(dy, h, weight, rstd, dx, dw=None, d_h=None, workspace=None):
     current stream of dy's device; returns None."""
     import torch
 
-    T, D, dev = _rank2("dy", dy)
-    f32, bf16 = (torch.float32,), (torch.bfloat16,)
-    _want("dy", dy, f32 + bf16, (T, D), dev)
-    _want("h", h, bf16, (T, D), dev)
-    _want("weight", weight, bf16, (D,), dev)
-    _want("rstd", rstd, f32, (T,), dev)
-    _want("dx", dx, bf16, (T, D), dev)
+    T, D, idx = _rank2("dy", dy)
+    f32, bf16 = torch.float32, torch.bfloat16
+    _want2("dy", dy, bf16, f32, (T, D), idx)
+    _want("h", h, bf16, (T, D), idx)
+    _want("weight", weight, bf16, (D,), idx)
+    _want("rstd", rstd, f32, (T,), idx)
+    _want("dx", dx, bf16, (T, D), idx)
     if dw is not None:
-        _want("dw", dw, f32, (D,), dev)
+        _want("dw", dw, f32, (D,), idx)
     if d_h is not None:
-        _want("d_h", d_h, bf16, (T, D), dev)
+        _want("d_h", d_h, bf16, (T, D), idx)
     nbytes = 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+        if workspace.get_device() != idx or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on cuda:%d" % idx)
         nbytes = workspace.numel() * workspace.element_size()
-    _enqueue(lib().rms_norm_bwd, "rms_norm_bwd", dev, dy.data_ptr(), F32 if dy.dtype == torch.float32 else BF16,
+    _enqueue(lib().rms_norm_bwd, "rms_norm_bwd", idx, dy.data_ptr(), F32 if dy.dtype == torch.float32 else BF16,
              h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _ptr(d_h), dx.data_ptr(), _ptr(dw), _ptr(workspace),
              nbytes, T, D)
 
@@ -493,20 +514,20 @@ def mxfp4_quant(x, q=None, s=None, q_t=None, s_t=None):
     device; returns None."""
     import torch
 
-    R, K, dev = _rank2("x", x)
-    u8 = (torch.uint8,)
-    _want("x", x, (torch.bfloat16,), (R, K), dev)
+    R, K, idx = _rank2("x", x)
+    u8 = torch.uint8
+    _want("x", x, torch.bfloat16, (R, K), idx)
     if (q is None) != (s is None) or (q_t is None) != (s_t is None) or (q is None and q_t is None):
         raise ValueError("q and s go together, q_t and s_t too, and one of the pairs is needed")
     if q is not None:
         b = -(-K // MX_BLOCK)
-        _want("q", q, u8, (R, 16 * b), dev)
-        _want("s", s, u8, (R, b), dev)
+        _want("q", q, u8, (R, 16 * b), idx)
+        _want("s", s, u8, (R, b), idx)
     if q_t is not None:
         b = -(-R // MX_BLOCK)
-        _want("q_t", q_t, u8, (K, 16 * b), dev)
-        _want("s_t", s_t, u8, (K, b), dev)
-    _enqueue(lib().mxfp4_quant, "mxfp4_quant", dev, x.data_ptr(), _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t), R, K)
+        _want("q_t", q_t, u8, (K, 16 * b), idx)
+        _want("s_t", s_t, u8, (K, b), idx)
+    _enqueue(lib().mxfp4_quant, "mxfp4_quant", idx, x.data_ptr(), _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t), R, K)
 
 
 def mxfp4_gemm(A, sA, B, sB, C):
@@ -516,15 +537,15 @@ def mxfp4_gemm(A, sA, B, sB, C):
     stream of A's device; returns None."""
     import torch
 
-    M, half, dev = _rank2("A", A)
+    M, half, idx = _rank2("A", A)
     N = _rank2("B", B)[0]
-    u8, blocks = (torch.uint8,), half // 16
-    _want("A", A, u8, (M, 16 * blocks), dev)
-    _want("sA", sA, u8, (M, blocks), dev)
-    _want("B", B, u8, (N, 16 * blocks), dev)
-    _want("sB", sB, u8, (N, blocks), dev)
-    _want("C", C, (torch.float32, torch.bfloat16), (M, N), dev)
-    _enqueue(lib().mxfp4_gemm, "mxfp4_gemm", dev, A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
+    u8, blocks = torch.uint8, half // 16
+    _want("A", A, u8, (M, 16 * blocks), idx)
+    _want("sA", sA, u8, (M, blocks), idx)
+    _want("B", B, u8, (N, 16 * blocks), idx)
+    _want("sB", sB, u8, (N, blocks), idx)
+    _want2("C", C, torch.bfloat16, torch.float32, (M, N), idx)
+    _enqueue(lib().mxfp4_gemm, "mxfp4_gemm", idx, A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
              C.data_ptr(), M, N, 32 * blocks, F32 if C.dtype == torch.float32 else BF16)
 
 
@@ -533,12 +554,12 @@ def mxfp4_dequant(q, s, out):
     (mxfp4_shapes(R, K)).  Enqueued on the current stream of q's device."""
     import torch
 
-    R, K, dev = _rank2("out", out)
+    R, K, idx = _rank2("out", out)
     blocks = -(-K // MX_BLOCK)
-    _want("out", out, (torch.bfloat16,), (R, K), dev)
-    _want("q", q, (torch.uint8,), (R, 16 * blocks), dev)
-    _want("s", s, (torch.uint8,), (R, blocks), dev)
-    _enqueue(lib().mxfp4_dequant, "mxfp4_dequant", dev, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K)
+    _want("out", out, torch.bfloat16, (R, K), idx)
+    _want("q", q, torch.uint8, (R, 16 * blocks), idx)
+    _want("s", s, torch.uint8, (R, blocks), idx)
+    _enqueue(lib().mxfp4_dequant, "mxfp4_dequant", idx, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K)
 
 
 def group_dequant(q, s, out, group_size: int = GROUP):
@@ -547,14 +568,14 @@ def group_dequant(q, s, out, group_size: int = GROUP):
     Enqueued on the current stream of q's device."""
     import torch
 
-    R, K, dev = _rank2("out", out)
+    R, K, idx = _rank2("out", out)
     if group_size not in GROUPS:
         raise ValueError("group_size must be one of %s" % (GROUPS,))
     fmt = _code_format("q", q)
-    _want("out", out, (torch.bfloat16,), (R, K), dev)
-    _want("q", q, (q.dtype,), (R, K), dev)
-    _want("s", s, (torch.float32,), (R, -(-K // group_size)), dev)
-    _enqueue(lib().group_dequant, "group_dequant", dev, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K, group_size,
+    _want("out", out, torch.bfloat16, (R, K), idx)
+    _want("q", q, q.dtype, (R, K), idx)
+    _want("s", s, torch.float32, (R, -(-K // group_size)), idx)
+    _enqueue(lib().group_dequant, "group_dequant", idx, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K, group_size,
              fmt)
 
 

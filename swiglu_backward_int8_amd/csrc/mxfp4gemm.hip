@@ -145,66 +145,63 @@ __global__ __launch_bounds__(64 * kW) void mx_gemm_stream_kernel(const GemmArgs 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kb = lane >> 4;
-  const int tn = blockIdx.x % a.tiles_n, tm = blockIdx.x / a.tiles_n;
-  int64_t row_a[kM], row_b[kN];
+  for (int64_t tile = blockIdx.x; tile < (int64_t)a.tiles_m * a.tiles_n; tile += gridDim.x) {
+    const int tm = (int)(tile / a.tiles_n), tn = (int)(tile - (int64_t)tm * a.tiles_n);
+    int64_t row_a[kM], row_b[kN];
 #pragma unroll
-  for (int i = 0; i < kM; ++i) {
-    const int64_t m = ((int64_t)tm * kM + i) * 16 + r;
-    row_a[i] = m < a.M ? m : a.M - 1;
-  }
+    for (int i = 0; i < kM; ++i) {
+      const int64_t m = ((int64_t)tm * kM + i) * 16 + r;
+      row_a[i] = m < a.M ? m : a.M - 1;
+    }
 #pragma unroll
-  for (int j = 0; j < kN; ++j) {
-    const int64_t n = ((int64_t)tn * kN + j) * 16 + r;
-    row_b[j] = n < a.N ? n : a.N - 1;
-  }
-  // The B rows come first in the instruction, so that a lane holds four
-  // consecutive columns of C: D[row 4 kb + i][column r] = C[m = r][n = 4 kb + i].
-  f32x4 acc[kM][kN];
-#pragma unroll
-  for (int i = 0; i < kM; ++i)
-#pragma unroll
-    for (int j = 0; j < kN; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
-  const int chunks = (a.blocks + kChunkBlocks - 1) / kChunkBlocks;
-  for (int c = wave; c < chunks; c += kW) {
-    Frag fa[kM], fb[kN];
-#pragma unroll
-    for (int j = 0; j < kN; ++j) fb[j] = load_frag(a.B, a.sB, row_b[j], a.blocks, c, kb);
-#pragma unroll
-    for (int i = 0; i < kM; ++i) fa[i] = load_frag(a.A, a.sA, row_a[i], a.blocks, c, kb);
+    for (int j = 0; j < kN; ++j) {
+      const int64_t n = ((int64_t)tn * kN + j) * 16 + r;
+      row_b[j] = n < a.N ? n : a.N - 1;
+    }
+    // The B rows come first in the instruction, so that a lane holds four
+    // consecutive columns of C: D[row 4 kb + i][column r] = C[m = r][n = 4 kb + i].
+    f32x4 acc[kM][kN];
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        acc[i][j] = mfma16<0>(fb[j].c[0], fb[j].s, fa[i].c[0], fa[i].s, acc[i][j]);
-        acc[i][j] = mfma16<1>(fb[j].c[1], fb[j].s, fa[i].c[1], fa[i].s, acc[i][j]);
-        acc[i][j] = mfma16<2>(fb[j].c[2], fb[j].s, fa[i].c[2], fa[i].s, acc[i][j]);
-        acc[i][j] = mfma16<3>(fb[j].c[3], fb[j].s, fa[i].c[3], fa[i].s, acc[i][j]);
-      }
-  }
-  if (kW > 1) {
-    if (wave > 0) {
+      for (int j = 0; j < kN; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+    const int chunks = (a.blocks + kChunkBlocks - 1) / kChunkBlocks;
+    for (int c = wave; c < chunks; c += kW) {
+      Frag fa[kM], fb[kN];
+#pragma unroll
+      for (int j = 0; j < kN; ++j) fb[j] = load_frag(a.B, a.sB, row_b[j], a.blocks, c, kb);
+#pragma unroll
+      for (int i = 0; i < kM; ++i) fa[i] = load_frag(a.A, a.sA, row_a[i], a.blocks, c, kb);
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          acc[i][j] = mfma16<0>(fb[j].c[0], fb[j].s, fa[i].c[0], fa[i].s, acc[i][j]);
+          acc[i][j] = mfma16<1>(fb[j].c[1], fb[j].s, fa[i].c[1], fa[i].s, acc[i][j]);
+          acc[i][j] = mfma16<2>(fb[j].c[2], fb[j].s, fa[i].c[2], fa[i].s, acc[i][j]);
+          acc[i][j] = mfma16<3>(fb[j].c[3], fb[j].s, fa[i].c[3], fa[i].s, acc[i][j]);
+        }
+    }
+    if (kW > 1 && wave > 0) {
 #pragma unroll
       for (int i = 0; i < kM; ++i)
 #pragma unroll
         for (int j = 0; j < kN; ++j) s_sum[wave - 1][i * kN + j][lane] = acc[i][j];
     }
     __syncthreads();
-    if (wave > 0) return;
+    if (wave == 0) {
 #pragma unroll
-    for (int i = 0; i < kM; ++i)
+      for (int i = 0; i < kM; ++i) {
+        const int64_t m = ((int64_t)tm * kM + i) * 16 + r;
 #pragma unroll
-      for (int j = 0; j < kN; ++j)
-        for (int w = 0; w < kW - 1; ++w) acc[i][j] += s_sum[w][i * kN + j][lane];
-  }
-#pragma unroll
-  for (int i = 0; i < kM; ++i) {
-    const int64_t m = ((int64_t)tm * kM + i) * 16 + r;
-    if (m >= a.M) continue;
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int64_t n = ((int64_t)tn * kN + j) * 16 + 4 * kb;
-      if (n < a.N) store4<kBf16Out>(a.C, m * a.N + n, acc[i][j], a.N - n);
+        for (int j = 0; j < kN; ++j) {
+          for (int w = 0; w < kW - 1; ++w) acc[i][j] += s_sum[w][i * kN + j][lane];
+          const int64_t n = ((int64_t)tn * kN + j) * 16 + 4 * kb;
+          if (m < a.M && n < a.N) store4<kBf16Out>(a.C, m * a.N + n, acc[i][j], a.N - n);
+        }
+      }
     }
+    __syncthreads();
   }
 }
 
@@ -829,7 +826,7 @@ template <int kM, int kN, int kW>
 void launch_stream(GemmArgs a, bool bf16, hipStream_t stream) {
   a.tiles_m = (int)((a.M + 16 * kM - 1) / (16 * kM));
   a.tiles_n = (int)((a.N + 16 * kN - 1) / (16 * kN));
-  const dim3 grid((unsigned)((int64_t)a.tiles_m * a.tiles_n)), block(64 * kW);
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.tiles_m * a.tiles_n, 1 << 20)), block(64 * kW);
   if (bf16)
     hipLaunchKernelGGL((mx_gemm_stream_kernel<kM, kN, kW, true>), grid, block, 0, stream, a);
   else
@@ -849,12 +846,11 @@ void launch_stream(GemmArgs a, bool bf16, hipStream_t stream) {
 //   * tiles of 128 or of 256 by their rounds: one of 256 x 256 tiles takes 27 us,
 //     one of 128 x 128 24 us (15 us when every CU has one of them: 512 x 22016:
 //     35 us and 47 us, 2048 x 4096: 28 us and 24 us);
-//   * without words, the stream in place of the slices (777 x 1001 x 1376: 7.1
-//     us in blocks of 32 x 32 by 4 waves, 9.3 us in 64 x 64, tiles 9.8 us; 256 x
-//     4096: 20, 14 and 15 us).
+//   * without words, the stream in place of the slices (256 x 4096 x 1376: 7.3
+//     us, tiles of 128 9.1; 512 x 4096 x 1376: 12.7 and 9.4 us).
 void pick_and_launch(const GemmArgs& a, bool bf16, int cus, hipStream_t stream) {
   auto tiles = [&](int64_t tm, int64_t tn) { return ((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn); };
-  if (a.M <= 32 && a.N <= (int64_t(1) << 24)) {
+  if (a.M <= 32) {
     if (a.M <= 16)
       return tiles(16, 16) <= 2 * cus ? launch_stream<1, 1, 8>(a, bf16, stream) : launch_stream<1, 2, 8>(a, bf16, stream);
     if (tiles(32, 64) > cus) return launch_stream<2, 2, 4>(a, bf16, stream);
@@ -865,8 +861,8 @@ void pick_and_launch(const GemmArgs& a, bool bf16, int cus, hipStream_t stream) 
     if (tiles(64, 32) <= cus) return launch_slice<2, 1, 3>(a, bf16, stream);
     if (tiles(64, 64) <= cus) return launch_slice<2, 2, 2>(a, bf16, stream);
   } else {
-    if (tiles(32, 32) <= 3 * cus) return launch_stream<2, 2, 4>(a, bf16, stream);
-    if (tiles(64, 64) <= cus || a.M * a.blocks < 4 || a.N * a.blocks < 4) return launch_stream<4, 4, 4>(a, bf16, stream);
+    // (the tiles' reads of exponents need four of them in either operand)
+    if (tiles(32, 32) <= 4 * cus || std::min(a.M, a.N) * a.blocks < 4) return launch_stream<2, 2, 4>(a, bf16, stream);
   }
   const int64_t small = tiles(128, 128), large = tiles(256, 256);
   const int64_t cost_small = small <= cus ? 15 : 24 * ((small + 2 * cus - 1) / (2 * cus));
