@@ -77,7 +77,7 @@ struct Walk {
   int64_t units, col_units;
 };
 
-template <class Op, bool kFlat, int kUnroll>
+template <class Op, Kind kKind, int kUnroll>
 __global__ __launch_bounds__(kThreads) void piece_kernel(const Op op, const Walk k) {
   for (int64_t t = blockIdx.x; t * kUnroll < k.units; t += gridDim.x) {
     Where at[kUnroll];
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kThreads) void piece_kernel(const Op op, const Walk
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t unit = t * kUnroll + u;
-      if (kFlat) {
+      if (kKind == kFull) {
         const int64_t p = unit * kThreads + threadIdx.x;
         at[u] = {0, 8 * p, 8, p < k.pieces};
       } else {
@@ -94,10 +94,10 @@ __global__ __launch_bounds__(kThreads) void piece_kernel(const Op op, const Walk
         const int64_t row = rg * (kThreads >> k.lg) + (threadIdx.x >> k.lg);
         at[u] = {row, 8 * p, (int)(k.cols - 8 * p), unit < k.units && row < k.rows && p < k.pieces};
       }
-      in[u] = op.template load<!kFlat>(at[u]);
+      in[u] = op.template load<kKind>(at[u]);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) op.template finish<!kFlat>(at[u], in[u]);
+    for (int u = 0; u < kUnroll; ++u) op.template finish<kKind>(at[u], in[u]);
   }
 }
 
@@ -123,9 +123,11 @@ void launch_walk(const Op& op, int64_t R, int64_t C, int64_t group, hipStream_t 
   const dim3 grid((unsigned)std::min<int64_t>(groups, 1 << 22)), block(kThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, op, k); };
   if (flat)
-    many ? go(piece_kernel<Op, true, 4>) : go(piece_kernel<Op, true, 1>);
+    many ? go(piece_kernel<Op, kFull, 4>) : go(piece_kernel<Op, kFull, 1>);
+  else if (C >= 8)
+    many ? go(piece_kernel<Op, kRagged, 4>) : go(piece_kernel<Op, kRagged, 1>);
   else
-    many ? go(piece_kernel<Op, false, 4>) : go(piece_kernel<Op, false, 1>);
+    many ? go(piece_kernel<Op, kTiny, 4>) : go(piece_kernel<Op, kTiny, 1>);
 }
 
 struct MxQuantRows {
@@ -133,11 +135,11 @@ struct MxQuantRows {
   uint8_t *q, *s;
   int64_t cols, blocks;  // per row
   using In = Piece;
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ In load(const Where& a) const {
-    return a.live ? load_bf16<kTail>(x + a.row * cols + a.col, a.n) : zero_piece();
+    return a.live ? load_bf16<kKind, true>(x + a.row * cols + a.col, a.n) : zero_piece();
   }
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ void finish(const Where& a, const In& p) const {
     const uint32_t b = block_exponent(group_amax_bits<false>(p, 4));
     const uint32_t c = mx_codes8(p, exponent_value(b));
@@ -156,7 +158,7 @@ struct MxDequantRows {
   struct In {
     uint32_t c, b;
   };
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ In load(const Where& a) const {
     In in = {0, 127};
     if (a.live) {
@@ -166,9 +168,9 @@ struct MxDequantRows {
     }
     return in;
   }
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ void finish(const Where& a, const In& in) const {
-    if (a.live) store_bf16<kTail>(out + a.row * cols + a.col, mx_values8(in.c, in.b), a.n);
+    if (a.live) store_bf16<kKind, true>(out + a.row * cols + a.col, mx_values8(in.c, in.b), a.n);
   }
 };
 
@@ -183,12 +185,12 @@ struct GroupDequant {
     uint32_t c[2];
     float s;
   };
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ In load(const Where& a) const {
     In in = {{0, 0}, 0.0f};
-    if (a.live && (!kTail || a.n > 0)) {
+    if (a.live && (kKind == kFull || a.n > 0)) {
       const uint8_t* p = q + a.row * cols + a.col;
-      if (!kTail || a.n >= 8) {
+      if (kKind == kFull || a.n >= 8) {
         const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(p));
         in.c[0] = v.x, in.c[1] = v.y;
       } else {
@@ -200,7 +202,7 @@ struct GroupDequant {
     }
     return in;
   }
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ void finish(const Where& a, const In& in) const {
     float v[8];
 #pragma unroll
@@ -217,7 +219,7 @@ struct GroupDequant {
     Piece p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) p.w[i] = pack_bf16(v[2 * i] * in.s, v[2 * i + 1] * in.s);
-    if (a.live) store_bf16<kTail>(out + a.row * cols + a.col, p, a.n);
+    if (a.live) store_bf16<kKind, true>(out + a.row * cols + a.col, p, a.n);
   }
 };
 
@@ -231,21 +233,48 @@ struct BothArgs {
   int64_t blocks_r;
 };
 
-constexpr int kBothWaves = 4;
-// Wave w of workgroup (bx, by): rows 32 (4 by + w) .. + 31, columns 512 bx .. + 511.
-template <bool kTail>
-__global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const BothArgs a) {
+// A workgroup takes 256 rows x 128 columns, a wave 128 of the rows: lane (b, p) =
+// (lane / 16, lane % 16) holds rows 32 b .. + 31 of columns 8 p .. + 7, so that a
+// load covers 256 bytes of four rows and four neighbouring column blocks leave
+// as 64 contiguous bytes.  The exponents of the columns meet in LDS (stored
+// from the lanes, a byte each in a line of its own, they cost a fifth of the
+// time).  Each XCD takes whole bands of rows, so that the lines that two
+// neighbouring workgroups share are put together in its L2.
+constexpr int kBothWaves = 2, kBothCols = 128, kBothRows = 128 * kBothWaves;
+
+template <Kind kKind>
+__global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const BothArgs a, int64_t tiles, int64_t per_xcd,
+                                                                        int tiles_k) {
+  static_assert(4 * kBothWaves == 8 && 64 * kBothWaves == kBothCols, "a thread stores a column's eight exponents");
+  __shared__ __attribute__((aligned(16))) uint8_t s_exp[kBothCols][4 * kBothWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = 8 * ((int)blockIdx.x * 64 + lane), n = a.K - col;
-  const bool in_block = col < 32 * a.blocks_k;  // the same for four neighbouring lanes
-  for (int64_t br = (int64_t)blockIdx.y * kBothWaves + wave; br < a.blocks_r; br += (int64_t)gridDim.y * kBothWaves) {
-    const int64_t r0 = 32 * br;
-    const int rows_here = (int)(a.R - r0 < 32 ? a.R - r0 : 32);
+  const int blk = lane >> 4, col_in = 8 * (lane & 15);
+  for (int64_t i = blockIdx.x >> 3; i < per_xcd; i += gridDim.x >> 3) {
+    const int64_t tile = (blockIdx.x & 7) * per_xcd + i;
+    if (tile >= tiles) break;
+    const int64_t band = tile / tiles_k;
+    const int col0 = (int)(tile - band * tiles_k) * kBothCols, col = col0 + col_in, n = a.K - col;
+    const bool in_block = col < 32 * a.blocks_k;  // the same for four neighbouring lanes
+    const int64_t br = band * (4 * kBothWaves) + 4 * wave + blk, r0 = 32 * br;
+    const int rows_here = (int)(a.R - r0 < 32 ? (a.R - r0 > 0 ? a.R - r0 : 0) : 32);
+    // rows past the last are read as the last and then taken for zeros: a branch
+    // for each row would load them one by one
     Piece x[32];
+    const uint16_t* from = a.x + r0 * a.K + col;
+    if (kKind == kFull || (rows_here > 0 && (kKind != kWhole || n > 0))) {
 #pragma unroll
-    for (int r = 0; r < 32; ++r)
-      x[r] = (kTail ? n > 0 && r < rows_here : true) ? load_bf16<kTail>(a.x + (r0 + r) * a.K + col, n) : zero_piece();
+      for (int r = 0; r < 32; ++r)
+        x[r] = load_bf16<kKind == kWhole ? kFull : kKind, true>(from + (kKind == kFull ? r : min(r, rows_here - 1)) * (int64_t)a.K, n);
+      if (kKind != kFull && rows_here < 32) {
+#pragma unroll
+        for (int r = 1; r < 32; ++r)
+          if (r >= rows_here) x[r] = zero_piece();
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 32; ++r) x[r] = zero_piece();
+    }
     if (a.q) {
 #pragma unroll
       for (int r4 = 0; r4 < 8; ++r4) {
@@ -255,12 +284,12 @@ __global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const Bo
           const int r = 4 * r4 + j;
           const uint32_t b = block_exponent(group_amax_bits<false>(x[r], 4));
           const uint32_t c = mx_codes8(x[r], exponent_value(b));
-          if (in_block && r < rows_here)
-            __builtin_nontemporal_store(c, reinterpret_cast<uint32_t*>(a.q) + (r0 + r) * (4 * (int64_t)a.blocks_k) + (col >> 3));
+          if (kKind == kFull || (in_block && r < rows_here))
+            reinterpret_cast<uint32_t*>(a.q)[(r0 + r) * (4 * (int64_t)a.blocks_k) + (col >> 3)] = c;
           keep = (lane & 3) == j ? b : keep;
         }
         const int r = 4 * r4 + (lane & 3);  // four rows' exponents in one store
-        if (in_block && r < rows_here) a.s[(r0 + r) * a.blocks_k + (col >> 5)] = (uint8_t)keep;
+        if (kKind == kFull || (in_block && r < rows_here)) a.s[(r0 + r) * a.blocks_k + (col >> 5)] = (uint8_t)keep;
       }
     }
 #pragma unroll
@@ -277,19 +306,31 @@ __global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const Bo
         for (int k = 0; k < 4; ++k) {
           Piece p;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * k + 2 * i;
-            p.w[i] = __builtin_amdgcn_perm(x[r + 1].w[h], x[r].w[h], half ? 0x07060302u : 0x05040100u);
+          for (int t = 0; t < 4; ++t) {
+            const int r = 8 * k + 2 * t;
+            p.w[t] = __builtin_amdgcn_perm(x[r + 1].w[h], x[r].w[h], half ? 0x07060302u : 0x05040100u);
           }
           codes[k] = mx_codes8(p, scale);
         }
-        const int c = col + 2 * h + half;
-        if (c < a.K) {
-          *reinterpret_cast<u32x4*>(a.q_t + ((int64_t)c * a.blocks_r + br) * 16) = codes;
-          a.s_t[(int64_t)c * a.blocks_r + br] = (uint8_t)b;
-        }
+        const int c = 2 * h + half;
+        if (kKind == kFull || (c < n && rows_here > 0))
+          *reinterpret_cast<u32x4*>(a.q_t + ((int64_t)(col + c) * a.blocks_r + br) * 16) = codes;
+        s_exp[col_in + c][4 * wave + blk] = (uint8_t)b;
       }
     }
+    __syncthreads();
+    // 8 exponents of a column in one store where the band has them all
+    const int c = threadIdx.x & (kBothCols - 1);
+    const int64_t br0 = band * (4 * kBothWaves);
+    if (col0 + c < a.K) {
+      uint8_t* to = a.s_t + (int64_t)(col0 + c) * a.blocks_r + br0;
+      if (kKind == kFull || a.blocks_r - br0 >= 4 * kBothWaves) {
+        *reinterpret_cast<u32x2_a1*>(to) = *reinterpret_cast<const u32x2*>(s_exp[c]);
+      } else {
+        for (int k = 0; k < (int)(a.blocks_r - br0); ++k) to[k] = s_exp[c][k];
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -317,11 +358,17 @@ __attribute__((visibility("default"))) int mxfp4_quant(const void* x, void* q, v
     launch_walk(MxQuantRows{xb, qb, sb, K, bk}, R, K, 32, stream);
   } else {
     const BothArgs a = {xb, qb, sb, static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(s_t), R, (int)K, (int)bk, br};
-    const dim3 grid((unsigned)((K + 511) / 512), (unsigned)std::min<int64_t>((br + kBothWaves - 1) / kBothWaves, 32768));
-    if (K % 512 != 0 || R % 32 != 0)
-      hipLaunchKernelGGL((mx_quant_both_kernel<true>), grid, dim3(64 * kBothWaves), 0, stream, a);
+    const int64_t tiles_k = (K + kBothCols - 1) / kBothCols, tiles = (R + kBothRows - 1) / kBothRows * tiles_k;
+    const int64_t per_xcd = (tiles + 7) / 8;
+    const dim3 grid((unsigned)(8 * std::min<int64_t>(per_xcd, 1 << 19)));
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(64 * kBothWaves), 0, stream, a, tiles, per_xcd, (int)tiles_k);
+    };
+    if (K % kBothCols == 0 && R % kBothRows == 0)
+      go(mx_quant_both_kernel<kFull>);
     else
-      hipLaunchKernelGGL((mx_quant_both_kernel<false>), grid, dim3(64 * kBothWaves), 0, stream, a);
+      K % 8 == 0 ? go(mx_quant_both_kernel<kWhole>)
+                 : K > 8 ? go(mx_quant_both_kernel<kRagged>) : go(mx_quant_both_kernel<kTiny>);
   }
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }

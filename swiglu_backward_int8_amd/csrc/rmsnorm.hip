@@ -13,10 +13,12 @@
 // backward pass read, and y is rounded to bf16 before quantising as everywhere
 // in this library, so that codes made here are those of the bf16 y.
 //
-// Layout: one wave per row while a row fits 64 lanes x 8 pieces of 8 columns
-// (D <= 4096), so that rows need no barrier and a lane has up to 16 loads of
-// 16 bytes in flight; four waves per row up to 16384 columns, and also for
-// shorter rows when there are too few rows to fill the chip.
+// Layout: a lane owns two pieces of 8 columns.  Rows of up to 1024 columns go to
+// a wave each, which needs no barrier; longer ones, up to 16384 columns, to a
+// workgroup of as many waves as they fill.  More pieces per lane and fewer
+// waves, which saves the barrier, measured slower (16384 x 4096: four waves of
+// two pieces 80 us, one of eight 89 us): the loads of more waves are in flight
+// while others compute.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,6 +31,9 @@
 namespace {
 
 using namespace rows;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
 
@@ -82,7 +87,7 @@ struct NormArgs {
   uint16_t* h;  // null: no h
   float* rstd;  // null: no statistics
   int64_t T;
-  int D, group_lanes, groups;  // group_lanes: lanes per group (4, 8, 16)
+  int D, lg_lanes, groups;  // lg_lanes: log2 of the lanes per group (4, 8, 16)
   float eps;
 };
 
@@ -92,9 +97,9 @@ struct XPiece;
 template <>
 struct XPiece<false> {
   Piece v;
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ void load(const void* x, int64_t at, int n) {
-    v = load_bf16<kTail>(static_cast<const uint16_t*>(x) + at, n);
+    v = load_bf16<kKind, false>(static_cast<const uint16_t*>(x) + at, n);
   }
   __device__ __forceinline__ Piece plus(const Piece& r) const {
     Piece o;
@@ -108,9 +113,9 @@ struct XPiece<false> {
 template <>
 struct XPiece<true> {
   float v[8];
-  template <bool kTail>
+  template <Kind kKind>
   __device__ __forceinline__ void load(const void* x, int64_t at, int n) {
-    load_f32<kTail>(v, static_cast<const float*>(x) + at, n);
+    load_f32<kKind>(v, static_cast<const float*>(x) + at, n);
   }
   __device__ __forceinline__ Piece plus(const Piece& r) const {
     Piece o;
@@ -146,70 +151,72 @@ __device__ __forceinline__ Piece scaled(const Piece& h, const Piece& w, float rs
 }
 
 // Codes and scale of one piece's group; every lane of the wave calls it.
-template <bool kE4M3, bool kTail>
+template <bool kE4M3, Kind kKind>
 __device__ __forceinline__ void quantise(const NormArgs& a, const Piece& y, int64_t row, int col, int n) {
-  const uint32_t amax = group_amax_bits<true>(y, a.group_lanes);
+  const uint32_t amax = group_amax_bits<true>(y, 1 << a.lg_lanes);
   const float scale = group_scale<kE4M3>(amax);
   const float inv = 1.0f / scale;
   u32x2 c = codes8<kE4M3, false>(y, inv);
   if (__any(inv == __builtin_huge_valf())) c = codes8<kE4M3, true>(y, inv);
   if (n > 0) {
-    store_codes<kTail>(a.q + row * a.D + col, c.x, c.y, n);
-    if ((threadIdx.x & (a.group_lanes - 1)) == 0) a.s[row * a.groups + col / (8 * a.group_lanes)] = scale;
+    store_codes<kKind>(a.q + row * a.D + col, c.x, c.y, n);
+    if ((threadIdx.x & ((1 << a.lg_lanes) - 1)) == 0) a.s[row * a.groups + (col >> (3 + a.lg_lanes))] = scale;
   }
 }
 
-// kWaves waves per row (1: the workgroup's four waves take a row each), each
-// lane kChunks pieces; kTail: D is not a multiple of 8 or of the row's pieces.
-template <int kWaves, int kChunks, bool kXF32, bool kTail, bool kE4M3>
-__global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void rms_norm_quant_kernel(const NormArgs a) {
-  constexpr int kRowsPerGroup = kWaves == 1 ? 4 : 1;
-  __shared__ float s_sum[kWaves];
+// The sum over a workgroup's waves (16 at most) of their own sums, in wave order.
+__device__ __forceinline__ float group_sum(float v, float (&s)[16], int wave, int waves) {
   const int lane = threadIdx.x & 63;
+  v = wave_sum(v);
+  if (lane == 0) s[wave] = v;
+  __syncthreads();
+  v = sum16((lane & 15) < waves ? s[lane & 15] : 0.0f);
+  __syncthreads();  // before the next row's sums
+  return v;
+}
+
+// kOneWave: each wave of the workgroup takes rows of its own; otherwise the
+// workgroup shares a row.  Piece c of a lane starts kPieces' width of the lanes
+// further.
+template <bool kOneWave, int kPieces, bool kXF32, Kind kKind, bool kE4M3>
+__global__ __launch_bounds__(kOneWave ? 256 : 1024) void rms_norm_quant_kernel(const NormArgs a) {
+  __shared__ float s_sum[16];
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int first = 8 * (kWaves == 1 ? lane : (int)threadIdx.x);  // column of piece 0; pieces are kWaves * 512 apart
-  constexpr int kStep = 512 * kWaves;
-  for (int64_t row = (int64_t)blockIdx.x * kRowsPerGroup + (kWaves == 1 ? wave : 0); row < a.T;
-       row += (int64_t)gridDim.x * kRowsPerGroup) {
-    const int64_t at = row * a.D;
-    XPiece<kXF32> x[kChunks];
-    Piece h[kChunks];
+  const int first = 8 * (kOneWave ? lane : (int)threadIdx.x), step = 8 * (kOneWave ? 64 : (int)blockDim.x);
+  const int64_t rows_at_once = kOneWave ? waves : 1;
+  for (int64_t row = blockIdx.x * rows_at_once + (kOneWave ? wave : 0); row < a.T; row += gridDim.x * rows_at_once) {
+    const int64_t at = row * a.D + first;
+    const int n0 = a.D - first;
+    XPiece<kXF32> x[kPieces];
+    Piece h[kPieces], w[kPieces];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) x[c].template load<kTail>(a.x, at + first + c * kStep, a.D - first - c * kStep);
+    for (int c = 0; c < kPieces; ++c) x[c].template load<kKind>(a.x, at + c * step, n0 - c * step);
     if (a.residual) {
-      Piece r[kChunks];
+      Piece r[kPieces];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        r[c] = load_bf16<kTail>(a.residual + at + first + c * kStep, a.D - first - c * kStep);
+      for (int c = 0; c < kPieces; ++c) r[c] = load_bf16<kKind, false>(a.residual + at + c * step, n0 - c * step);
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) h[c] = x[c].plus(r[c]);
+      for (int c = 0; c < kPieces; ++c) h[c] = x[c].plus(r[c]);
     } else {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) h[c] = x[c].alone();
+      for (int c = 0; c < kPieces; ++c) h[c] = x[c].alone();
     }
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) w[c] = load_bf16<kKind, false>(a.weight + first + c * step, n0 - c * step);
     float sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) sum = sum_squares(sum, h[c]);
-    sum = wave_sum(sum);
-    if (kWaves > 1) {
-      if (lane == 0) s_sum[wave] = sum;
-      __syncthreads();
-      sum = s_sum[0];
-#pragma unroll
-      for (int i = 1; i < kWaves; ++i) sum += s_sum[i];
-      __syncthreads();  // before the next row's sums
-    }
+    for (int c = 0; c < kPieces; ++c) sum = sum_squares(sum, h[c]);
+    sum = kOneWave ? wave_sum(sum) : group_sum(sum, s_sum, wave, waves);
     const float rstd = inverse_rms(sum, a.D, a.eps);
     if (a.rstd && first == 0) a.rstd[row] = rstd;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int col = first + c * kStep, n = a.D - col;
-      if (kTail && __all(n <= 0)) break;
-      const Piece w = load_bf16<kTail>(a.weight + col, n);
-      if (a.h) store_bf16<kTail>(a.h + at + col, h[c], n);
-      const Piece y = scaled(h[c], w, rstd);
-      if (a.y) store_bf16<kTail>(a.y + at + col, y, n);
-      if (a.q) quantise<kE4M3, kTail>(a, y, row, col, n);
+    for (int c = 0; c < kPieces; ++c) {
+      const int n = n0 - c * step;
+      if (a.h) store_bf16<kKind, true>(a.h + at + c * step, h[c], n);
+      const Piece y = scaled(h[c], w[c], rstd);
+      if (a.y) store_bf16<kKind, true>(a.y + at + c * step, y, n);
+      if (a.q) quantise<kE4M3, kKind>(a, y, row, first + c * step, n);
     }
   }
 }
@@ -219,7 +226,7 @@ __global__ __launch_bounds__(kWaves == 1 ? 256 : 64 * kWaves) void rms_norm_quan
 constexpr int kWideThreads = 1024;
 template <bool kXF32, bool kE4M3>
 __global__ __launch_bounds__(kWideThreads) void rms_norm_quant_wide_kernel(const NormArgs a) {
-  __shared__ float s_sum[kWideThreads / 64];
+  __shared__ float s_sum[16];
   const int tid = threadIdx.x;
   const int steps = (a.D + 8 * kWideThreads - 1) / (8 * kWideThreads);
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
@@ -227,30 +234,25 @@ __global__ __launch_bounds__(kWideThreads) void rms_norm_quant_wide_kernel(const
     auto h_piece = [&](int col) {
       const int n = a.D - col;
       XPiece<kXF32> x;
-      x.template load<true>(a.x, at + col, n);
-      return a.residual ? x.plus(load_bf16<true>(a.residual + at + col, n)) : x.alone();
+      x.template load<kRagged>(a.x, at + col, n);
+      return a.residual ? x.plus(load_bf16<kRagged, false>(a.residual + at + col, n)) : x.alone();
     };
     float sum = 0.0f;
     for (int i = 0; i < steps; ++i) {
       const int col = 8 * (i * kWideThreads + tid);
       const Piece h = h_piece(col);
-      if (a.h) store_bf16<true>(a.h + at + col, h, a.D - col);
+      if (a.h) store_bf16<kRagged, true>(a.h + at + col, h, a.D - col);
       sum = sum_squares(sum, h);
     }
-    sum = wave_sum(sum);
-    if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
-    __syncthreads();
-    sum = s_sum[0];
-    for (int i = 1; i < kWideThreads / 64; ++i) sum += s_sum[i];
-    __syncthreads();
+    sum = group_sum(sum, s_sum, tid >> 6, kWideThreads / 64);
     const float rstd = inverse_rms(sum, a.D, a.eps);
     if (a.rstd && tid == 0) a.rstd[row] = rstd;
     for (int i = 0; i < steps; ++i) {
       const int col = 8 * (i * kWideThreads + tid), n = a.D - col;
-      const Piece h = a.h ? load_bf16<true>(a.h + at + col, n) : h_piece(col);
-      const Piece y = scaled(h, load_bf16<true>(a.weight + col, n), rstd);
-      if (a.y) store_bf16<true>(a.y + at + col, y, n);
-      if (a.q) quantise<kE4M3, true>(a, y, row, col, n);
+      const Piece h = a.h ? load_bf16<kRagged, false>(a.h + at + col, n) : h_piece(col);
+      const Piece y = scaled(h, load_bf16<kRagged, false>(a.weight + col, n), rstd);
+      if (a.y) store_bf16<kRagged, true>(a.y + at + col, y, n);
+      if (a.q) quantise<kE4M3, kRagged>(a, y, row, col, n);
     }
   }
 }
@@ -269,59 +271,55 @@ struct BwdArgs {
   int D;
 };
 
-template <bool kF32, bool kTail>
+template <bool kF32, Kind kKind>
 __device__ __forceinline__ void load_grad(float (&v)[8], const void* p, int64_t at, int n) {
   if constexpr (kF32)
-    load_f32<kTail>(v, static_cast<const float*>(p) + at, n);
+    load_f32<kKind>(v, static_cast<const float*>(p) + at, n);
   else
-    unpack(v, load_bf16<kTail>(static_cast<const uint16_t*>(p) + at, n));
+    unpack(v, load_bf16<kKind, true>(static_cast<const uint16_t*>(p) + at, n));
 }
 
-// kWaves == 1: each of the workgroup's waves (blockDim.x / 64 of them) walks
-// rows of its own; kWaves == 4: the workgroup's four waves share a row.  A
-// lane keeps the dw sums of its columns in registers over all its rows; the
-// waves' sums are added in LDS at the end, in wave order, so that the result
-// does not depend on timing.
-template <int kWaves, int kChunks, bool kDyF32, bool kTail>
-__global__ __launch_bounds__(kWaves == 1 ? 512 : 64 * kWaves) void rms_norm_bwd_kernel(const BwdArgs a) {
-  __shared__ float s_dw[kWaves == 1 ? 512 * kChunks : 1];
-  __shared__ float s_sum[kWaves];
-  const int lane = threadIdx.x & 63;
+// The same division of rows as in the forward pass.  A lane keeps the dw sums of
+// its columns in registers over all its rows; where waves have rows of their
+// own, their sums are added in LDS at the end, in wave order, so that the
+// result does not depend on timing.
+template <bool kOneWave, int kPieces, bool kDyF32, Kind kKind>
+__global__ __launch_bounds__(kOneWave ? 512 : 1024) void rms_norm_bwd_kernel(const BwdArgs a) {
+  __shared__ float s_dw[kOneWave ? 512 * kPieces : 1];
+  __shared__ float s_sum[16];
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
-  const int first = 8 * (kWaves == 1 ? lane : (int)threadIdx.x);
-  constexpr int kStep = 512 * kWaves;
-  Piece w[kChunks];
-  float dw[kChunks][8];
+  const int first = 8 * (kOneWave ? lane : (int)threadIdx.x), step = 8 * (kOneWave ? 64 : (int)blockDim.x);
+  const int n0 = a.D - first;
+  Piece w[kPieces];
+  float dw[kPieces][8];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    w[c] = load_bf16<kTail>(a.weight + first + c * kStep, a.D - first - c * kStep);
+  for (int c = 0; c < kPieces; ++c) {
+    w[c] = load_bf16<kKind, false>(a.weight + first + c * step, n0 - c * step);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
   }
-  const int64_t per_group = kWaves == 1 ? waves : 1;
-  for (int64_t row = blockIdx.x * per_group + (kWaves == 1 ? wave : 0); row < a.T; row += gridDim.x * per_group) {
-    const int64_t at = row * a.D;
+  const int64_t rows_at_once = kOneWave ? waves : 1;
+  for (int64_t row = blockIdx.x * rows_at_once + (kOneWave ? wave : 0); row < a.T; row += gridDim.x * rows_at_once) {
+    const int64_t at = row * a.D + first;
     const float rstd = a.rstd[row];
-    float dy[kChunks][8];
-    Piece h[kChunks], d[kChunks];
+    float dy[kPieces][8];
+    Piece h[kPieces], d[kPieces];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int col = first + c * kStep, n = a.D - col;
-      load_grad<kDyF32, kTail>(dy[c], a.dy, at + col, n);
-      h[c] = load_bf16<kTail>(a.h + at + col, n);
+    for (int c = 0; c < kPieces; ++c) {
+      load_grad<kDyF32, kKind>(dy[c], a.dy, at + c * step, n0 - c * step);
+      h[c] = load_bf16<kKind, true>(a.h + at + c * step, n0 - c * step);
     }
     if (a.d_h) {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        d[c] = load_bf16<kTail>(a.d_h + at + first + c * kStep, a.D - first - c * kStep);
+      for (int c = 0; c < kPieces; ++c) d[c] = load_bf16<kKind, true>(a.d_h + at + c * step, n0 - c * step);
     } else {
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) d[c] = zero_piece();
+      for (int c = 0; c < kPieces; ++c) d[c] = zero_piece();
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
+    for (int c = 0; c < kPieces; ++c) {
       float hv[8], wv[8];
       unpack(hv, h[c]);
       unpack(wv, w[c]);
@@ -332,18 +330,10 @@ __global__ __launch_bounds__(kWaves == 1 ? 512 : 64 * kWaves) void rms_norm_bwd_
         sum = __builtin_fmaf(dy[c][i] * wv[i], n, sum);
       }
     }
-    sum = wave_sum(sum);
-    if (kWaves > 1) {
-      if (lane == 0) s_sum[wave] = sum;
-      __syncthreads();
-      sum = s_sum[0];
-#pragma unroll
-      for (int i = 1; i < kWaves; ++i) sum += s_sum[i];
-      __syncthreads();
-    }
+    sum = kOneWave ? wave_sum(sum) : group_sum(sum, s_sum, wave, waves);
     const float mean = sum / (float)a.D;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
+    for (int c = 0; c < kPieces; ++c) {
       float hv[8], wv[8], dv[8], o[8];
       unpack(hv, h[c]);
       unpack(wv, w[c]);
@@ -353,18 +343,17 @@ __global__ __launch_bounds__(kWaves == 1 ? 512 : 64 * kWaves) void rms_norm_bwd_
         const float n = hv[i] * rstd, g = dy[c][i] * wv[i];
         o[i] = __builtin_fmaf(rstd, __builtin_fmaf(-n, mean, g), dv[i]);
       }
-      const int col = first + c * kStep;
       const Piece out = {{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])}};
-      store_bf16<kTail>(a.dx + at + col, out, a.D - col);
+      store_bf16<kKind, false>(a.dx + at + c * step, out, n0 - c * step);
     }
   }
   if (!a.part) return;
-  if (kWaves == 1) {
+  if (kOneWave) {
     // wave by wave into LDS; a lane only ever touches the places of its own columns
     for (int turn = 0; turn < waves; ++turn) {
       if (wave == turn) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+        for (int c = 0; c < kPieces; ++c)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float* p = &s_dw[(c * 8 + i) * 64 + lane];
@@ -376,32 +365,42 @@ __global__ __launch_bounds__(kWaves == 1 ? 512 : 64 * kWaves) void rms_norm_bwd_
     }
     if (wave != waves - 1) return;
   }
-  float* out = a.part + (int64_t)blockIdx.x * a.D;
+  float* out = a.part + (int64_t)blockIdx.x * a.D + first;
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c)
+  for (int c = 0; c < kPieces; ++c) {
+    const int n = n0 - c * step;
+    if (kKind == kFull || n >= 8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int col = first + c * kStep + i;
-      if (col < a.D) out[col] = dw[c][i];
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<f32x4_a4*>(out + c * step + 4 * k) =
+            (f32x4){dw[c][4 * k], dw[c][4 * k + 1], dw[c][4 * k + 2], dw[c][4 * k + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) out[c * step + i] = dw[c][i];
     }
+  }
 }
 
-// dw[d] = the sum of the partial rows, in row order within each of 16 strips
-// and then in strip order: 64 columns per workgroup.
-constexpr int kSumStrips = 16;
-__global__ __launch_bounds__(64 * kSumStrips) void rms_norm_dw_kernel(const float* part, float* dw, int parts, int D) {
-  __shared__ float s[kSumStrips][64];
-  const int lane = threadIdx.x & 63, strip = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+// dw[d] = the sum of the partial rows: 16 columns per workgroup, 64 strips of
+// rows, each in row order, and then the strips in order.
+constexpr int kSumStrips = 64, kSumCols = 16;
+__global__ __launch_bounds__(kSumCols * kSumStrips) void rms_norm_dw_kernel(const float* part, float* dw, int parts, int D) {
+  __shared__ float s[kSumStrips][kSumCols];
+  const int c = threadIdx.x & (kSumCols - 1), strip = threadIdx.x / kSumCols;
+  const int col = blockIdx.x * kSumCols + c;
   float sum = 0.0f;
-  if (col < D)
+  if (col < D) {
+#pragma unroll 8
     for (int p = strip; p < parts; p += kSumStrips) sum += part[(int64_t)p * D + col];
-  s[strip][lane] = sum;
-  __syncthreads();
-  if (strip == 0 && col < D) {
-    for (int i = 1; i < kSumStrips; ++i) sum += s[i][lane];
-    dw[col] = sum;
   }
+  s[strip][c] = sum;
+  __syncthreads();
+  for (int half = kSumStrips / 2; half > 0; half >>= 1) {
+    if (strip < half) s[strip][c] += s[strip + half][c];
+    __syncthreads();
+  }
+  if (strip == 0 && col < D) dw[col] = s[0][c];
 }
 
 // Rows past 16384 columns, in two launches: a workgroup per row for the mean,
@@ -415,9 +414,9 @@ __global__ __launch_bounds__(kWideThreads) void rms_norm_bwd_mean_kernel(const B
     float sum = 0.0f;
     for (int col = 8 * tid; col < a.D; col += 8 * kWideThreads) {
       float dy[8], hv[8], wv[8];
-      load_grad<kDyF32, true>(dy, a.dy, row * a.D + col, a.D - col);
-      unpack(hv, load_bf16<true>(a.h + row * a.D + col, a.D - col));
-      unpack(wv, load_bf16<true>(a.weight + col, a.D - col));
+      load_grad<kDyF32, kRagged>(dy, a.dy, row * a.D + col, a.D - col);
+      unpack(hv, load_bf16<kRagged, false>(a.h + row * a.D + col, a.D - col));
+      unpack(wv, load_bf16<kRagged, false>(a.weight + col, a.D - col));
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(dy[i] * wv[i], hv[i] * rstd, sum);
     }
@@ -437,13 +436,13 @@ __global__ __launch_bounds__(kTileThreads) void rms_norm_bwd_tile_kernel(const B
   const int col = 8 * ((int)blockIdx.x * kTileThreads + (int)threadIdx.x), n = a.D - col;
   if (n <= 0) return;
   float wv[8], dw[8] = {};
-  unpack(wv, load_bf16<true>(a.weight + col, n));
+  unpack(wv, load_bf16<kRagged, false>(a.weight + col, n));
   for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
     const float rstd = a.rstd[row], m = mean[row];
     float dy[8], hv[8], dv[8], o[8];
-    load_grad<kDyF32, true>(dy, a.dy, row * a.D + col, n);
-    unpack(hv, load_bf16<true>(a.h + row * a.D + col, n));
-    unpack(dv, a.d_h ? load_bf16<true>(a.d_h + row * a.D + col, n) : zero_piece());
+    load_grad<kDyF32, kRagged>(dy, a.dy, row * a.D + col, n);
+    unpack(hv, load_bf16<kRagged, false>(a.h + row * a.D + col, n));
+    unpack(dv, a.d_h ? load_bf16<kRagged, false>(a.d_h + row * a.D + col, n) : zero_piece());
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = hv[i] * rstd;
@@ -451,7 +450,7 @@ __global__ __launch_bounds__(kTileThreads) void rms_norm_bwd_tile_kernel(const B
       o[i] = __builtin_fmaf(rstd, __builtin_fmaf(-t, m, dy[i] * wv[i]), dv[i]);
     }
     const Piece out = {{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])}};
-    store_bf16<true>(a.dx + row * a.D + col, out, n);
+    store_bf16<kRagged, true>(a.dx + row * a.D + col, out, n);
   }
   if (a.part) {
 #pragma unroll
@@ -464,32 +463,47 @@ constexpr int64_t kMaxD = int64_t(1) << 22, kMaxT = int64_t(1) << 31;
 constexpr int kRegisterD = 16384;  // rows up to here stay in registers
 constexpr int kMaxGrid = 1 << 20;  // workgroups of the forward kernels; further rows are walked
 
-// Workgroups of the backward pass, each with a partial dw row.
-int bwd_parts(int64_t T, int64_t D) { return (int)std::min<int64_t>(T, D <= 2048 ? 256 : 512); }
-
-template <int kWaves, int kChunks>
-void launch_norm(const NormArgs& a, bool f32, bool tail, bool e4m3, hipStream_t stream) {
-  const int64_t groups = kWaves == 1 ? (a.T + 3) / 4 : a.T;
-  const dim3 grid((unsigned)std::min<int64_t>(groups, kMaxGrid)), block(kWaves == 1 ? 256 : 64 * kWaves);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
-  auto pick = [&](auto f, auto t) {
-    if (e4m3)
-      go(rms_norm_quant_kernel<kWaves, kChunks, decltype(f)::value, decltype(t)::value, true>);
-    else
-      go(rms_norm_quant_kernel<kWaves, kChunks, decltype(f)::value, decltype(t)::value, false>);
-  };
-  using Y = std::true_type;
-  using N = std::false_type;
-  f32 ? (tail ? pick(Y{}, Y{}) : pick(Y{}, N{})) : (tail ? pick(N{}, Y{}) : pick(N{}, N{}));
+// Workgroups of the backward pass, each with a partial dw row: eight waves per
+// CU (16384 x 4096, four waves each: 256 workgroups 104 us, 512 90 us, 1024 103
+// us), and one workgroup per CU at the least.
+int bwd_parts(int64_t T, int64_t D) {
+  const int64_t waves = D <= 1024 ? 8 : D <= kRegisterD ? (D + 1023) / 1024 : 8;
+  return (int)std::min<int64_t>(T, std::max<int64_t>(256, 2048 / waves));
 }
 
-template <int kWaves, int kChunks>
-void launch_bwd(const BwdArgs& a, bool f32, bool tail, int grid, int threads, hipStream_t stream) {
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, stream, a); };
-  if (f32)
-    tail ? go(rms_norm_bwd_kernel<kWaves, kChunks, true, true>) : go(rms_norm_bwd_kernel<kWaves, kChunks, true, false>);
+// Calls f with the kind of the pieces of a row of D columns, where the lanes'
+// pieces cover `covered`, as a type.
+template <class F>
+void with_kind(int64_t D, int64_t covered, F&& f) {
+  if (D == covered)
+    f(std::integral_constant<Kind, kFull>{});
+  else if (D % 8 == 0)
+    f(std::integral_constant<Kind, kWhole>{});
   else
-    tail ? go(rms_norm_bwd_kernel<kWaves, kChunks, false, true>) : go(rms_norm_bwd_kernel<kWaves, kChunks, false, false>);
+    D >= 8 ? f(std::integral_constant<Kind, kRagged>{}) : f(std::integral_constant<Kind, kTiny>{});
+}
+
+template <bool kOneWave, int kPieces>
+void launch_norm(const NormArgs& a, bool f32, bool e4m3, int waves, hipStream_t stream) {
+  const int64_t groups = kOneWave ? (a.T + waves - 1) / waves : a.T;
+  const dim3 grid((unsigned)std::min<int64_t>(groups, kMaxGrid)), block(64 * waves);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+  with_kind(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
+    constexpr Kind k = decltype(kind)::value;
+    if (f32)
+      e4m3 ? go(rms_norm_quant_kernel<kOneWave, kPieces, true, k, true>) : go(rms_norm_quant_kernel<kOneWave, kPieces, true, k, false>);
+    else
+      e4m3 ? go(rms_norm_quant_kernel<kOneWave, kPieces, false, k, true>) : go(rms_norm_quant_kernel<kOneWave, kPieces, false, k, false>);
+  });
+}
+
+template <bool kOneWave, int kPieces>
+void launch_bwd(const BwdArgs& a, bool f32, int grid, int waves, hipStream_t stream) {
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * waves), 0, stream, a); };
+  with_kind(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
+    constexpr Kind k = decltype(kind)::value;
+    f32 ? go(rms_norm_bwd_kernel<kOneWave, kPieces, true, k>) : go(rms_norm_bwd_kernel<kOneWave, kPieces, false, k>);
+  });
 }
 
 }  // namespace
@@ -523,7 +537,7 @@ __attribute__((visibility("default"))) int rms_norm_quant(const void* x, int x_d
   const bool e4m3 = code_format == SILUQUANT_CODE_E4M3;
   const NormArgs a = {x, static_cast<const uint16_t*>(residual), static_cast<const uint16_t*>(weight),
                       static_cast<uint8_t*>(y_q), y_s, static_cast<uint16_t*>(y_bf16), static_cast<uint16_t*>(h),
-                      rstd, T, (int)D, (int)(group / 8), (int)groups, eps};
+                      rstd, T, (int)D, group == 32 ? 2 : group == 64 ? 3 : 4, (int)groups, eps};
   if (D > kRegisterD) {
     const dim3 grid((unsigned)std::min<int64_t>(T, kMaxGrid)), block(kWideThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
@@ -532,16 +546,9 @@ __attribute__((visibility("default"))) int rms_norm_quant(const void* x, int x_d
     else
       e4m3 ? go(rms_norm_quant_wide_kernel<false, true>) : go(rms_norm_quant_wide_kernel<false, false>);
   } else {
-    const bool few = T < 2048;  // too few rows for a wave each to fill 256 CUs
-    auto tail = [&](int columns) { return D % columns != 0; };
-    if (D <= 512) launch_norm<1, 1>(a, f32, tail(512), e4m3, stream);
-    else if (few && D <= 2048) launch_norm<4, 1>(a, f32, tail(2048), e4m3, stream);
-    else if (few && D <= 4096) launch_norm<4, 2>(a, f32, tail(4096), e4m3, stream);
-    else if (D <= 1024) launch_norm<1, 2>(a, f32, tail(1024), e4m3, stream);
-    else if (D <= 2048) launch_norm<1, 4>(a, f32, tail(2048), e4m3, stream);
-    else if (D <= 4096) launch_norm<1, 8>(a, f32, tail(4096), e4m3, stream);
-    else if (D <= 8192) launch_norm<4, 4>(a, f32, tail(8192), e4m3, stream);
-    else launch_norm<4, 8>(a, f32, tail(16384), e4m3, stream);
+    if (D <= 512) launch_norm<true, 1>(a, f32, e4m3, 4, stream);
+    else if (D <= 1024) launch_norm<true, 2>(a, f32, e4m3, 4, stream);
+    else launch_norm<false, 2>(a, f32, e4m3, (int)((D + 1023) / 1024), stream);
   }
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }
@@ -563,7 +570,7 @@ __attribute__((visibility("default"))) int rms_norm_bwd(const void* dy, int dy_d
   if (T == 0) {  // no rows: no gradient for the weight
     if (!dw) return SILUQUANT_OK;
     if (misaligned(dw, 4)) return SILUQUANT_ERR_MISALIGNED;
-    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((D + 63) / 64)), dim3(64 * kSumStrips), 0, stream,
+    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((D + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumStrips), 0, stream,
                        (const float*)nullptr, dw, 0, (int)D);
     return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
   }
@@ -600,16 +607,12 @@ __attribute__((visibility("default"))) int rms_norm_bwd(const void* dy, int dy_d
     }
   } else {
     const int waves = (int)std::min<int64_t>((T + parts - 1) / parts, 8);
-    auto tail = [&](int columns) { return D % columns != 0; };
-    if (D <= 512) launch_bwd<1, 1>(a, f32, tail(512), parts, 64 * waves, stream);
-    else if (D <= 1024) launch_bwd<1, 2>(a, f32, tail(1024), parts, 64 * waves, stream);
-    else if (D <= 2048) launch_bwd<1, 4>(a, f32, tail(2048), parts, 64 * waves, stream);
-    else if (D <= 4096) launch_bwd<4, 2>(a, f32, tail(4096), parts, 256, stream);
-    else if (D <= 8192) launch_bwd<4, 4>(a, f32, tail(8192), parts, 256, stream);
-    else launch_bwd<4, 8>(a, f32, tail(16384), parts, 256, stream);
+    if (D <= 512) launch_bwd<true, 1>(a, f32, parts, waves, stream);
+    else if (D <= 1024) launch_bwd<true, 2>(a, f32, parts, waves, stream);
+    else launch_bwd<false, 2>(a, f32, parts, (int)((D + 1023) / 1024), stream);
   }
   if (dw && parts > 1)
-    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((D + 63) / 64)), dim3(64 * kSumStrips), 0, stream, part, dw,
+    hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((D + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumStrips), 0, stream, part, dw,
                        parts, (int)D);
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }

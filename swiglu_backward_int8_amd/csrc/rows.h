@@ -6,8 +6,9 @@
 // lanes own a group of 32, 64 or 128.  Rows of a width that is not a multiple
 // of 8 start off 16 bytes: the pieces are then loaded and stored with the same
 // 16-byte instructions at 2-byte alignment (gfx950 takes them; the vector
-// types below say so to the compiler), and only a row's last, partial piece
-// goes element by element.
+// types below say so to the compiler).  A row's last, partial piece is loaded
+// from where it ends and shifted, so that no lane leaves the others' way; it is
+// stored element by element.
 #ifndef SILUQUANT_ROWS_H
 #define SILUQUANT_ROWS_H
 
@@ -39,40 +40,79 @@ struct Piece {
 };
 __device__ __forceinline__ Piece zero_piece() { return {{0, 0, 0, 0}}; }
 
-// n: how many of the piece's eight elements the row has; kTail says that n may
-// be other than 8 (0 and below: none).
-template <bool kTail>
+// What a piece may be, by the row's width: whole (kFull); whole or none of the
+// row's (kWhole, widths of a multiple of 8); partial (kRagged), in rows of at
+// least eight elements, or shorter ones (kTiny).  n: how many of its eight
+// elements the row has, 0 and below for none; looked at as far as the kind asks.
+enum Kind { kFull = 0, kWhole = 1, kRagged = 2, kTiny = 3 };
+
+__device__ __forceinline__ Piece piece_of(const u32x4& v) { return {{v.x, v.y, v.z, v.w}}; }
+
+// The elements d and on of a piece, in its first places, zeros behind them.
+__device__ __forceinline__ Piece shifted(Piece v, int d) {
+  if (d & 4) v = {{v.w[2], v.w[3], 0, 0}};
+  if (d & 2) v = {{v.w[1], v.w[2], v.w[3], 0}};
+  if (d & 1)
+    v = {{__builtin_amdgcn_alignbit(v.w[1], v.w[0], 16), __builtin_amdgcn_alignbit(v.w[2], v.w[1], 16),
+          __builtin_amdgcn_alignbit(v.w[3], v.w[2], 16), v.w[3] >> 16}};
+  if (d >= 8) v = zero_piece();
+  return v;
+}
+
+// kNt: streamed, for what nobody reads soon.
+template <Kind kKind, bool kNt>
 __device__ __forceinline__ Piece load_bf16(const uint16_t* p, int n) {
-  Piece r = zero_piece();
-  if (!kTail || n >= 8) {
-    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
-    r = {{v.x, v.y, v.z, v.w}};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) r.w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  auto at = [](const uint16_t* q) {
+    const u32x4_a2* v = reinterpret_cast<const u32x4_a2*>(q);
+    return piece_of(kNt ? __builtin_nontemporal_load(v) : *v);
+  };
+  if (kKind == kFull) return at(p);
+  if (kKind == kWhole) return n > 0 ? at(p) : zero_piece();
+  if (kKind == kRagged) {
+    const int d = n < 8 ? 8 - n : 0;  // past the row's end: its last eight elements, all shifted out
+    return shifted(at(p - d), d);
   }
+  Piece r = zero_piece();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) r.w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
   return r;
 }
 
-template <bool kTail>
+template <Kind kKind>
 __device__ __forceinline__ void load_f32(float (&v)[8], const float* p, int n) {
-  if (!kTail || n >= 8) {
-    const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p));
-    const u32x4 b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p + 4));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]), v[4 + i] = __uint_as_float(b[i]);
-  } else {
+  if (kKind == kTiny) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+    return;
   }
+  const int d = kKind == kRagged && n < 8 ? 8 - n : 0;
+  u32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+  if (kKind != kWhole || n > 0) {
+    a = *reinterpret_cast<const u32x4_a4*>(p - d);
+    b = *reinterpret_cast<const u32x4_a4*>(p - d + 4);
+  }
+  if (kKind == kRagged) {
+    const u32x4 zero = {0, 0, 0, 0};
+    if (d & 4) a = b, b = zero;
+    if (d & 2) a = (u32x4){a.z, a.w, b.x, b.y}, b = (u32x4){b.z, b.w, 0, 0};
+    if (d & 1) a = (u32x4){a.y, a.z, a.w, b.x}, b = (u32x4){b.y, b.z, b.w, 0};
+    if (d >= 8) a = zero, b = zero;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]), v[4 + i] = __uint_as_float(b[i]);
 }
 
-template <bool kTail>
+template <Kind kKind, bool kNt>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const Piece& v, int n) {
-  if (!kTail || n >= 8) {
-    __builtin_nontemporal_store((u32x4){v.w[0], v.w[1], v.w[2], v.w[3]}, reinterpret_cast<u32x4_a2*>(p));
-  } else {
+  if (kKind == kFull || (kKind == kWhole ? n > 0 : n >= 8)) {
+    const u32x4 x = {v.w[0], v.w[1], v.w[2], v.w[3]};
+    u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p);
+    if (kNt)
+      __builtin_nontemporal_store(x, q);
+    else
+      *q = x;
+  } else if (kKind >= kRagged) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
       if (i < n) p[i] = (uint16_t)(v.w[i >> 1] >> (16 * (i & 1)));
@@ -80,11 +120,11 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const Piece& v, int n) {
 }
 
 // Eight one-byte codes.
-template <bool kTail>
+template <Kind kKind>
 __device__ __forceinline__ void store_codes(uint8_t* p, uint32_t lo, uint32_t hi, int n) {
-  if (!kTail || n >= 8) {
+  if (kKind == kFull || (kKind == kWhole ? n > 0 : n >= 8)) {
     __builtin_nontemporal_store((u32x2){lo, hi}, reinterpret_cast<u32x2_a1*>(p));
-  } else {
+  } else if (kKind >= kRagged) {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
       if (i < n) p[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
@@ -125,12 +165,17 @@ __device__ __forceinline__ uint32_t group_amax_bits(const Piece& p, int lanes) {
   return max(m & 0xffffu, m >> 16);
 }
 
-// Sum over the 64 lanes of a wave, in every lane, always added in the same order.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sums over 16 lanes, and over the 64 of a wave, in every lane, always added in
+// the same order.
+__device__ __forceinline__ float sum16(float v) {
   v += __uint_as_float(dpp<kXor1>(__float_as_uint(v)));
   v += __uint_as_float(dpp<kXor2>(__float_as_uint(v)));
   v += __uint_as_float(dpp<kHalfMirror>(__float_as_uint(v)));
   v += __uint_as_float(dpp<kMirror>(__float_as_uint(v)));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum16(v);
   v += __shfl_xor(v, 16);
   v += __shfl_xor(v, 32);
   return v;
