@@ -360,6 +360,21 @@ F32, BF16 = 0, 1
 CODE_INT8, CODE_E4M3 = 0, 1
 MX_BLOCK = 32  # values per E8M0 exponent
 
+_torch = None  # torch and what of it every call needs, once the first call has imported it
+
+
+def _need_torch():
+    global _torch, _f32, _bf16, _u8, _i8, _e4m3, _device_of_thread, _raw_stream
+    import torch
+
+    torch.cuda.init()
+    _f32, _bf16, _u8, _i8, _e4m3 = torch.float32, torch.bfloat16, torch.uint8, torch.int8, torch.float8_e4m3fn
+    # what current_device() and current_stream() wrap, without the wrapping (3 us a call)
+    _device_of_thread = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda idx: torch.cuda.current_stream(idx).cuda_stream)
+    _torch = torch
+
 
 def _refuse(name, t, dtypes, shape, idx):
     raise ValueError("%s must be a contiguous tensor of %s, shape %s, on cuda:%d; got %s %s on %s%s"
@@ -382,6 +397,8 @@ def _rank2(name, t):
     """(rows, columns, device index) of a two-dimensional GPU tensor."""
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU; %s is on %s" % (name, t.device))
+    if _torch is None:
+        _need_torch()
     shape = t.shape
     if len(shape) != 2:
         raise ValueError("%s must have two dimensions, got shape %s" % (name, tuple(shape)))
@@ -392,33 +409,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(idx):
-    """The current stream of device idx as a hipStream_t."""
-    import torch
-
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # what current_stream() wraps, without the wrapping
-    return raw(idx) if raw is not None else torch.cuda.current_stream(idx).cuda_stream
-
-
 def _enqueue(fn, what, idx, *args):
     """fn(*args, stream) on the current stream of device idx, with that device current."""
-    import torch
-
-    if idx == torch.cuda.current_device():
-        code = fn(*args, _stream_of(idx))
+    if idx == _device_of_thread():
+        code = fn(*args, _raw_stream(idx))
     else:
-        with torch.cuda.device(idx):
-            code = fn(*args, _stream_of(idx))
+        with _torch.cuda.device(idx):
+            code = fn(*args, _raw_stream(idx))
     if code:
         _check(code, what)
 
 
 def _code_format(name, t):
-    import torch
-
-    if t.dtype == torch.int8:
+    if t.dtype is _i8:
         return CODE_INT8
-    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
+    if t.dtype is _e4m3 or t.dtype is _u8:
         return CODE_E4M3
     raise ValueError("%s must be int8, or uint8 or float8_e4m3fn (E4M3); got %s" % (name, t.dtype))
 
@@ -433,30 +438,27 @@ def rms_norm_quant(x, weight, y_q=None, y_s=None, residual=None, h=None, rstd=No
     y_s fp32 [T, ceil(D/group_size)], y_bf16 [T, D], h bf16 [T, D] (may be
     residual itself) and rstd fp32 [T].  At least one of y_q and y_bf16 is
     needed.  Enqueued on the current stream of x's device; returns None."""
-    import torch
-
     T, D, idx = _rank2("x", x)
-    f32, bf16 = torch.float32, torch.bfloat16
     if group_size not in GROUPS:
         raise ValueError("group_size must be one of %s" % (GROUPS,))
-    _want2("x", x, bf16, f32, (T, D), idx)
-    _want("weight", weight, bf16, (D,), idx)
+    _want2("x", x, _bf16, _f32, (T, D), idx)
+    _want("weight", weight, _bf16, (D,), idx)
     if (y_q is None) != (y_s is None) or (y_q is None and y_bf16 is None):
         raise ValueError("y_q and y_s go together, and one of y_q and y_bf16 is needed")
     fmt = CODE_INT8
     if y_q is not None:
         fmt = _code_format("y_q", y_q)
         _want("y_q", y_q, y_q.dtype, (T, D), idx)
-        _want("y_s", y_s, f32, (T, -(-D // group_size)), idx)
+        _want("y_s", y_s, _f32, (T, -(-D // group_size)), idx)
     if residual is not None:
-        _want("residual", residual, bf16, (T, D), idx)
+        _want("residual", residual, _bf16, (T, D), idx)
     if h is not None:
-        _want("h", h, bf16, (T, D), idx)
+        _want("h", h, _bf16, (T, D), idx)
     if rstd is not None:
-        _want("rstd", rstd, f32, (T,), idx)
+        _want("rstd", rstd, _f32, (T,), idx)
     if y_bf16 is not None:
-        _want("y_bf16", y_bf16, bf16, (T, D), idx)
-    _enqueue(lib().rms_norm_quant, "rms_norm_quant", idx, x.data_ptr(), F32 if x.dtype == torch.float32 else BF16,
+        _want("y_bf16", y_bf16, _bf16, (T, D), idx)
+    _enqueue(lib().rms_norm_quant, "rms_norm_quant", idx, x.data_ptr(), F32 if x.dtype is _f32 else BF16,
              _ptr(residual), weight.data_ptr(), _ptr(y_q), _ptr(y_s), _ptr(y_bf16), _ptr(h), _ptr(rstd), T, D,
              group_size, fmt, eps)
 
@@ -478,25 +480,22 @@ def rms_norm_bwd(dy, h, weight, rstd, dx, dw=None, d_h=None, workspace=None):
     weight, rstd as in the forward call.  workspace: from
     rms_norm_bwd_workspace, needed for dw and for D > 16384.  Enqueued on the
     current stream of dy's device; returns None."""
-    import torch
-
     T, D, idx = _rank2("dy", dy)
-    f32, bf16 = torch.float32, torch.bfloat16
-    _want2("dy", dy, bf16, f32, (T, D), idx)
-    _want("h", h, bf16, (T, D), idx)
-    _want("weight", weight, bf16, (D,), idx)
-    _want("rstd", rstd, f32, (T,), idx)
-    _want("dx", dx, bf16, (T, D), idx)
+    _want2("dy", dy, _bf16, _f32, (T, D), idx)
+    _want("h", h, _bf16, (T, D), idx)
+    _want("weight", weight, _bf16, (D,), idx)
+    _want("rstd", rstd, _f32, (T,), idx)
+    _want("dx", dx, _bf16, (T, D), idx)
     if dw is not None:
-        _want("dw", dw, f32, (D,), idx)
+        _want("dw", dw, _f32, (D,), idx)
     if d_h is not None:
-        _want("d_h", d_h, bf16, (T, D), idx)
+        _want("d_h", d_h, _bf16, (T, D), idx)
     nbytes = 0
     if workspace is not None:
         if workspace.get_device() != idx or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on cuda:%d" % idx)
         nbytes = workspace.numel() * workspace.element_size()
-    _enqueue(lib().rms_norm_bwd, "rms_norm_bwd", idx, dy.data_ptr(), F32 if dy.dtype == torch.float32 else BF16,
+    _enqueue(lib().rms_norm_bwd, "rms_norm_bwd", idx, dy.data_ptr(), F32 if dy.dtype is _f32 else BF16,
              h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _ptr(d_h), dx.data_ptr(), _ptr(dw), _ptr(workspace),
              nbytes, T, D)
 
@@ -512,21 +511,18 @@ def mxfp4_quant(x, q=None, s=None, q_t=None, s_t=None):
     K)), q_t and s_t of the transpose (mxfp4_shapes(K, R)), all uint8; either
     pair or both, from one read of x.  Enqueued on the current stream of x's
     device; returns None."""
-    import torch
-
     R, K, idx = _rank2("x", x)
-    u8 = torch.uint8
-    _want("x", x, torch.bfloat16, (R, K), idx)
+    _want("x", x, _bf16, (R, K), idx)
     if (q is None) != (s is None) or (q_t is None) != (s_t is None) or (q is None and q_t is None):
         raise ValueError("q and s go together, q_t and s_t too, and one of the pairs is needed")
     if q is not None:
         b = -(-K // MX_BLOCK)
-        _want("q", q, u8, (R, 16 * b), idx)
-        _want("s", s, u8, (R, b), idx)
+        _want("q", q, _u8, (R, 16 * b), idx)
+        _want("s", s, _u8, (R, b), idx)
     if q_t is not None:
         b = -(-R // MX_BLOCK)
-        _want("q_t", q_t, u8, (K, 16 * b), idx)
-        _want("s_t", s_t, u8, (K, b), idx)
+        _want("q_t", q_t, _u8, (K, 16 * b), idx)
+        _want("s_t", s_t, _u8, (K, b), idx)
     _enqueue(lib().mxfp4_quant, "mxfp4_quant", idx, x.data_ptr(), _ptr(q), _ptr(s), _ptr(q_t), _ptr(s_t), R, K)
 
 
@@ -535,30 +531,26 @@ def mxfp4_gemm(A, sA, B, sB, C):
     sA uint8 [M, K/32], B uint8 [N, K/2] with sB uint8 [N, K/32] (as mxfp4_quant
     writes them), C fp32 or bf16 [M, N], overwritten.  Enqueued on the current
     stream of A's device; returns None."""
-    import torch
-
     M, half, idx = _rank2("A", A)
     N = _rank2("B", B)[0]
-    u8, blocks = torch.uint8, half // 16
-    _want("A", A, u8, (M, 16 * blocks), idx)
-    _want("sA", sA, u8, (M, blocks), idx)
-    _want("B", B, u8, (N, 16 * blocks), idx)
-    _want("sB", sB, u8, (N, blocks), idx)
-    _want2("C", C, torch.bfloat16, torch.float32, (M, N), idx)
+    blocks = half // 16
+    _want("A", A, _u8, (M, 16 * blocks), idx)
+    _want("sA", sA, _u8, (M, blocks), idx)
+    _want("B", B, _u8, (N, 16 * blocks), idx)
+    _want("sB", sB, _u8, (N, blocks), idx)
+    _want2("C", C, _bf16, _f32, (M, N), idx)
     _enqueue(lib().mxfp4_gemm, "mxfp4_gemm", idx, A.data_ptr(), sA.data_ptr(), B.data_ptr(), sB.data_ptr(),
-             C.data_ptr(), M, N, 32 * blocks, F32 if C.dtype == torch.float32 else BF16)
+             C.data_ptr(), M, N, 32 * blocks, F32 if C.dtype is _f32 else BF16)
 
 
 def mxfp4_dequant(q, s, out):
     """out bf16 [R, K] = the values of microscaled 4-bit codes q, s
     (mxfp4_shapes(R, K)).  Enqueued on the current stream of q's device."""
-    import torch
-
     R, K, idx = _rank2("out", out)
     blocks = -(-K // MX_BLOCK)
-    _want("out", out, torch.bfloat16, (R, K), idx)
-    _want("q", q, torch.uint8, (R, 16 * blocks), idx)
-    _want("s", s, torch.uint8, (R, blocks), idx)
+    _want("out", out, _bf16, (R, K), idx)
+    _want("q", q, _u8, (R, 16 * blocks), idx)
+    _want("s", s, _u8, (R, blocks), idx)
     _enqueue(lib().mxfp4_dequant, "mxfp4_dequant", idx, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K)
 
 
@@ -566,15 +558,13 @@ def group_dequant(q, s, out, group_size: int = GROUP):
     """out bf16 [R, K] = code * scale of the group-quantised rows q (int8, or
     E4M3 as uint8 or float8_e4m3fn) [R, K] and s fp32 [R, ceil(K/group_size)].
     Enqueued on the current stream of q's device."""
-    import torch
-
     R, K, idx = _rank2("out", out)
     if group_size not in GROUPS:
         raise ValueError("group_size must be one of %s" % (GROUPS,))
     fmt = _code_format("q", q)
-    _want("out", out, torch.bfloat16, (R, K), idx)
+    _want("out", out, _bf16, (R, K), idx)
     _want("q", q, q.dtype, (R, K), idx)
-    _want("s", s, torch.float32, (R, -(-K // group_size)), idx)
+    _want("s", s, _f32, (R, -(-K // group_size)), idx)
     _enqueue(lib().group_dequant, "group_dequant", idx, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K, group_size,
              fmt)
 
