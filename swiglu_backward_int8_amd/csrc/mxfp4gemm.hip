@@ -277,19 +277,21 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x
 // 32 with each stage: read from memory by every wave in every stage, 4 bytes a
 // row, they doubled the requests to L2 and cost a quarter of the time.
 //
-// Workgroups are persistent (one per CU for 256 x 256, two for 128 x 128): the
+// Workgroups are persistent (one per CU for 256 x 256, two for 128 x 128, or one
+// with four buffers, whose loads are three stages ahead): the
 // next tile's first stage is asked for before the present one's results are
 // stored, and the stores drain behind its first stage.
-template <int kFA, int kFB, int kWavesB>
+template <int kFA, int kFB, int kWavesB, int kBufs>
 struct TileShape {
   static constexpr int kWaves = 2 * kWavesB, kThreads = 64 * kWaves;
   static constexpr int kTileA = 64 * kFA, kTileB = 32 * kWavesB * kFB;  // rows of A and of B
-  static constexpr int kPerCu = kFA * kFB * kWavesB > 8 ? 1 : 2;        // workgroups that fit a CU's LDS
+  static constexpr int kPerCu = kFA * kFB * kWavesB * kBufs > 16 ? 1 : 2;  // workgroups that fit a CU's LDS
 };
-template <int kFA, int kFB, int kWavesB, bool kWords, bool kBf16Out>
-__global__ __launch_bounds__(128 * kWavesB, (kFA * kFB * kWavesB > 8 ? 1 : 2) * kWavesB / 2) void
+template <int kFA, int kFB, int kWavesB, int kBufs, bool kWords, bool kBf16Out>
+__global__ __launch_bounds__(128 * kWavesB, (kFA * kFB * kWavesB * kBufs > 16 ? 1 : 2) * kWavesB / 2) void
 mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
-  using Shape = TileShape<kFA, kFB, kWavesB>;
+  static_assert(kBufs == 2 || (kBufs == 4 && kWords), "exponents in registers are waited for with everything else");
+  using Shape = TileShape<kFA, kFB, kWavesB, kBufs>;
   constexpr int kWaves = Shape::kWaves, kTileA = Shape::kTileA, kTileB = Shape::kTileB;
   constexpr int kStage = (kTileA + kTileB) * kRowBytes;     // A's rows, then B's
   constexpr int kLoadsA = kTileA / 8 / kWaves, kLoadsB = kTileB / 8 / kWaves;  // wave-wide loads per stage: 8 rows each
@@ -298,7 +300,10 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   constexpr int kSpan = (kTileA + kTileB) * kSpanBytes;
   constexpr int kSpanLoads = (kTileA + kTileB) / 32;        // 32 rows each
   constexpr int kSpanPerWave = kSpanLoads / kWaves;         // of a span, one a stage
-  __shared__ __attribute__((aligned(16))) char s_tile[2 * kStage + (kWords ? 2 * kSpan : 0)];
+  // spans are loaded one span ahead into the other of two buffers; with more
+  // stages on their way than the waits ask for, two ahead into four
+  constexpr int kSpanBufs = kBufs, kSpansAhead = kBufs / 2;
+  __shared__ __attribute__((aligned(16))) char s_tile[kBufs * kStage + (kWords ? kSpanBufs * kSpan : 0)];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -361,7 +366,7 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   auto issue = [&](auto slow, int s, uint32_t past, int l) {
     const bool of_b = l & 1;
     const int i = l >> 1;
-    const uint32_t at = lds0 + (s & 1) * kStage + (of_b ? kTileA * kRowBytes : 0) + 8 * (kMostLoads * wave + i) * kRowBytes;
+    const uint32_t at = lds0 + (s & (kBufs - 1)) * kStage + (of_b ? kTileA * kRowBytes : 0) + 8 * (kMostLoads * wave + i) * kRowBytes;
     lds_load16<decltype(slow)::value>(of_b ? tile.b : tile.a, at, voff[i] | ((past << (31 - i)) & 0x80000000u),
                                       (uint32_t)(s * kRowBytes));
   };
@@ -385,7 +390,7 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
     i32x4 rs;
 #pragma unroll
     for (int w = 0; w < 4; ++w) rs[w] = of_b ? tile.eb[w] : tile.ea[w];
-    lds_load16<decltype(slow)::value>(rs, lds0 + 2 * kStage + (c & 1) * kSpan + r * kSpanBytes, at | none, 0);
+    lds_load16<decltype(slow)::value>(rs, lds0 + kBufs * kStage + (c & (kSpanBufs - 1)) * kSpan + r * kSpanBytes, at | none, 0);
   };
   // The exponents of stage s: from LDS, or (rows that start anywhere) asked for
   // in memory one stage ahead; a word that would pass the last row's end is
@@ -396,7 +401,7 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   };
   auto exponents_of = [&](const uint8_t* e, int64_t row) { return e + row * a.blocks; };
   auto exponents = [&](int s, uint32_t (&xa)[kFA], uint32_t (&xb)[kFB]) {
-    const char* t = s_tile + 2 * kStage + ((s >> 2) & 1) * kSpan + (s & 3) * kStageBlocks + 4 * half;
+    const char* t = s_tile + kBufs * kStage + ((s >> 2) & (kSpanBufs - 1)) * kSpan + (s & 3) * kStageBlocks + 4 * half;
 #pragma unroll
     for (int i = 0; i < kFA; ++i)
       xa[i] = kWords ? *reinterpret_cast<const uint32_t*>(t + (wm + 32 * i + lrow) * kSpanBytes)
@@ -426,7 +431,7 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   // Read n of a step's operands, in the order in which they are needed.
   constexpr int kReads = kFA + kFB;
   auto read = [&](int s, int j, int n) {
-    const char* t = s_tile + (s & 1) * kStage;
+    const char* t = s_tile + (s & (kBufs - 1)) * kStage;
     const bool of_b = n != 1 && n <= kFB;
     const int i = n == 0 || n == 1 ? 0 : of_b ? n - 1 : n - kFB;
     u32x4& to = of_b ? fb[j & 1][i] : fa[j & 1][i];
@@ -458,25 +463,27 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   };
   using std::integral_constant;
 
-  // A tile's first loads: its first stage and the first span of exponents.
-  constexpr int kFirst = kLoads + (kWords ? kSpanPerWave : 0);
+  // A tile's first loads: all stages but one of the buffers, and the first spans
+  // of exponents.
+  constexpr int kFirstStages = (kBufs - 1) * kLoads;
+  constexpr int kFirst = kFirstStages + (kWords ? kSpansAhead * kSpanPerWave : 0);
   auto start = [&](int l) {
-    if (l < kLoads)
-      issue(std::true_type{}, 0, past(0), l);
+    if (l < kFirstStages)
+      issue(std::true_type{}, l / kLoads, past(l / kLoads), l % kLoads);
     else
-      issue_span(std::true_type{}, 0, l - kLoads);
+      issue_span(std::true_type{}, (l - kFirstStages) / kSpanPerWave, (l - kFirstStages) % kSpanPerWave);
   };
 
-  // The results of a wave leave through a patch of LDS (in the second stage's
+  // The results of a wave leave through a patch of LDS (in the last buffer's
   // place), 32 rows of 128 bytes at a time, two blocks in turn: 16-byte chunk c
   // of row r at c ^ swz(r), the halves of a chunk swapped for rows with bit 4.
   constexpr int kPer = kBf16Out ? 8 : 4;               // columns per chunk
   constexpr int kPartsB = 32 * kFB / (8 * kPer);       // runs of columns
   constexpr int kPieces = kPartsB * kFA;               // of 32 rows x 128 bytes
   static_assert(kStage / kWaves >= 2 * 32 * 128, "two pieces fit");
-  char* patch = s_tile + kStage + wave * (kStage / kWaves);
-  constexpr int kPerPiece = 8;  // the next tile's first loads that go out with each piece
-  static_assert(kFirst <= kPerPiece * kPieces, "all go out");
+  char* patch = s_tile + (kBufs - 1) * kStage + wave * (kStage / kWaves);
+  // the next tile's first loads that go out with each piece
+  constexpr int kPerPiece = std::max(8, (kFirst + kPieces - 1) / kPieces);
 
 #pragma unroll
   for (int l = 0; l < kFirst; ++l) start(l);
@@ -500,25 +507,27 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
         finish_exponents(0, sa, sb);
       }
 #pragma unroll
-      for (int l = 0; l < kLoads / 2; ++l) issue(std::true_type{}, 1, past(1), l);
+      for (int l = 0; l < kLoads / 2; ++l) issue(std::true_type{}, kBufs - 1, past(kBufs - 1), l);
 #pragma unroll
       for (int n = 0; n < kReads; ++n) read(0, 0, n);
 #pragma unroll 1
       for (int s = 0; s < stages; ++s) {
         if (!kWords) exponents(s + 1, sa_next, sb_next);
         __builtin_amdgcn_sched_barrier(0);
-        const uint32_t past1 = past(s + 1), past2 = past(s + 2);
+        const uint32_t past1 = past(s + kBufs - 1), past2 = past(s + kBufs);
         step(integral_constant<int, 0>{}, [&](int t) {
           spread(t, kReads, 0, [&](int n) { read(s, 1, n); });
-          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + 1, past1, kLoads / 2 + l); });
+          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs - 1, past1, kLoads / 2 + l); });
         });
         step(integral_constant<int, 1>{}, [&](int t) {
           spread(t, kReads, 0, [&](int n) { read(s, 2, n); });
           if (kWords && t == kSlots / 2)  // with fewer than four a span, some are loaded twice
-            issue_span(std::false_type{}, (s >> 2) + 1, s & (kSpanPerWave - 1));
+            issue_span(std::false_type{}, (s >> 2) + kSpansAhead, s & (kSpanPerWave - 1));
         });
         step(integral_constant<int, 2>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(s, 3, n); }); });
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+        // with four buffers the loads of two later stages, and the exponents
+        // loaded meanwhile, may be on their way
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(kBufs == 2 ? 0 : (kBufs - 2) * kLoads + kBufs - 1) : "memory");
         if (!kWords) {
           // the exponents are used here, so that the compiler's own wait for
           // them comes before the next loads and not after
@@ -533,7 +542,7 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
         __builtin_amdgcn_sched_barrier(0);
         step(integral_constant<int, 3>{}, [&](int t) {
           spread(t, kReads, 0, [&](int n) { read(s + 1, 0, n); });
-          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + 2, past2, l); });
+          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs, past2, l); });
         });
         if (kWords) finish_exponents(s + 1, sa_next, sb_next);
 #pragma unroll
@@ -631,18 +640,21 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // nothing writes LDS after the workgroup's end
 }
 
-template <int kFA, int kFB, int kWavesB>
+template <int kFA, int kFB, int kWavesB, int kBufs>
 void launch_tile(GemmArgs a, bool bf16, int cus, hipStream_t stream) {
-  using Shape = TileShape<kFA, kFB, kWavesB>;
+  using Shape = TileShape<kFA, kFB, kWavesB, kBufs>;
   a.tiles_m = (int)((a.M + Shape::kTileA - 1) / Shape::kTileA);
   a.tiles_n = (int)((a.N + Shape::kTileB - 1) / Shape::kTileB);
   const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
   const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * Shape::kPerCu)), block(Shape::kThreads);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, per_xcd); };
-  if (words(a))
-    bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, true, true>) : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, true, false>);
-  else
-    bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, false, true>) : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, false, false>);
+  if (words(a)) {
+    bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, kBufs, true, true>)
+         : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, kBufs, true, false>);
+  } else if constexpr (kBufs == 2) {
+    bf16 ? go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, kBufs, false, true>)
+         : go(mx_gemm_tile_kernel<kFA, kFB, kWavesB, kBufs, false, false>);
+  }
 }
 
 // ---- few tiles: every wave its own slice of K ----
@@ -844,8 +856,9 @@ void launch_stream(GemmArgs a, bool bf16, hipStream_t stream) {
 //     us, tiles of 128 15.1); up to 32 rows of more columns than that, the
 //     stream (32 x 22016: 17.5 us, slices 18.5);
 //   * tiles of 128 or of 256 by their rounds: one of 256 x 256 tiles takes 27 us,
-//     one of 128 x 128 24 us (15 us when every CU has one of them: 512 x 22016:
-//     35 us and 47 us, 2048 x 4096: 28 us and 24 us);
+//     one of 128 x 128 24 us, or 15 us when no CU has two of them (512 x 22016:
+//     35 us and 47 us, 2048 x 4096: 27 us and 23 us), and then with four buffers
+//     (1024 x 4096: 14.5 us, with two 16.5; 512 x 4096 x 11008: 27 and 35 us);
 //   * without words, the stream in place of the slices (256 x 4096 x 1376: 7.3
 //     us, tiles of 128 9.1; 512 x 4096 x 1376: 12.7 and 9.4 us).
 void pick_and_launch(const GemmArgs& a, bool bf16, int cus, hipStream_t stream) {
@@ -867,9 +880,11 @@ void pick_and_launch(const GemmArgs& a, bool bf16, int cus, hipStream_t stream) 
   const int64_t small = tiles(128, 128), large = tiles(256, 256);
   const int64_t cost_small = small <= cus ? 15 : 24 * ((small + 2 * cus - 1) / (2 * cus));
   if (27 * ((large + cus - 1) / cus) <= cost_small)
-    launch_tile<4, 4, 2>(a, bf16, cus, stream);
+    launch_tile<4, 4, 2, 2>(a, bf16, cus, stream);
+  else if (small <= cus && words(a))
+    launch_tile<2, 2, 2, 4>(a, bf16, cus, stream);
   else
-    launch_tile<2, 2, 2>(a, bf16, cus, stream);
+    launch_tile<2, 2, 2, 2>(a, bf16, cus, stream);
 }
 
 }  // namespace

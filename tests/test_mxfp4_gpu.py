@@ -174,6 +174,7 @@ GEMM_SHAPES = [(1, 1, 32), (1, 16, 32), (1, 17, 64), (1, 4096, 4096), (1, 1000, 
                (300, 1001, 1376), (513, 511, 1056), (512, 768, 224), (777, 1001, 1376), (1024, 1024, 1024),
                (1030, 2060, 544), (4400, 4352, 128), (4352, 4400, 1152), (4360, 4352, 2144), (5000, 4096, 32), (200, 129, 32), (33, 1024, 4096),
                (60, 2000, 896), (64, 4096, 1408), (120, 4000, 1152), (250, 4000, 640), (20, 9000, 256), (300, 3, 32), (5000, 2, 64),
+               (1400, 2000, 128), (1408, 2048, 384), (1400, 2001, 896), (1401, 2000, 1152), (1290, 1290, 2176),
                (2176, 2200, 640), (2048, 300, 96), (3000, 17, 640), (9, 3000, 32), (1500, 2100, 2048)]
 
 
