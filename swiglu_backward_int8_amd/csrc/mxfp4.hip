@@ -29,6 +29,8 @@ namespace {
 
 using namespace rows;
 
+typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
+
 constexpr int kThreads = 256;
 
 // E8M0 byte of a block from its largest magnitude (bf16 bits).
@@ -233,20 +235,22 @@ struct BothArgs {
   int64_t blocks_r;
 };
 
-// A workgroup takes 256 rows x 128 columns, a wave 128 of the rows: lane (b, p) =
+// A workgroup takes 128 kWaves rows x 128 columns, a wave 128 of the rows: lane (b, p) =
 // (lane / 16, lane % 16) holds rows 32 b .. + 31 of columns 8 p .. + 7, so that a
 // load covers 256 bytes of four rows and four neighbouring column blocks leave
 // as 64 contiguous bytes.  The exponents of the columns meet in LDS (stored
 // from the lanes, a byte each in a line of its own, they cost a fifth of the
 // time).  Each XCD takes whole bands of rows, so that the lines that two
 // neighbouring workgroups share are put together in its L2.
-constexpr int kBothWaves = 2, kBothCols = 128, kBothRows = 128 * kBothWaves;
+constexpr int kBothCols = 128;
 
-template <Kind kKind>
-__global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const BothArgs a, int64_t tiles, int64_t per_xcd,
+template <Kind kKind, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void mx_quant_both_kernel(const BothArgs a, int64_t tiles, int64_t per_xcd,
                                                                         int tiles_k) {
-  static_assert(4 * kBothWaves == 8 && 64 * kBothWaves == kBothCols, "a thread stores a column's eight exponents");
-  __shared__ __attribute__((aligned(16))) uint8_t s_exp[kBothCols][4 * kBothWaves];
+  // a column's exponents of one band, stored by one thread
+  using Exps = std::conditional_t<kWaves == 4, u32x4_a1, u32x2_a1>;
+  static_assert(sizeof(Exps) == 4 * kWaves && 64 * kWaves >= kBothCols, "a thread per column");
+  __shared__ __attribute__((aligned(16))) uint8_t s_exp[kBothCols][4 * kWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blk = lane >> 4, col_in = 8 * (lane & 15);
@@ -256,7 +260,7 @@ __global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const Bo
     const int64_t band = tile / tiles_k;
     const int col0 = (int)(tile - band * tiles_k) * kBothCols, col = col0 + col_in, n = a.K - col;
     const bool in_block = col < 32 * a.blocks_k;  // the same for four neighbouring lanes
-    const int64_t br = band * (4 * kBothWaves) + 4 * wave + blk, r0 = 32 * br;
+    const int64_t br = band * (4 * kWaves) + 4 * wave + blk, r0 = 32 * br;
     const int rows_here = (int)(a.R - r0 < 32 ? (a.R - r0 > 0 ? a.R - r0 : 0) : 32);
     // rows past the last are read as the last and then taken for zeros: a branch
     // for each row would load them one by one
@@ -292,6 +296,10 @@ __global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const Bo
         if (kKind == kFull || (in_block && r < rows_here)) a.s[(r0 + r) * a.blocks_k + (col >> 5)] = (uint8_t)keep;
       }
     }
+    // without this the magnitudes that the rows' maxima took would be kept for
+    // the columns', in as many registers as x has (a wave per SIMD instead of three)
+#pragma unroll
+    for (int r = 0; r < 32; ++r) asm volatile("" : "+v"(x[r].w[0]), "+v"(x[r].w[1]), "+v"(x[r].w[2]), "+v"(x[r].w[3]));
 #pragma unroll
     for (int h = 0; h < 4; ++h) {  // columns 2h and 2h + 1 of the lane
       uint32_t m = x[0].w[h] & 0x7fff7fffu;
@@ -319,13 +327,13 @@ __global__ __launch_bounds__(64 * kBothWaves) void mx_quant_both_kernel(const Bo
       }
     }
     __syncthreads();
-    // 8 exponents of a column in one store where the band has them all
+    // all of a column in one store where the band is whole
     const int c = threadIdx.x & (kBothCols - 1);
-    const int64_t br0 = band * (4 * kBothWaves);
-    if (col0 + c < a.K) {
+    const int64_t br0 = band * (4 * kWaves);
+    if (threadIdx.x < kBothCols && col0 + c < a.K) {
       uint8_t* to = a.s_t + (int64_t)(col0 + c) * a.blocks_r + br0;
-      if (kKind == kFull || a.blocks_r - br0 >= 4 * kBothWaves) {
-        *reinterpret_cast<u32x2_a1*>(to) = *reinterpret_cast<const u32x2*>(s_exp[c]);
+      if (kKind == kFull || a.blocks_r - br0 >= 4 * kWaves) {
+        *reinterpret_cast<Exps*>(to) = *reinterpret_cast<const Exps*>(s_exp[c]);
       } else {
         for (int k = 0; k < (int)(a.blocks_r - br0); ++k) to[k] = s_exp[c][k];
       }
@@ -358,17 +366,27 @@ __attribute__((visibility("default"))) int mxfp4_quant(const void* x, void* q, v
     launch_walk(MxQuantRows{xb, qb, sb, K, bk}, R, K, 32, stream);
   } else {
     const BothArgs a = {xb, qb, sb, static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(s_t), R, (int)K, (int)bk, br};
-    const int64_t tiles_k = (K + kBothCols - 1) / kBothCols, tiles = (R + kBothRows - 1) / kBothRows * tiles_k;
-    const int64_t per_xcd = (tiles + 7) / 8;
-    const dim3 grid((unsigned)(8 * std::min<int64_t>(per_xcd, 1 << 19)));
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(64 * kBothWaves), 0, stream, a, tiles, per_xcd, (int)tiles_k);
+    // bands of 512 rows where they still give every CU a workgroup (8192 x 4096:
+    // 22.0 us, of 256 rows 23.8), of 256 rows otherwise (2048 x 4096: 9.8 us, of 512 10.6)
+    const int64_t tiles_k = (K + kBothCols - 1) / kBothCols;
+    auto launch = [&](auto waves) {
+      constexpr int kWaves = decltype(waves)::value;
+      const int64_t tiles = (R + 128 * kWaves - 1) / (128 * kWaves) * tiles_k, per_xcd = (tiles + 7) / 8;
+      const dim3 grid((unsigned)(8 * std::min<int64_t>(per_xcd, 1 << 19)));
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, stream, a, tiles, per_xcd, (int)tiles_k);
+      };
+      if (K % kBothCols == 0 && R % (128 * kWaves) == 0)
+        go(mx_quant_both_kernel<kFull, kWaves>);
+      else if (K % 8 == 0)
+        go(mx_quant_both_kernel<kWhole, kWaves>);
+      else
+        K > 8 ? go(mx_quant_both_kernel<kRagged, kWaves>) : go(mx_quant_both_kernel<kTiny, kWaves>);
     };
-    if (K % kBothCols == 0 && R % kBothRows == 0)
-      go(mx_quant_both_kernel<kFull>);
+    if ((R + 511) / 512 * tiles_k >= 256)
+      launch(std::integral_constant<int, 4>{});
     else
-      K % 8 == 0 ? go(mx_quant_both_kernel<kWhole>)
-                 : K > 8 ? go(mx_quant_both_kernel<kRagged>) : go(mx_quant_both_kernel<kTiny>);
+      launch(std::integral_constant<int, 2>{});
   }
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }

@@ -117,6 +117,9 @@ def test_quant_of_many_blocks():
     check_quant(quant(x), x)
     x = values(4500, 1001, 4)
     check_quant(quant(x), x)
+    for R, K in ((8200, 2048), (8192, 2048), (8195, 2050), (40000, 100), (40001, 5)):  # the wider bands
+        x = values(R, K, R + K)
+        check_quant(quant(x, cols=True), x)
 
 
 def test_quant_blocks_that_are_not_finite():
