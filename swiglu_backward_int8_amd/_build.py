@@ -16,6 +16,8 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -46,15 +48,23 @@ def build(verbose: bool = False) -> str:
 
     sigmoid_table.write(os.path.join(GEN, "sigmoid_table.inc"))
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I" + INCLUDE, "-I" + GEN] + SRCS + ["-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
     # the host pass does not know the packed-fp32 feature and says so; harmless
     noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)
-    if r.returncode != 0:
-        raise RuntimeError("hipcc failed (%d):\n%s" % (r.returncode, err))
-    if verbose and err.strip():
-        print(err)
+
+    def run(cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)
+        if r.returncode != 0:
+            raise RuntimeError("hipcc failed (%d):\n%s" % (r.returncode, err))
+        if verbose and err.strip():
+            print(err)
+
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in SRCS]
+        flags = [f for f in HIPCC_FLAGS if f != "-shared"] + ["-I" + INCLUDE, "-I" + GEN, "-c"]
+        with ThreadPoolExecutor(len(SRCS)) as pool:  # one compiler process per source
+            list(pool.map(run, [[hipcc()] + flags + [s, "-o", o] for s, o in zip(SRCS, objs)]))
+        run([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC"] + objs + ["-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 
@@ -63,7 +73,6 @@ def device_asm(src: str) -> str:
     """gfx950 assembly of one HIP source, compiled with the library's flags
     (for checks of the generated instructions)."""
     from swiglu_backward_int8_amd import sigmoid_table
-    import tempfile
 
     sigmoid_table.write(os.path.join(GEN, "sigmoid_table.inc"))
     flags = [f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")]

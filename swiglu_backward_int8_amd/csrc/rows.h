@@ -63,8 +63,13 @@ __device__ __forceinline__ Piece shifted(Piece v, int d) {
 template <Kind kKind, bool kNt>
 __device__ __forceinline__ Piece load_bf16(const uint16_t* p, int n) {
   auto at = [](const uint16_t* q) {
-    const u32x4_a2* v = reinterpret_cast<const u32x4_a2*>(q);
-    return piece_of(kNt ? __builtin_nontemporal_load(v) : *v);
+    const u32x4_a2* from = reinterpret_cast<const u32x4_a2*>(q);
+    u32x4 v;
+    if (kNt)
+      v = __builtin_nontemporal_load(from);
+    else
+      v = *from;
+    return piece_of(v);
   };
   if (kKind == kFull) return at(p);
   if (kKind == kWhole) return n > 0 ? at(p) : zero_piece();
