@@ -381,11 +381,12 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
     if ((stages - 1) * kStageBlocks + 4 * half + j < a.blocks) keep_last |= 0xffu << (8 * j);
   uint32_t sa[kFA], sb[kFB], sa_next[kFA], sb_next[kFB];
   // Load p (one of kSpanPerWave) of this wave of exponent span c: 32 rows, two
-  // lanes to a row; spans past K are not read.
+  // lanes to a row, which change places in every other eight rows, so that the
+  // words read below fall on twice as many banks; spans past K are not read.
   auto issue_span = [&](auto slow, int c, int p) {
     const int r = 32 * (kWaves * p + wave);  // of A's and B's rows in turn
     const bool of_b = r >= kTileA;
-    const uint32_t at = (uint32_t)((r - (of_b ? kTileA : 0) + (lane >> 1)) * a.blocks + kSpanBytes * c + 16 * (lane & 1));
+    const uint32_t at = (uint32_t)((r - (of_b ? kTileA : 0) + (lane >> 1)) * a.blocks + kSpanBytes * c + 16 * ((lane ^ (lane >> 4)) & 1));
     const uint32_t none = 4 * c < stages ? 0u : 0x80000000u;
     i32x4 rs;
 #pragma unroll
@@ -401,7 +402,7 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
   };
   auto exponents_of = [&](const uint8_t* e, int64_t row) { return e + row * a.blocks; };
   auto exponents = [&](int s, uint32_t (&xa)[kFA], uint32_t (&xb)[kFB]) {
-    const char* t = s_tile + kBufs * kStage + ((s >> 2) & (kSpanBufs - 1)) * kSpan + (s & 3) * kStageBlocks + 4 * half;
+    const char* t = s_tile + kBufs * kStage + ((s >> 2) & (kSpanBufs - 1)) * kSpan + ((8 * (s & 3)) ^ (2 * (lrow & 8))) + 4 * half;
 #pragma unroll
     for (int i = 0; i < kFA; ++i)
       xa[i] = kWords ? *reinterpret_cast<const uint32_t*>(t + (wm + 32 * i + lrow) * kSpanBytes)
