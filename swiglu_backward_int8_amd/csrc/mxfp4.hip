@@ -16,6 +16,10 @@
 // lane.  Quantising both axes reads x once: a lane holds 32 rows of eight
 // columns in registers, so that a column's block lies inside the lane (no
 // transpose through LDS) and a row's block inside four neighbouring lanes.
+// Measured: rows of 16384 x 11008 71 us (6.4 TB/s), dequantised 22016 x 4096 39 us
+// (5.9 TB/s); both axes of 8192 x 4096 22 us (4.7 TB/s), of 16384 x 11008 114 us
+// (4.85 TB/s): what is missing there is the columns' stores, pieces of 64 bytes
+// of lines that a workgroup fills over four waves.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -107,7 +107,8 @@ __device__ __forceinline__ void store_chunk(void* C, int64_t at, const u32x4& v,
 // A workgroup owns 16 kM rows of A by 16 kN rows of B; its kW waves split K in
 // chunks of 16 blocks (512 values) and their sums meet in LDS.  Nothing is
 // shared between waves, so nothing waits: the weight streams through once.
-// Rows past M or N are read as the last row and not stored.
+// Rows past M or N are read as the last row and not stored.  Bound by memory: 1 x
+// 22016 x 4096 takes 11 us for 48 MB (4.4 TB/s, the launch included).
 constexpr int kChunkBlocks = 16;
 
 struct Frag {
@@ -210,10 +211,20 @@ __global__ __launch_bounds__(64 * kW) void mx_gemm_stream_kernel(const GemmArgs 
 // A workgroup owns a tile of kTileA x kTileB results, its waves (2 x kWavesB)
 // kFA x kFB blocks of 32 x 32 each.  A stage is 256 values (8 blocks, 128
 // bytes) of every row of the tile: the codes go from memory straight into LDS
-// (buffer loads with the lds flag), double buffered, the exponents into
-// registers.  Rows of 128 bytes lie in LDS as eight 16-byte chunks, chunk c of
-// row r at c ^ swz(r), so that the 16 lanes that read a chunk of consecutive
-// rows fall on distinct banks.
+// (buffer loads with the lds flag), double buffered.  Rows of 128 bytes lie in
+// LDS as eight 16-byte chunks, chunk c of row r at c ^ swz(r), so that the 16
+// lanes that read a chunk of consecutive rows fall on distinct banks.
+//
+// Bound by the matrix cores' power: multiplying random codes from registers
+// alone, nothing else running, they reach 6.6 PFLOP/s at a lowered clock (9.4
+// with zeros).  256 x 256 tiles of 128 x 128 per wave, the most that fits the
+// registers, read LDS for half of the cycles and L2 for a third.  16384 x 4096 x
+// 11008: 311 us, 4.75 PFLOP/s; 16384 x 22016 x 4096: 690 to 720 us, 4.1 to 4.3.
+// A stage of 2048 matrix cycles takes 2900; a tile's end (results out through
+// LDS, next tile's start) as long as three stages, most of it the stores' way to
+// memory.  Loads not spread over two steps, larger or smaller rasters, eight
+// waves of 128 x 64, counted waits that let stores run into the next tile, and
+// workgroups started out of step all measured slower or the same.
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -665,7 +676,8 @@ void launch_tile(GemmArgs a, bool bf16, int cus, hipStream_t stream) {
 // 32 kFB results; its four waves take its stages (256 values, as above) in turn,
 // each through a ring of kDepth stages of LDS that is its own: a wave waits for
 // nothing but its own oldest loads, and 100 KB or more are on their way to
-// every CU.  The four sums meet in LDS at the end.
+// every CU.  The four sums meet in LDS at the end.  64 x 4096 x 11008: 9.2 us for
+// 25 MB, of which the launch and the two ends of the pipeline are about half.
 constexpr int kSliceWaves = 4;
 
 template <int kFA, int kFB, int kDepth, bool kBf16Out>
