@@ -616,19 +616,30 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
       for (int l = kPerPiece * t; l < kPerPiece * (t + 1); ++l)
         if (l < kFirst) start(l);
     };
+    // Whole lines are streamed: left in L2, a round's results (4 MB an XCD) drive
+    // out the operands (16384 x 22016 x 4096: 785 us, streamed 692).  Rows that
+    // start inside lines are not: their lines have to meet in L2 (10308 x 10558 x
+    // 384, fp32: streamed 384 us, else 221; rows of whole lines 94).
+    const bool streamed = ((reinterpret_cast<uintptr_t>(a.C) | (uintptr_t)(a.N * (16 / kPer))) & 63) == 0;
     if (whole) {
 #pragma unroll
       for (int t = 0; t < kPieces + 2; ++t) {
         loads(t);
         if (t < kPieces) put(t);
         if (t >= 2) {
+          auto at = [&](int x) {
+            return reinterpret_cast<u32x4_a2*>(to0 + (32 * ((t - 2) % kFA) + 8 * x) * a.N * (16 / kPer) +
+                                               128 * ((t - 2) / kFA));
+          };
+          if (streamed) {  // the two notes keep these stores from being merged into plain ones
+            asm volatile("; streamed");
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            // streamed: left in L2, a round's results (4 MB an XCD) drive out the
-            // operands (16384 x 22016 x 4096: 806 us, streamed 728 us)
-            __builtin_nontemporal_store(
-                out[t & 1][x], reinterpret_cast<u32x4_a2*>(to0 + (32 * ((t - 2) % kFA) + 8 * x) * a.N * (16 / kPer) +
-                                                           128 * ((t - 2) / kFA)));
+            for (int x = 0; x < 4; ++x) __builtin_nontemporal_store(out[t & 1][x], at(x));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) *at(x) = out[t & 1][x];
+            asm volatile("; cached");
+          }
         }
         if (t >= 1 && t <= kPieces) get(t - 1);
         __builtin_amdgcn_sched_barrier(0);
