@@ -17,9 +17,10 @@
 // columns in registers, so that a column's block lies inside the lane (no
 // transpose through LDS) and a row's block inside four neighbouring lanes.
 // Measured: rows of 16384 x 11008 71 us (6.4 TB/s), dequantised 22016 x 4096 39 us
-// (5.9 TB/s); both axes of 8192 x 4096 22 us (4.7 TB/s), of 16384 x 11008 114 us
-// (4.85 TB/s): what is missing there is the columns' stores, pieces of 64 bytes
-// of lines that a workgroup fills over four waves.
+// (5.9 TB/s); both axes of 8192 x 4096 20 us (5.1 TB/s), of 16384 x 11008 103 us
+// (5.4 TB/s), of which reading and computing alone take 15 and 62: with all of a
+// tile's rows in registers a wave's loads and stores do not overlap.  Rows that
+// are not whole lines cost more (8192 x 4104: 29 us), in x and in the codes.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -231,6 +232,8 @@ struct GroupDequant {
 
 // ---- both axes in one read ----
 
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
+
 struct BothArgs {
   const uint16_t* x;
   uint8_t *q, *s, *q_t, *s_t;  // q and s may be null together: columns only
@@ -239,50 +242,94 @@ struct BothArgs {
   int64_t blocks_r;
 };
 
-// A workgroup takes 128 kWaves rows x 128 columns, a wave 128 of the rows: lane (b, p) =
-// (lane / 16, lane % 16) holds rows 32 b .. + 31 of columns 8 p .. + 7, so that a
-// load covers 256 bytes of four rows and four neighbouring column blocks leave
-// as 64 contiguous bytes.  The exponents of the columns meet in LDS (stored
-// from the lanes, a byte each in a line of its own, they cost a fifth of the
-// time).  Each XCD takes whole bands of rows, so that the lines that two
-// neighbouring workgroups share are put together in its L2.
-constexpr int kBothCols = 128;
-
-template <Kind kKind, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void mx_quant_both_kernel(const BothArgs a, int64_t tiles, int64_t per_xcd,
-                                                                        int tiles_k) {
-  // a column's exponents of one band, stored by one thread
-  using Exps = std::conditional_t<kWaves == 4, u32x4_a1, u32x2_a1>;
-  static_assert(sizeof(Exps) == 4 * kWaves && 64 * kWaves >= kBothCols, "a thread per column");
-  __shared__ __attribute__((aligned(16))) uint8_t s_exp[kBothCols][4 * kWaves];
+// A wave takes 128 rows x 128 columns, a workgroup kSide x kSide of those: lane
+// (b, p) = (lane / 16, lane % 16) holds rows 32 b .. + 31 of columns 8 p .. + 7,
+// so that a load covers 256 bytes of four rows and four neighbouring column
+// blocks leave as 64 contiguous bytes.  Two waves side by side and two below
+// each other write whole 128-byte lines of both kinds of codes (16384 x 11008:
+// 103 us; four below each other 109, side by side 112).  The exponents meet in
+// LDS, from where a thread stores all that a tile has of a column or of a row
+// (stored from the lanes, a byte each, the columns' cost a fifth of the time and
+// the rows' another 5 us).  Each XCD takes whole bands of rows, so that the lines
+// that two neighbouring workgroups share are put together in its L2.
+//
+// Tiles inside the tensor need no care for its edges; kEdge is the kind of those
+// that reach past its rows or columns (kFull: there are none).
+template <Kind kEdge, int kSide>
+__global__ __launch_bounds__(64 * kSide * kSide) void mx_quant_both_kernel(const BothArgs a, int64_t tiles,
+                                                                           int64_t per_xcd, int tiles_k) {
+  constexpr int kThreads = 64 * kSide * kSide, kRows = 128 * kSide, kCols = 128 * kSide, kBlocks = 4 * kSide;
+  // exponents of a tile: a column's and a row's
+  using Exps = std::conditional_t<kSide == 2, u32x2_a1, u32_a1>;
+  static_assert(sizeof(Exps) == kBlocks, "one store");
+  __shared__ __attribute__((aligned(16))) uint8_t s_col[kCols][kBlocks], s_row[kRows][kBlocks];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int blk = lane >> 4, col_in = 8 * (lane & 15);
-  for (int64_t i = blockIdx.x >> 3; i < per_xcd; i += gridDim.x >> 3) {
-    const int64_t tile = (blockIdx.x & 7) * per_xcd + i;
-    if (tile >= tiles) break;
-    const int64_t band = tile / tiles_k;
-    const int col0 = (int)(tile - band * tiles_k) * kBothCols, col = col0 + col_in, n = a.K - col;
+  const int blk = 4 * (wave / kSide) + (lane >> 4), col_in = 128 * (wave % kSide) + 8 * (lane & 15);
+
+  // the wave's part of the tile at (row0, col0)
+  auto part = [&](auto kind, int64_t row0, int col0) {
+    constexpr Kind kKind = decltype(kind)::value;
+    // streamed where rows are whole pieces; other rows share pieces of lines,
+    // which have to stay in L2 (3000 x 4100: 21 us streamed, 16 cached; 8192 x
+    // 4096: 20 us and 25)
+    constexpr bool kNt = kEdge <= kWhole;
+    const int col = col0 + col_in, n = a.K - col;
     const bool in_block = col < 32 * a.blocks_k;  // the same for four neighbouring lanes
-    const int64_t br = band * (4 * kWaves) + 4 * wave + blk, r0 = 32 * br;
+    const int64_t r0 = row0 + 32 * blk;
     const int rows_here = (int)(a.R - r0 < 32 ? (a.R - r0 > 0 ? a.R - r0 : 0) : 32);
-    // rows past the last are read as the last and then taken for zeros: a branch
-    // for each row would load them one by one
     Piece x[32];
     const uint16_t* from = a.x + r0 * a.K + col;
-    if (kKind == kFull || (rows_here > 0 && (kKind != kWhole || n > 0))) {
+    if (kKind == kFull) {
 #pragma unroll
-      for (int r = 0; r < 32; ++r)
-        x[r] = load_bf16<kKind == kWhole ? kFull : kKind, true>(from + (kKind == kFull ? r : min(r, rows_here - 1)) * (int64_t)a.K, n);
-      if (kKind != kFull && rows_here < 32) {
+      for (int r = 0; r < 32; ++r) x[r] = load_bf16<kFull, kNt>(from + r * (int64_t)a.K, 8);
+    } else if (kKind == kTiny) {
 #pragma unroll
-        for (int r = 1; r < 32; ++r)
+      for (int r = 0; r < 32; ++r) x[r] = r < rows_here ? load_bf16<kTiny, kNt>(from + r * (int64_t)a.K, n) : zero_piece();
+    } else {
+      // Whole pieces everywhere, and what is not the tensor's is taken out of
+      // them: a branch for each row would load them one by one.  A piece past
+      // the row's columns is read as the row's last one, one that the row's end
+      // cuts runs on into the next row, and a row that has no next one, or is
+      // past the last, is read as the one before it.
+      const int d = n < 8 ? 8 - n : 0;
+      const bool ends = kKind == kRagged && d > 0 && a.R - r0 <= 32;  // in the last row
+      int last = rows_here - 1 - (ends && n > 0);
+      const uint16_t* at = from;
+      if (n <= 0 || last < 0) at -= d;
+      if (rows_here <= 0) at = a.x;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        x[r] = load_bf16<kFull, kNt>(at, 8);
+        if (r < last) at += a.K;
+      }
+      if (kKind == kRagged && row0 + kRows >= a.R) {
+        const int last_row = (int)((a.R - 1) & 31);  // the tensor's last row, in its block
+        Piece end = zero_piece();
+        if (ends && rows_here > 0) end = load_bf16<kRagged, kNt>(from + last_row * (int64_t)a.K, n);
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+          if (r == last_row && ends) x[r] = end;
+      }
+      if (row0 + kRows > a.R) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
           if (r >= rows_here) x[r] = zero_piece();
       }
-    } else {
+      if (col0 + kCols > a.K) {
+        uint32_t keep[4];
 #pragma unroll
-      for (int r = 0; r < 32; ++r) x[r] = zero_piece();
+        for (int k = 0; k < 4; ++k) keep[k] = n > 2 * k + 1 ? ~0u : n == 2 * k + 1 ? 0xffffu : 0u;
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[r].w[k] &= keep[k];
+      }
     }
+    // rows past the last lie past the record count, and lanes past the blocks too
+    const int row_bytes = 16 * a.blocks_k;
+    const auto to_q = __builtin_amdgcn_make_buffer_rsrc(a.q + row0 * row_bytes, 0, (int)(std::min<int64_t>(a.R - row0, kRows) * row_bytes), 0x20000);
+    const uint32_t at_q = (uint32_t)(32 * blk * row_bytes + (col >> 1)) | (in_block ? 0 : 0x80000000u);
     if (a.q) {
 #pragma unroll
       for (int r4 = 0; r4 < 8; ++r4) {
@@ -292,16 +339,17 @@ __global__ __launch_bounds__(64 * kWaves) void mx_quant_both_kernel(const BothAr
           const int r = 4 * r4 + j;
           const uint32_t b = block_exponent(group_amax_bits<false>(x[r], 4));
           const uint32_t c = mx_codes8(x[r], exponent_value(b));
-          if (kKind == kFull || (in_block && r < rows_here))
+          if (kKind == kFull)
             reinterpret_cast<uint32_t*>(a.q)[(r0 + r) * (4 * (int64_t)a.blocks_k) + (col >> 3)] = c;
+          else
+            __builtin_amdgcn_raw_buffer_store_b32(c, to_q, at_q, r * row_bytes, 0);
           keep = (lane & 3) == j ? b : keep;
         }
-        const int r = 4 * r4 + (lane & 3);  // four rows' exponents in one store
-        if (kKind == kFull || (in_block && r < rows_here)) a.s[(r0 + r) * a.blocks_k + (col >> 5)] = (uint8_t)keep;
+        s_row[32 * blk + 4 * r4 + (lane & 3)][col_in >> 5] = (uint8_t)keep;
       }
     }
     // without this the magnitudes that the rows' maxima took would be kept for
-    // the columns', in as many registers as x has (a wave per SIMD instead of three)
+    // the columns', in as many registers as x has (a wave per SIMD instead of two or three)
 #pragma unroll
     for (int r = 0; r < 32; ++r) asm volatile("" : "+v"(x[r].w[0]), "+v"(x[r].w[1]), "+v"(x[r].w[2]), "+v"(x[r].w[3]));
 #pragma unroll
@@ -326,21 +374,39 @@ __global__ __launch_bounds__(64 * kWaves) void mx_quant_both_kernel(const BothAr
         }
         const int c = 2 * h + half;
         if (kKind == kFull || (c < n && rows_here > 0))
-          *reinterpret_cast<u32x4*>(a.q_t + ((int64_t)(col + c) * a.blocks_r + br) * 16) = codes;
-        s_exp[col_in + c][4 * wave + blk] = (uint8_t)b;
+          *reinterpret_cast<u32x4*>(a.q_t + ((int64_t)(col + c) * a.blocks_r + (row0 >> 5) + blk) * 16) = codes;
+        s_col[col_in + c][blk] = (uint8_t)b;
       }
     }
+  };
+
+  for (int64_t i = blockIdx.x >> 3; i < per_xcd; i += gridDim.x >> 3) {
+    const int64_t tile = (blockIdx.x & 7) * per_xcd + i;
+    if (tile >= tiles) break;
+    const int64_t band = tile / tiles_k, row0 = band * kRows, rows = a.R - row0;
+    const int col0 = (int)(tile - band * tiles_k) * kCols, cols = a.K - col0;
+    const bool inside = kEdge == kFull || (kEdge != kTiny && rows >= kRows && cols >= kCols);
+    if (inside) {
+      if constexpr (kEdge != kTiny) part(std::integral_constant<Kind, kFull>{}, row0, col0);
+    } else if constexpr (kEdge != kFull) {
+      if (32 * (blk & ~3) < rows && 128 * (wave % kSide) < cols) part(std::integral_constant<Kind, kEdge>{}, row0, col0);
+    }
     __syncthreads();
-    // all of a column in one store where the band is whole
-    const int c = threadIdx.x & (kBothCols - 1);
-    const int64_t br0 = band * (4 * kWaves);
-    if (threadIdx.x < kBothCols && col0 + c < a.K) {
-      uint8_t* to = a.s_t + (int64_t)(col0 + c) * a.blocks_r + br0;
-      if (kKind == kFull || a.blocks_r - br0 >= 4 * kWaves) {
-        *reinterpret_cast<Exps*>(to) = *reinterpret_cast<const Exps*>(s_exp[c]);
+    auto store = [&](uint8_t* to, const uint8_t* from, int64_t n) {
+      if (inside || n >= kBlocks) {
+        *reinterpret_cast<Exps*>(to) = *reinterpret_cast<const Exps*>(from);
       } else {
-        for (int k = 0; k < (int)(a.blocks_r - br0); ++k) to[k] = s_exp[c][k];
+        for (int k = 0; k < (int)n; ++k) to[k] = from[k];
       }
+    };
+#pragma unroll
+    for (int c = threadIdx.x; c < kCols; c += kThreads)
+      if (inside || c < cols)
+        store(a.s_t + (int64_t)(col0 + c) * a.blocks_r + (row0 >> 5), s_col[c], a.blocks_r - (row0 >> 5));
+    if (a.q) {
+#pragma unroll
+      for (int r = threadIdx.x; r < kRows; r += kThreads)
+        if (inside || r < rows) store(a.s + (row0 + r) * a.blocks_k + (col0 >> 5), s_row[r], a.blocks_k - (col0 >> 5));
     }
     __syncthreads();
   }
@@ -370,27 +436,28 @@ __attribute__((visibility("default"))) int mxfp4_quant(const void* x, void* q, v
     launch_walk(MxQuantRows{xb, qb, sb, K, bk}, R, K, 32, stream);
   } else {
     const BothArgs a = {xb, qb, sb, static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(s_t), R, (int)K, (int)bk, br};
-    // bands of 512 rows where they still give every CU a workgroup (8192 x 4096:
-    // 22.0 us, of 256 rows 23.8), of 256 rows otherwise (2048 x 4096: 9.8 us, of 512 10.6)
-    const int64_t tiles_k = (K + kBothCols - 1) / kBothCols;
-    auto launch = [&](auto waves) {
-      constexpr int kWaves = decltype(waves)::value;
-      const int64_t tiles = (R + 128 * kWaves - 1) / (128 * kWaves) * tiles_k, per_xcd = (tiles + 7) / 8;
+    auto launch = [&](auto side) {
+      constexpr int kSide = decltype(side)::value, kTile = 128 * kSide;
+      const int64_t tiles_k = (K + kTile - 1) / kTile;
+      const int64_t tiles = (R + kTile - 1) / kTile * tiles_k, per_xcd = (tiles + 7) / 8;
       const dim3 grid((unsigned)(8 * std::min<int64_t>(per_xcd, 1 << 19)));
       auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, stream, a, tiles, per_xcd, (int)tiles_k);
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * kSide * kSide), 0, stream, a, tiles, per_xcd, (int)tiles_k);
       };
-      if (K % kBothCols == 0 && R % (128 * kWaves) == 0)
-        go(mx_quant_both_kernel<kFull, kWaves>);
+      if (K % kTile == 0 && R % kTile == 0)
+        go(mx_quant_both_kernel<kFull, kSide>);
       else if (K % 8 == 0)
-        go(mx_quant_both_kernel<kWhole, kWaves>);
+        go(mx_quant_both_kernel<kWhole, kSide>);
       else
-        K > 8 ? go(mx_quant_both_kernel<kRagged, kWaves>) : go(mx_quant_both_kernel<kTiny, kWaves>);
+        K > 8 ? go(mx_quant_both_kernel<kRagged, kSide>) : go(mx_quant_both_kernel<kTiny, kSide>);
     };
-    if ((R + 511) / 512 * tiles_k >= 256)
-      launch(std::integral_constant<int, 4>{});
-    else
+    // tiles of 256 x 256 where they give three CUs of four one (3000 x 4096: 13.4
+    // us, of 128 x 128 13.5; 8192 x 4096: 20.1 and 22.1), of 128 x 128 otherwise
+    // (1024 x 4096: 7.9 us, of 256 x 256 9.3)
+    if ((R + 255) / 256 * ((K + 255) / 256) >= 192)
       launch(std::integral_constant<int, 2>{});
+    else
+      launch(std::integral_constant<int, 1>{});
   }
   return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
 }

@@ -219,12 +219,13 @@ __global__ __launch_bounds__(64 * kW) void mx_gemm_stream_kernel(const GemmArgs 
 // alone, nothing else running, they reach 6.6 PFLOP/s at a lowered clock (9.4
 // with zeros).  256 x 256 tiles of 128 x 128 per wave, the most that fits the
 // registers, read LDS for half of the cycles and L2 for a third.  16384 x 4096 x
-// 11008: 311 us, 4.75 PFLOP/s; 16384 x 22016 x 4096: 690 to 720 us, 4.1 to 4.3.
+// 11008: 311 us, 4.75 PFLOP/s; 16384 x 22016 x 4096: 690 to 710 us, 4.2 to 4.3.
 // A stage of 2048 matrix cycles takes 2900; a tile's end (results out through
-// LDS, next tile's start) as long as three stages, most of it the stores' way to
-// memory.  Loads not spread over two steps, larger or smaller rasters, eight
-// waves of 128 x 64, counted waits that let stores run into the next tile, and
-// workgroups started out of step all measured slower or the same.
+// LDS, next tile's start) as long as three stages, half of it the stores' way to
+// memory (without any stores 640 us).  Loads not spread over two steps, larger
+// or smaller rasters, eight waves of 128 x 64, patches outside the buffers, so
+// that the second stage's loads need not follow the stores, and workgroups
+// started out of step all measured slower or the same.
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 

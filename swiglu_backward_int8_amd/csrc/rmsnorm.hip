@@ -19,7 +19,7 @@
 // waves, which saves the barrier, measured slower (16384 x 4096: four waves of
 // two pieces 80 us, one of eight 89 us): the loads of more waves are in flight
 // while others compute.  At 16384 x 4096 the forward pass moves 470 MB in 80 us
-// (5.9 TB/s), the backward pass 537 MB in 89 us (6.0 TB/s) and sums dw in 4 more;
+// (5.9 TB/s), the backward pass 537 MB in 92 us (5.8 TB/s) and sums dw in 5 more;
 // a plain 2 GiB copy reaches 4.8 TB/s here.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

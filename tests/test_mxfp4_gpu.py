@@ -122,6 +122,22 @@ def test_quant_of_many_blocks():
         check_quant(quant(x, cols=True), x)
 
 
+@pytest.mark.parametrize("R,K", [
+    (1, 1), (1, 9), (2, 10), (31, 9), (33, 11), (127, 129), (128, 129), (129, 127), (129, 136), (256, 264), (257, 250),
+    (255, 393), (160, 135), (161, 512), (300, 8), (300, 7),
+    (3329, 3849), (3329, 3848), (3328, 3855), (3297, 3842), (49153, 9), (49153, 5), (6400, 2049), (6401, 2048)])
+def test_quant_of_both_axes_at_the_edges(R, K):
+    # tiles that reach past the rows, the columns or both, in tensors of both
+    # tile sizes; what lies around x is NaN and would show in the exponents
+    print("quant", R, K, flush=True)
+    x = values(R, K, R + K)
+    room = torch.full((R * K + 1040,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    inside = room[520:520 + R * K].view(R, K)
+    inside.copy_(x)
+    for rows in (True, False):
+        check_quant(quant(inside, rows=rows, cols=True), x)
+
+
 def test_quant_blocks_that_are_not_finite():
     x = values(40, 200, 5)
     x[1, 40], x[2, 199], x[3, 0], x[39, 64] = float("inf"), float("nan"), -float("inf"), float("nan")
