@@ -593,9 +593,8 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
     // (10 us for a tile of 256 x 256); out of the patch it is 8 rows of 128.
     // A wave's LDS operations are carried out in their order and its patch is
     // its own, so nothing waits but the stores for what they store.
-    auto put = [&](int piece) {
-      const int i = piece % kFA, part = piece / kFA;
-      char* to = patch + (piece & 1) * 32 * 128 + lrow * 128;
+    auto put = [&](int turn, int i, int part) {
+      char* to = patch + (turn & 1) * 32 * 128 + lrow * 128;
 #pragma unroll
       for (int k = 0; k < kPer / 4; ++k)
 #pragma unroll
@@ -611,12 +610,12 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
     };
     const int r = lane >> 3;
     u32x4 out[2][4];
-    auto get = [&](int piece) {
+    auto get = [&](int turn) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int row = 8 * x + r;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(patch + (piece & 1) * 32 * 128 + row * 128 + 16 * ((lane & 7) ^ swz(row)));
-        out[piece & 1][x] = kBf16Out && x >= 2 ? (u32x4){v.z, v.w, v.x, v.y} : v;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(patch + (turn & 1) * 32 * 128 + row * 128 + 16 * ((lane & 7) ^ swz(row)));
+        out[turn & 1][x] = kBf16Out && x >= 2 ? (u32x4){v.z, v.w, v.x, v.y} : v;
       }
     };
     char* const to0 = static_cast<char*>(a.C) + ((m0 + r) * a.N + n0 + kPer * (lane & 7)) * (16 / kPer);
@@ -628,40 +627,47 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
     // Whole lines are streamed: left in L2, a round's results (4 MB an XCD) drive
     // out the operands (16384 x 22016 x 4096: 785 us, streamed 692).  Rows that
     // start inside lines are not: their lines have to meet in L2 (10308 x 10558 x
-    // 384, fp32: streamed 384 us, else 221; rows of whole lines 94).
-    const bool streamed = ((reinterpret_cast<uintptr_t>(a.C) | (uintptr_t)(a.N * (16 / kPer))) & 63) == 0;
-    if (whole) {
+    // 384, fp32: streamed 384 us, else 221), and soon, so that a row's pieces
+    // follow each other (146 us; rows of whole lines 94).  Whole lines go column
+    // of pieces by column (16384 x 8192 x 4096, fp32: 286 us, by rows 301).
+    auto store_whole = [&](auto streamed) {
+      constexpr bool kStreamed = decltype(streamed)::value;
+      auto row_of = [](int n) { return kStreamed ? n % kFA : n / kPartsB; };
+      auto part_of = [](int n) { return kStreamed ? n / kFA : n % kPartsB; };
 #pragma unroll
       for (int t = 0; t < kPieces + 2; ++t) {
         loads(t);
-        if (t < kPieces) put(t);
+        if (t < kPieces) put(t, row_of(t), part_of(t));
         if (t >= 2) {
           auto at = [&](int x) {
-            return reinterpret_cast<u32x4_a2*>(to0 + (32 * ((t - 2) % kFA) + 8 * x) * a.N * (16 / kPer) +
-                                               128 * ((t - 2) / kFA));
+            return reinterpret_cast<u32x4_a2*>(to0 + (32 * row_of(t - 2) + 8 * x) * a.N * (16 / kPer) + 128 * part_of(t - 2));
           };
-          if (streamed) {  // the two notes keep these stores from being merged into plain ones
-            asm volatile("; streamed");
 #pragma unroll
-            for (int x = 0; x < 4; ++x) __builtin_nontemporal_store(out[t & 1][x], at(x));
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) *at(x) = out[t & 1][x];
-            asm volatile("; cached");
+          for (int x = 0; x < 4; ++x) {
+            if (kStreamed)
+              __builtin_nontemporal_store(out[t & 1][x], at(x));
+            else
+              *at(x) = out[t & 1][x];
           }
         }
         if (t >= 1 && t <= kPieces) get(t - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (kStreamed) asm volatile("; streamed");  // keeps the last stores from being merged with the others' last
+    };
+    if (whole && ((reinterpret_cast<uintptr_t>(a.C) | (uintptr_t)(a.N * (16 / kPer))) & 63) == 0) {
+      store_whole(std::true_type{});
+    } else if (whole) {
+      store_whole(std::false_type{});
     } else {
 #pragma unroll
       for (int t = 0; t < kPieces; ++t) {
         loads(t);
-        put(t);
+        put(t, t / kPartsB, t % kPartsB);
         get(t);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int64_t m = m0 + 32 * (t % kFA) + 8 * x + r, n = n0 + 8 * kPer * (t / kFA) + kPer * (lane & 7);
+          const int64_t m = m0 + 32 * (t / kPartsB) + 8 * x + r, n = n0 + 8 * kPer * (t % kPartsB) + kPer * (lane & 7);
           if (m < a.M && n < a.N) store_chunk<kBf16Out>(a.C, m * a.N + n, out[t & 1][x], a.N - n);
         }
         __builtin_amdgcn_sched_barrier(0);

@@ -209,6 +209,11 @@ def test_product_is_exact_where_fp32_is(M, N, K):
     assert torch.equal(got, torch.from_numpy(want.astype(np.float32)).bfloat16())
 
 
+@pytest.mark.parametrize("M,N,K", [(4352, 4353, 160), (4300, 4370, 1152), (1536, 1540, 256), (1664, 1665, 96)])
+def test_product_of_whole_tiles_in_rows_off_the_lines(M, N, K):
+    test_product_is_exact_where_fp32_is(M, N, K)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 500, 4096), (40, 70, 11008), (129, 260, 2048), (600, 700, 1376)])
 def test_product_of_wide_exponents(M, N, K):
     ops = operands(M, N, K, (107, 147), 9)
