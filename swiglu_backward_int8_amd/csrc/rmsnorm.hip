@@ -177,6 +177,19 @@ __device__ __forceinline__ float group_sum(float v, float (&s)[16], int wave, in
   return v;
 }
 
+// f(kind, c) for the pieces of a lane.  Only the last can reach past the row:
+// there are as many waves as the row fills with all pieces but it (D > 512 of
+// one wave, D > 1024 (waves - 1) >= 512 waves of more).  Shifts and short stores
+// for both pieces measured slower (16384 x 4100 forward 113 us, so 109; backward
+// 151 and 142).  What rows off 16 bytes still cost (16384 x 4104: 85 and 98 us)
+// is their unaligned loads and stores.
+template <Kind kKind, int kPieces, class F>
+__device__ __forceinline__ void each_piece(F&& f) {
+  static_assert(kPieces == 1 || kPieces == 2, "one or two");
+  if constexpr (kPieces == 2) f(std::integral_constant<Kind, kFull>{}, 0);
+  f(std::integral_constant<Kind, kKind>{}, kPieces - 1);
+}
+
 // kOneWave: each wave of the workgroup takes rows of its own; otherwise the
 // workgroup shares a row.  Piece c of a lane starts kPieces' width of the lanes
 // further.
@@ -192,34 +205,35 @@ __global__ __launch_bounds__(kOneWave ? 256 : 1024) void rms_norm_quant_kernel(c
     const int n0 = a.D - first;
     XPiece<kXF32> x[kPieces];
     Piece h[kPieces], w[kPieces];
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) x[c].template load<kKind>(a.x, at + c * step, n0 - c * step);
+    each_piece<kKind, kPieces>([&](auto kind, int c) { x[c].template load<decltype(kind)::value>(a.x, at + c * step, n0 - c * step); });
     if (a.residual) {
       Piece r[kPieces];
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c) r[c] = load_bf16<kKind, false>(a.residual + at + c * step, n0 - c * step);
+      each_piece<kKind, kPieces>([&](auto kind, int c) {
+        r[c] = load_bf16<decltype(kind)::value, false>(a.residual + at + c * step, n0 - c * step);
+      });
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) h[c] = x[c].plus(r[c]);
     } else {
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) h[c] = x[c].alone();
     }
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) w[c] = load_bf16<kKind, false>(a.weight + first + c * step, n0 - c * step);
+    each_piece<kKind, kPieces>([&](auto kind, int c) {
+      w[c] = load_bf16<decltype(kind)::value, false>(a.weight + first + c * step, n0 - c * step);
+    });
     float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) sum = sum_squares(sum, h[c]);
     sum = kOneWave ? wave_sum(sum) : group_sum(sum, s_sum, wave, waves);
     const float rstd = inverse_rms(sum, a.D, a.eps);
     if (a.rstd && first == 0) a.rstd[row] = rstd;
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
+    each_piece<kKind, kPieces>([&](auto kind, int c) {
+      constexpr Kind k = decltype(kind)::value;
       const int n = n0 - c * step;
-      if (a.h) store_bf16<kKind, true>(a.h + at + c * step, h[c], n);
+      if (a.h) store_bf16<k, true>(a.h + at + c * step, h[c], n);
       const Piece y = scaled(h[c], w[c], rstd);
-      if (a.y) store_bf16<kKind, true>(a.y + at + c * step, y, n);
-      if (a.q) quantise<kE4M3, kKind>(a, y, row, first + c * step, n);
-    }
+      if (a.y) store_bf16<k, true>(a.y + at + c * step, y, n);
+      if (a.q) quantise<kE4M3, k>(a, y, row, first + c * step, n);
+    });
   }
 }
 
@@ -295,26 +309,25 @@ __global__ __launch_bounds__(kOneWave ? 512 : 1024) void rms_norm_bwd_kernel(con
   const int n0 = a.D - first;
   Piece w[kPieces];
   float dw[kPieces][8];
-#pragma unroll
-  for (int c = 0; c < kPieces; ++c) {
-    w[c] = load_bf16<kKind, false>(a.weight + first + c * step, n0 - c * step);
+  each_piece<kKind, kPieces>([&](auto kind, int c) {
+    w[c] = load_bf16<decltype(kind)::value, false>(a.weight + first + c * step, n0 - c * step);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
-  }
+  });
   const int64_t rows_at_once = kOneWave ? waves : 1;
   for (int64_t row = blockIdx.x * rows_at_once + (kOneWave ? wave : 0); row < a.T; row += gridDim.x * rows_at_once) {
     const int64_t at = row * a.D + first;
     const float rstd = a.rstd[row];
     float dy[kPieces][8];
     Piece h[kPieces], d[kPieces];
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-      load_grad<kDyF32, kKind>(dy[c], a.dy, at + c * step, n0 - c * step);
-      h[c] = load_bf16<kKind, true>(a.h + at + c * step, n0 - c * step);
-    }
+    each_piece<kKind, kPieces>([&](auto kind, int c) {
+      load_grad<kDyF32, decltype(kind)::value>(dy[c], a.dy, at + c * step, n0 - c * step);
+      h[c] = load_bf16<decltype(kind)::value, true>(a.h + at + c * step, n0 - c * step);
+    });
     if (a.d_h) {
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c) d[c] = load_bf16<kKind, true>(a.d_h + at + c * step, n0 - c * step);
+      each_piece<kKind, kPieces>([&](auto kind, int c) {
+        d[c] = load_bf16<decltype(kind)::value, true>(a.d_h + at + c * step, n0 - c * step);
+      });
     } else {
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) d[c] = zero_piece();
@@ -334,8 +347,7 @@ __global__ __launch_bounds__(kOneWave ? 512 : 1024) void rms_norm_bwd_kernel(con
     }
     sum = kOneWave ? wave_sum(sum) : group_sum(sum, s_sum, wave, waves);
     const float mean = sum / (float)a.D;
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
+    each_piece<kKind, kPieces>([&](auto kind, int c) {
       float hv[8], wv[8], dv[8], o[8];
       unpack(hv, h[c]);
       unpack(wv, w[c]);
@@ -346,8 +358,8 @@ __global__ __launch_bounds__(kOneWave ? 512 : 1024) void rms_norm_bwd_kernel(con
         o[i] = __builtin_fmaf(rstd, __builtin_fmaf(-n, mean, g), dv[i]);
       }
       const Piece out = {{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])}};
-      store_bf16<kKind, false>(a.dx + at + c * step, out, n0 - c * step);
-    }
+      store_bf16<decltype(kind)::value, false>(a.dx + at + c * step, out, n0 - c * step);
+    });
   }
   if (!a.part) return;
   if (kOneWave) {
@@ -368,10 +380,9 @@ __global__ __launch_bounds__(kOneWave ? 512 : 1024) void rms_norm_bwd_kernel(con
     if (wave != waves - 1) return;
   }
   float* out = a.part + (int64_t)blockIdx.x * a.D + first;
-#pragma unroll
-  for (int c = 0; c < kPieces; ++c) {
+  each_piece<kKind, kPieces>([&](auto kind, int c) {
     const int n = n0 - c * step;
-    if (kKind == kFull || n >= 8) {
+    if (decltype(kind)::value == kFull || n >= 8) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         *reinterpret_cast<f32x4_a4*>(out + c * step + 4 * k) =
@@ -381,7 +392,7 @@ __global__ __launch_bounds__(kOneWave ? 512 : 1024) void rms_norm_bwd_kernel(con
       for (int i = 0; i < 7; ++i)
         if (i < n) out[c * step + i] = dw[c][i];
     }
-  }
+  });
 }
 
 // dw[d] = the sum of the partial rows: 16 columns per workgroup, 64 strips of
