@@ -326,7 +326,8 @@ __global__ __launch_bounds__(64 * kSide * kSide) void mx_quant_both_kernel(const
           for (int k = 0; k < 4; ++k) x[r].w[k] &= keep[k];
       }
     }
-    // rows past the last lie past the record count, and lanes past the blocks too
+    // Rows past the last lie past the record count, and lanes past the blocks too.
+    // All of the offset is the vector register's: the check need not count a scalar's.
     const int row_bytes = 16 * a.blocks_k;
     const auto to_q = __builtin_amdgcn_make_buffer_rsrc(a.q + row0 * row_bytes, 0, (int)(std::min<int64_t>(a.R - row0, kRows) * row_bytes), 0x20000);
     const uint32_t at_q = (uint32_t)(32 * blk * row_bytes + (col >> 1)) | (in_block ? 0 : 0x80000000u);
@@ -342,7 +343,7 @@ __global__ __launch_bounds__(64 * kSide * kSide) void mx_quant_both_kernel(const
           if (kKind == kFull)
             reinterpret_cast<uint32_t*>(a.q)[(r0 + r) * (4 * (int64_t)a.blocks_k) + (col >> 3)] = c;
           else
-            __builtin_amdgcn_raw_buffer_store_b32(c, to_q, at_q, r * row_bytes, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(c, to_q, at_q + (uint32_t)(r * row_bytes), 0, 0);
           keep = (lane & 3) == j ? b : keep;
         }
         s_row[32 * blk + 4 * r4 + (lane & 3)][col_in >> 5] = (uint8_t)keep;
