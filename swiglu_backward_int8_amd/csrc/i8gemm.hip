@@ -35,6 +35,7 @@
 
 #include <type_traits>
 
+#include "code_objects.h"
 #include "siluquant.h"
 
 namespace {
@@ -289,6 +290,8 @@ bool spans_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 }
 
 }  // namespace
+
+hipError_t code_objects::load_i8gemm() { return load(i8_gemm_kernel<true, true, 128>); }
 
 extern "C" {
 

@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "code_objects.h"
 #include "rows.h"
 #include "siluquant.h"
 
@@ -416,6 +417,8 @@ __global__ __launch_bounds__(64 * kSide * kSide) void mx_quant_both_kernel(const
 constexpr int64_t kMaxCols = int64_t(1) << 22, kMaxRows = int64_t(1) << 31;
 
 }  // namespace
+
+hipError_t code_objects::load_mxfp4() { return load(piece_kernel<MxQuantRows, kFull, 1>); }
 
 extern "C" {
 

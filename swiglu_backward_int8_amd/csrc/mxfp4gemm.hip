@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "code_objects.h"
 #include "rows.h"
 #include "siluquant.h"
 
@@ -928,6 +929,8 @@ void pick_and_launch(const GemmArgs& a, bool bf16, int cus, hipStream_t stream) 
 }
 
 }  // namespace
+
+hipError_t code_objects::load_mxfp4gemm() { return load(mx_gemm_stream_kernel<1, 1, 8, true>); }
 
 extern "C" {
 

@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "code_objects.h"
 #include "rows.h"
 #include "siluquant.h"
 
@@ -520,6 +521,8 @@ void launch_bwd(const BwdArgs& a, bool f32, int grid, int waves, hipStream_t str
 }
 
 }  // namespace
+
+hipError_t code_objects::load_rmsnorm() { return load(rms_norm_dw_kernel); }
 
 extern "C" {
 

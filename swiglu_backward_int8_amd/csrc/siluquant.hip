@@ -43,6 +43,7 @@
 
 #include <algorithm>
 
+#include "code_objects.h"
 #include "siluquant.h"
 
 namespace {
@@ -2925,15 +2926,12 @@ __attribute__((visibility("default"))) const char* siluquant_strerror(int status
 }
 
 __attribute__((visibility("default"))) int siluquant_prepare(void) {
-  // Asking for a kernel's attributes makes the runtime load the library's
-  // code object on the current device, which it would otherwise do at the
-  // first launch.
   int cus = 0;
   int rc = device_cus(&cus);
   if (rc != SILUQUANT_OK) return rc;
-  hipFuncAttributes attr;
-  if (hipFuncGetAttributes(&attr, reinterpret_cast<const void*>(silu_quant_bwd_kernel<Fmt::kInt8, 128>)) !=
-      hipSuccess)
+  using namespace code_objects;
+  if (load(silu_quant_bwd_kernel<Fmt::kInt8, 128>) != hipSuccess || load_i8gemm() != hipSuccess ||
+      load_rmsnorm() != hipSuccess || load_mxfp4() != hipSuccess || load_mxfp4gemm() != hipSuccess)
     return SILUQUANT_ERR_DEVICE;
   return SILUQUANT_OK;
 }
