@@ -591,8 +591,9 @@ __attribute__((visibility("default"))) int rms_norm_bwd(const void* dy, int dy_d
     return hipGetLastError() == hipSuccess ? SILUQUANT_OK : SILUQUANT_ERR_LAUNCH_FAILED;
   }
   const bool wide = D > kRegisterD;
+  if (!dw && !wide) workspace = nullptr, workspace_bytes = need;  // not looked at
   if (!dy || !h || !weight || !rstd || !dx || ((dw || wide) && !workspace)) return SILUQUANT_ERR_NULL_PTR;
-  if (workspace_bytes < ((dw || wide) ? need : 0)) return SILUQUANT_ERR_BAD_SHAPE;
+  if (workspace_bytes < need) return SILUQUANT_ERR_BAD_SHAPE;
   if (misaligned(dy, 16) || misaligned(h, 16) || misaligned(weight, 16) || misaligned(d_h, 16) || misaligned(dx, 16) ||
       misaligned(rstd, 4) || misaligned(dw, 4) || misaligned(workspace, 16))
     return SILUQUANT_ERR_MISALIGNED;
