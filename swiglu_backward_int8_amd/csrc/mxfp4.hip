@@ -35,8 +35,6 @@ namespace {
 
 using namespace rows;
 
-typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
-
 constexpr int kThreads = 256;
 
 // E8M0 byte of a block from its largest magnitude (bf16 bits).

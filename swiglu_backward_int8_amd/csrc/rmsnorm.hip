@@ -486,15 +486,14 @@ int bwd_parts(int64_t T, int64_t D) {
 }
 
 // Calls f with the kind of the pieces of a row of D columns, where the lanes'
-// pieces cover `covered`, as a type.
-template <class F>
+// pieces cover `covered`, as a type.  Two pieces per lane start at 513 columns.
+template <int kPieces, class F>
 void with_kind(int64_t D, int64_t covered, F&& f) {
-  if (D == covered)
-    f(std::integral_constant<Kind, kFull>{});
-  else if (D % 8 == 0)
-    f(std::integral_constant<Kind, kWhole>{});
-  else
-    D >= 8 ? f(std::integral_constant<Kind, kRagged>{}) : f(std::integral_constant<Kind, kTiny>{});
+  if (D == covered) return f(std::integral_constant<Kind, kFull>{});
+  if (D % 8 == 0) return f(std::integral_constant<Kind, kWhole>{});
+  if constexpr (kPieces == 1)
+    if (D < 8) return f(std::integral_constant<Kind, kTiny>{});
+  f(std::integral_constant<Kind, kRagged>{});
 }
 
 template <bool kOneWave, int kPieces>
@@ -502,7 +501,7 @@ void launch_norm(const NormArgs& a, bool f32, bool e4m3, int waves, hipStream_t 
   const int64_t groups = kOneWave ? (a.T + waves - 1) / waves : a.T;
   const dim3 grid((unsigned)std::min<int64_t>(groups, kMaxGrid)), block(64 * waves);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
-  with_kind(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
+  with_kind<kPieces>(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
     constexpr Kind k = decltype(kind)::value;
     if (f32)
       e4m3 ? go(rms_norm_quant_kernel<kOneWave, kPieces, true, k, true>) : go(rms_norm_quant_kernel<kOneWave, kPieces, true, k, false>);
@@ -514,7 +513,7 @@ void launch_norm(const NormArgs& a, bool f32, bool e4m3, int waves, hipStream_t 
 template <bool kOneWave, int kPieces>
 void launch_bwd(const BwdArgs& a, bool f32, int grid, int waves, hipStream_t stream) {
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * waves), 0, stream, a); };
-  with_kind(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
+  with_kind<kPieces>(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
     constexpr Kind k = decltype(kind)::value;
     f32 ? go(rms_norm_bwd_kernel<kOneWave, kPieces, true, k>) : go(rms_norm_bwd_kernel<kOneWave, kPieces, false, k>);
   });
