@@ -1,9 +1,7 @@
-"""Which kernels of the norm and microscaled operators are compiled (CPU only):
-none that no call reaches."""
+"""Which kernels of the norm are compiled (CPU only): none that no call reaches."""
 
-import pytest
-
-from test_isa_operators import kernels, asm, pytestmark  # noqa: F401
+import isa
+from test_isa_waits import pytestmark  # noqa: F401
 
 
 def pieces_and_kind(name):
@@ -15,10 +13,10 @@ def pieces_and_kind(name):
     return None
 
 
-def test_short_rows_have_one_piece_per_lane(asm):
+def test_short_rows_have_one_piece_per_lane():
     # rows of fewer than 8 columns (kind 3) go to a wave with one piece per lane;
     # two pieces start at 513 columns
-    found = [pieces_and_kind(n) for n in kernels(asm["rmsnorm"])]
+    found = [pieces_and_kind(n) for n in isa.kernels("rmsnorm")]
     found = [f for f in found if f]
     assert (1, 3) in found and (2, 2) in found
     assert (2, 3) not in found
