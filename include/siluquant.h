@@ -239,8 +239,9 @@ enum siluquant_code_format { SILUQUANT_CODE_INT8 = 0, SILUQUANT_CODE_E4M3 = 1 };
 
 /*
  * rms_norm_quant -- root-mean-square norm with the residual's addition, its
- * output quantised by row groups: the operand of i8_gemm_group_scaled (int8)
- * or of an E4M3 product.
+ * output quantised by row groups: in int8 the operand of i8_gemm_group_scaled;
+ * E4M3 codes are for a product of the caller's (the library has none) or for
+ * group_dequant.
  *
  *   h[t, d]  = bf16(x[t, d] + residual[t, d])        (one fp32 addition)
  *   rstd[t]  = 1 / sqrt(sum_d h[t, d]^2 / D + eps)   (fp32)
@@ -263,8 +264,12 @@ enum siluquant_code_format { SILUQUANT_CODE_INT8 = 0, SILUQUANT_CODE_E4M3 = 1 };
  * Sizes: T <= 2^31, D <= 2^22, any D (the last group of a row may be short);
  *   T == 0 or D == 0 is a no-op.  group: 128, 64 or 32.  eps: finite, >= 0 (a
  *   row of zeros with eps == 0 gives NaN).
- * A row that holds an infinity or a NaN gives NaN scales (or NaN codes) in the
- * groups whose y is not finite; other rows are not affected.
+ * y that is not finite shows in its group's scale: NaN where the group's y holds
+ * a NaN, +infinity where it holds an infinity and no NaN (a weight that is, or a
+ * product past bf16's range); the group's codes then mean nothing.  A NaN in a
+ * row of h makes all of the row's y NaN, an infinity its own place alone (rstd
+ * is 0 and the rest of the row too).  Other groups, and other rows, are not
+ * affected.
  */
 int rms_norm_quant(const void* x, int x_dtype, const void* residual, const void* weight, void* y_q, float* y_s,
                    void* y_bf16, void* h, float* rstd, int64_t T, int64_t D, int64_t group, int code_format, float eps,
@@ -326,8 +331,9 @@ int mxfp4_quant(const void* x, void* q, void* s, void* q_t, void* s_t, int64_t R
  * K counts whole blocks: a multiple of 32 (mxfp4_quant's rows are filled up).
  * Sums are fp32; bf16 output rounds them once (nearest, ties to even).  An
  * exponent byte of 255 makes the row or column of C it belongs to NaN.
- * Sizes: any M, N >= 0 (M == 0 or N == 0 is a no-op), K <= 2^22 (K == 0 writes
- * zeros).  From single rows (the weight streams through once) to large tiles.
+ * Sizes: 0 <= M, N <= 2^31 (M == 0 or N == 0 is a no-op) with ceil(M/128) *
+ * ceil(N/128) <= 2^30, K <= 2^22 (K == 0 writes zeros).  From single rows (the
+ * weight streams through once) to large tiles.
  */
 int mxfp4_gemm(const void* A, const void* sA, const void* B, const void* sB, void* C, int64_t M, int64_t N, int64_t K,
                int c_dtype, hipStream_t stream);

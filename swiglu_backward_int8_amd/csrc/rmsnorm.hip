@@ -397,7 +397,8 @@ __global__ __launch_bounds__(kOneWave ? 512 : 1024) void rms_norm_bwd_kernel(con
 }
 
 // dw[d] = the sum of the partial rows: 16 columns per workgroup, 64 strips of
-// rows, each in row order, and then the strips in order.
+// rows (every 64th), each in row order, and then the strips in pairs, halving
+// their number, always the same ones.
 constexpr int kSumStrips = 64, kSumCols = 16;
 __global__ __launch_bounds__(kSumCols * kSumStrips) void rms_norm_dw_kernel(const float* part, float* dw, int parts, int D) {
   __shared__ float s[kSumStrips][kSumCols];
