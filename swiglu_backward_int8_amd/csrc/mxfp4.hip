@@ -16,11 +16,13 @@
 // lane.  Quantising both axes reads x once: a lane holds 32 rows of eight
 // columns in registers, so that a column's block lies inside the lane (no
 // transpose through LDS) and a row's block inside four neighbouring lanes.
-// Measured: rows of 16384 x 11008 71 us (6.4 TB/s), dequantised 22016 x 4096 39 us
-// (5.9 TB/s); both axes of 8192 x 4096 20 us (5.1 TB/s), of 16384 x 11008 103 us
-// (5.4 TB/s), of which reading and computing alone take 15 and 62: with all of a
-// tile's rows in registers a wave's loads and stores do not overlap.  Rows that
-// are not whole lines cost more (8192 x 4104: 29 us), in x and in the codes.
+// Measured, over as many sets of tensors as leave the cache nothing of use: rows
+// of 16384 x 11008 74 us (6.2 TB/s), dequantised 22016 x 4096 38 us (6.0 TB/s);
+// both axes of 8192 x 4096 20 us (5.1 TB/s), of 16384 x 11008 130 us (4.3 TB/s;
+// one set over and over, part of which stays in the Infinity Cache, 106), columns
+// alone 16 and 92 us.  Of the 20 us reading and computing alone take 15: with all
+// of a tile's rows in registers a wave's loads and stores do not overlap.  Rows
+// that are not whole lines cost more (8192 x 4104: 29 us), in x and in the codes.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -245,8 +247,8 @@ struct BothArgs {
 // (b, p) = (lane / 16, lane % 16) holds rows 32 b .. + 31 of columns 8 p .. + 7,
 // so that a load covers 256 bytes of four rows and four neighbouring column
 // blocks leave as 64 contiguous bytes.  Two waves side by side and two below
-// each other write whole 128-byte lines of both kinds of codes (16384 x 11008:
-// 103 us; four below each other 109, side by side 112).  The exponents meet in
+// each other write whole 128-byte lines of both kinds of codes (16384 x 11008,
+// one set over and over: 103 us; four below each other 109, side by side 112).  The exponents meet in
 // LDS, from where a thread stores all that a tile has of a column or of a row
 // (stored from the lanes, a byte each, the columns' cost a fifth of the time and
 // the rows' another 5 us).  Each XCD takes whole bands of rows, so that the lines
@@ -269,9 +271,10 @@ __global__ __launch_bounds__(64 * kSide * kSide) void mx_quant_both_kernel(const
   // the wave's part of the tile at (row0, col0)
   auto part = [&](auto kind, int64_t row0, int col0) {
     constexpr Kind kKind = decltype(kind)::value;
-    // streamed where rows are whole pieces; other rows share pieces of lines,
+    // streamed where rows are whole pieces of 16 bytes; others share pieces,
     // which have to stay in L2 (3000 x 4100: 21 us streamed, 16 cached; 8192 x
-    // 4096: 20 us and 25)
+    // 4096: 20 us and 25).  Widths of a multiple of 8 but not of 64 share lines,
+    // not pieces, and are streamed too (8192 x 4104: 29 us; not timed cached).
     constexpr bool kNt = kEdge <= kWhole;
     const int col = col0 + col_in, n = a.K - col;
     const bool in_block = col < 32 * a.blocks_k;  // the same for four neighbouring lanes

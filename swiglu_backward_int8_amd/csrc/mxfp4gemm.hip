@@ -288,7 +288,9 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4& a, uint32_t sa, const u32x
 // kWords: rows of exponents start on 4 bytes (K is a multiple of 128, in aligned buffers).  They
 // then go into LDS too, 32 blocks of every row at a time, a quarter of the next
 // 32 with each stage: read from memory by every wave in every stage, 4 bytes a
-// row, they doubled the requests to L2 and cost a quarter of the time.
+// row, they doubled the requests to L2 and cost a quarter of the time.  Exponents
+// of any other K, or off 4 bytes, are still read that way: 16384 x 22016 x 4064
+// takes 932 us (4096: 690; 4096 off 4 bytes: 868), 4096 x 4096 x 4064 46 us (36).
 //
 // Workgroups are persistent (one per CU for 256 x 256, two for 128 x 128, or one
 // with four buffers, whose loads are three stages ahead): the
@@ -902,6 +904,14 @@ void launch_stream(GemmArgs a, bool bf16, hipStream_t stream) {
 //     (1024 x 4096: 14.5 us, with two 16.5; 512 x 4096 x 11008: 27 and 35 us);
 //   * without words, the stream in place of the slices (256 x 4096 x 1376: 7.3
 //     us, tiles of 128 9.1; 512 x 4096 x 1376: 12.7 and 9.4 us).
+// The tiles' rounds were measured at K = 4096 and decide at every K.  Tiles of 256
+// and of 128, in us, the rule's choice first: 16384 x 22016 x 128 160 and 152, x
+// 256 157 and 154, x 1024 262 and 301, x 11008 1718 and 2412; 8192 x 8192 x 128 34
+// and 37, x 512 45 and 42, x 1024 66 and 62, x 11008 329 and 471; 4096 x 4096 x 128
+// 11.4 and 10.0, x 1024 17.4 and 18.0, x 4064 46 and 69; 2048 x 4096 (128 first) x
+// 256 7.0 and 8.5, x 11008 58 and 60.  It is never more than a seventh off there, and at
+// short K the time is that of the results' way to memory (16384 x 22016 x 32: 158
+// us, 4.6 TB/s).
 void pick_and_launch(const GemmArgs& a, bool bf16, int cus, hipStream_t stream) {
   auto tiles = [&](int64_t tm, int64_t tn) { return ((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn); };
   if (a.M <= 32) {
