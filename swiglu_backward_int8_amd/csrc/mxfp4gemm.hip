@@ -220,7 +220,7 @@ __global__ __launch_bounds__(64 * kW) void mx_gemm_stream_kernel(const GemmArgs 
 // alone, nothing else running, they reach 6.6 PFLOP/s at a lowered clock (9.4
 // with zeros).  256 x 256 tiles of 128 x 128 per wave, the most that fits the
 // registers, read LDS for half of the cycles and L2 for a third.  16384 x 4096 x
-// 11008: 311 us, 4.75 PFLOP/s; 16384 x 22016 x 4096: 690 to 710 us, 4.2 to 4.3.
+// 11008: 311 to 330 us, 4.5 to 4.75 PFLOP/s; 16384 x 22016 x 4096: 690 to 710 us, 4.2 to 4.3.
 // A stage of 2048 matrix cycles takes 2900; a tile's end (results out through
 // LDS, next tile's start) as long as three stages, half of it the stores' way to
 // memory (without any stores 640 us).  Loads not spread over two steps, larger
