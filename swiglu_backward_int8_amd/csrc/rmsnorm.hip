@@ -32,7 +32,7 @@
 #include <type_traits>
 
 #include "code_objects.h"
-#include "rows.h"
+#include "norm_rows.h"
 #include "siluquant.h"
 
 namespace {
@@ -41,48 +41,6 @@ using namespace rows;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
-
-constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
-
-// Eight codes of the bf16 values in p.  int8: p * inv is one fp32 product, and
-// adding kMagic leaves its nearest integer in the low byte.  E4M3: the hardware
-// conversion (nearest, ties to even).  kSafe serves an inverse that overflowed:
-// products clamp to the largest code, zeros stay zeros.
-template <bool kE4M3, bool kSafe>
-__device__ __forceinline__ u32x2 codes8(const Piece& p, float inv) {
-  constexpr float kTop = kE4M3 ? 448.0f : 127.0f;
-  float v[8];
-  unpack(v, p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = v[i] * inv;
-    v[i] = !kSafe ? t : v[i] == 0.0f ? v[i] : __builtin_amdgcn_fmed3f(t, -kTop, kTop);
-  }
-  u32x2 out;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float* q = v + 4 * k;
-    if (kE4M3) {
-      int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-      out[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
-    } else {
-      uint32_t b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[i] + kMagic);
-      const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
-      const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
-      out[k] = lo | (hi << 16);
-    }
-  }
-  return out;
-}
-
-// Scale of a group from its largest bf16 magnitude, and the scale's inverse.
-template <bool kE4M3>
-__device__ __forceinline__ float group_scale(uint32_t amax_bits) {
-  const float amax = __uint_as_float(amax_bits << 16);
-  return amax == 0.0f ? 1.0f : amax / (kE4M3 ? 448.0f : 127.0f);
-}
 
 struct NormArgs {
   const void* x;
@@ -155,44 +113,6 @@ __device__ __forceinline__ Piece scaled(const Piece& h, const Piece& w, float rs
   for (int i = 0; i < 4; ++i)
     o.w[i] = pack_bf16((bf16_lo(h.w[i]) * rstd) * bf16_lo(w.w[i]), (bf16_hi(h.w[i]) * rstd) * bf16_hi(w.w[i]));
   return o;
-}
-
-// Codes and scale of one piece's group; every lane of the wave calls it.
-template <bool kE4M3, Kind kKind>
-__device__ __forceinline__ void quantise(const NormArgs& a, const Piece& y, int64_t row, int col, int n) {
-  const uint32_t amax = group_amax_bits<true>(y, 1 << a.lg_lanes);
-  const float scale = group_scale<kE4M3>(amax);
-  const float inv = 1.0f / scale;
-  u32x2 c = codes8<kE4M3, false>(y, inv);
-  if (__any(inv == __builtin_huge_valf())) c = codes8<kE4M3, true>(y, inv);
-  if (n > 0) {
-    store_codes<kKind>(a.q + row * a.D + col, c.x, c.y, n);
-    if ((threadIdx.x & ((1 << a.lg_lanes) - 1)) == 0) a.s[row * a.groups + (col >> (3 + a.lg_lanes))] = scale;
-  }
-}
-
-// The sum over a workgroup's waves (16 at most) of their own sums, in wave order.
-__device__ __forceinline__ float group_sum(float v, float (&s)[16], int wave, int waves) {
-  const int lane = threadIdx.x & 63;
-  v = wave_sum(v);
-  if (lane == 0) s[wave] = v;
-  __syncthreads();
-  v = sum16((lane & 15) < waves ? s[lane & 15] : 0.0f);
-  __syncthreads();  // before the next row's sums
-  return v;
-}
-
-// f(kind, c) for the pieces of a lane.  Only the last can reach past the row:
-// there are as many waves as the row fills with all pieces but it (D > 512 of
-// one wave, D > 1024 (waves - 1) >= 512 waves of more).  Shifts and short stores
-// for both pieces measured slower (16384 x 4100 forward 113 us, so 109; backward
-// 151 and 142).  What rows off 16 bytes still cost (16384 x 4104: 85 and 98 us)
-// is their unaligned loads and stores.
-template <Kind kKind, int kPieces, class F>
-__device__ __forceinline__ void each_piece(F&& f) {
-  static_assert(kPieces == 1 || kPieces == 2, "one or two");
-  if constexpr (kPieces == 2) f(std::integral_constant<Kind, kFull>{}, 0);
-  f(std::integral_constant<Kind, kKind>{}, kPieces - 1);
 }
 
 // kOneWave: each wave of the workgroup takes rows of its own; otherwise the
@@ -291,14 +211,6 @@ struct BwdArgs {
   int64_t T;
   int D;
 };
-
-template <bool kF32, Kind kKind>
-__device__ __forceinline__ void load_grad(float (&v)[8], const void* p, int64_t at, int n) {
-  if constexpr (kF32)
-    load_f32<kKind>(v, static_cast<const float*>(p) + at, n);
-  else
-    unpack(v, load_bf16<kKind, true>(static_cast<const uint16_t*>(p) + at, n));
-}
 
 // The same division of rows as in the forward pass.  A lane keeps the dw sums of
 // its columns in registers over all its rows; where waves have rows of their
@@ -488,17 +400,6 @@ constexpr int kMaxGrid = 1 << 20;  // workgroups of the forward kernels; further
 int bwd_parts(int64_t T, int64_t D) {
   const int64_t waves = D <= 1024 ? 8 : D <= kRegisterD ? (D + 1023) / 1024 : 8;
   return (int)std::min<int64_t>(T, std::max<int64_t>(256, 2048 / waves));
-}
-
-// Calls f with the kind of the pieces of a row of D columns, where the lanes'
-// pieces cover `covered`, as a type.  Two pieces per lane start at 513 columns.
-template <int kPieces, class F>
-void with_kind(int64_t D, int64_t covered, F&& f) {
-  if (D == covered) return f(std::integral_constant<Kind, kFull>{});
-  if (D % 8 == 0) return f(std::integral_constant<Kind, kWhole>{});
-  if constexpr (kPieces == 1)
-    if (D < 8) return f(std::integral_constant<Kind, kTiny>{});
-  f(std::integral_constant<Kind, kRagged>{});
 }
 
 template <bool kOneWave, int kPieces>
