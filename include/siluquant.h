@@ -352,6 +352,88 @@ int mxfp4_dequant(const void* q, const void* s, void* out, int64_t R, int64_t K,
 int group_dequant(const void* q, const float* s, void* out, int64_t R, int64_t K, int64_t group, int code_format,
                   hipStream_t stream);
 
+/* ---- the same block in bf16: layer norm, dropout ---- */
+
+/*
+ * A dropout's mask is made where it is used and never stored.  Element (t, d) of
+ * a [T, D] tensor is dropped where word d % 4 of
+ *   Philox4x32-10(key = rng[0], counter = (d / 4, t, rng[1] + offset))
+ * is below p * 2^32 (nearest).  That is the generator of Salmon, Moraes, Dror and
+ * Shaw ("Parallel random numbers: as easy as 1, 2, 3", SC 2011); the key's and the
+ * counter's last two words are the 64-bit numbers' low and high halves.  What is
+ * kept is multiplied by 1 / (1 - p), one fp32 number; what is dropped is 0,
+ * whatever it was.  So the backward pass, given the same p, rng and offset, has
+ * the forward pass's mask.
+ *   p       0 <= p < 1 as fp32; 0: nothing is dropped, rng is not looked at
+ *   rng     int64 [2] in device memory (8-byte aligned): a seed, and a number that
+ *           the program changes from step to step.  Read when the kernels run: a
+ *           captured call draws a new mask at a replay if they have changed.
+ *   offset  added to rng[1] (modulo 2^64): tells the dropouts of a step apart
+ *
+ * dropout_add -- out = bf16(residual + dropout(x)), one fp32 product and one fp32
+ * sum.  On the gradient of out, without a residual, the backward pass for x.
+ *   x         bf16 or fp32 [T, D] by x_dtype
+ *   residual  bf16 [T, D], or NULL for none
+ *   out       bf16 [T, D]; may be residual itself, or x itself if that is bf16
+ * 16-byte aligned.  T <= 2^31, D <= 2^22, T * D <= 2^40; T == 0 or D == 0 is a
+ * no-op.
+ */
+int dropout_add(const void* x, int x_dtype, const void* residual, void* out, int64_t T, int64_t D, float p,
+                const int64_t* rng, int64_t offset, hipStream_t stream);
+
+/*
+ * layer_norm_quant -- layer norm with a dropout and the residual's addition in
+ * front of it, its output in bf16, or quantised by row groups as rms_norm_quant's.
+ *
+ *   h[t, d]  = bf16(residual[t, d] + dropout(x)[t, d])     (as dropout_add)
+ *   mean[t]  = sum_d h[t, d] / D
+ *   rstd[t]  = 1 / sqrt(sum_d (h[t, d] - mean[t])^2 / D + eps)
+ *   y[t, d]  = bf16(((h[t, d] - mean[t]) * rstd[t]) * weight[d] + bias[d])
+ *   codes and scales of y by groups of `group` channels, as rms_norm_quant.
+ *
+ *   weight, bias  bf16 [D]; bias may be NULL for none
+ *   mean, rstd    fp32 [T], or NULL: what layer_norm_bwd needs
+ *   p, rng, offset  the dropout, as above
+ *   The other arguments, alignments, sizes and the place of h (it may be `residual`
+ *   itself) as rms_norm_quant.
+ * A NaN or an infinity in a row of h makes all of the row's y NaN, which shows in
+ * its scales as there; other rows are not affected.  A row of one value has a
+ * variance of zero, up to the rounding of its mean: with eps == 0 its y means
+ * nothing.
+ */
+int layer_norm_quant(const void* x, int x_dtype, const void* residual, const void* weight, const void* bias, void* y_q,
+                     float* y_s, void* y_bf16, void* h, float* mean, float* rstd, int64_t T, int64_t D, int64_t group,
+                     int code_format, float eps, float p, const int64_t* rng, int64_t offset, hipStream_t stream);
+
+/*
+ * layer_norm_bwd -- the gradients of that norm.  With n = (h - mean) * rstd and
+ * g = dy * weight:
+ *
+ *   dx[t, d]  = rstd[t] * (g[t, d] - sum_d(g) / D - n[t, d] * sum_d(g * n) / D) + d_h[t, d]
+ *   dw[d]     = sum_t dy[t, d] * n[t, d];   db[d] = sum_t dy[t, d]
+ *
+ * dx, rounded to bf16, is the gradient of h: for the residual, and for x where
+ * nothing was dropped.  dx_drop is the gradient for x through the dropout: the
+ * same numbers before they are rounded, masked and multiplied as above.
+ *   dy       bf16 or fp32 [T, D] by dy_dtype
+ *   h, weight, mean, rstd   as layer_norm_quant wrote and read them
+ *   d_h      bf16 [T, D], or NULL; dx may be d_h itself
+ *   dx       bf16 [T, D];  dx_drop  bf16 [T, D], or NULL (it needs p > 0: with
+ *            p == 0 it returns SILUQUANT_ERR_BAD_SHAPE); without it rng is not
+ *            looked at
+ *   dw, db   fp32 [D], either NULL where it is not wanted
+ *   workspace  layer_norm_bwd_workspace_bytes(T, D) bytes, 16-byte aligned; only
+ *            looked at when dw or db is wanted or D > 16384.  Its contents before
+ *            and after a call mean nothing.  The sums do not depend on timing.
+ * Sizes as layer_norm_quant; T == 0 writes zeros to dw and db.  A workspace that is
+ * too small returns SILUQUANT_ERR_BAD_SHAPE.
+ */
+int64_t layer_norm_bwd_workspace_bytes(int64_t T, int64_t D);
+int layer_norm_bwd(const void* dy, int dy_dtype, const void* h, const void* weight, const float* mean, const float* rstd,
+                   const void* d_h, void* dx, void* dx_drop, float* dw, float* db, void* workspace,
+                   int64_t workspace_bytes, int64_t T, int64_t D, float p, const int64_t* rng, int64_t offset,
+                   hipStream_t stream);
+
 /* Optional: makes the HIP runtime load the library's kernels on the current
  * device now, which it otherwise does at the first launch.  No entry point
  * needs it first.  Enqueues nothing, allocates nothing itself; safe to call

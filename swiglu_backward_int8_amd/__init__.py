@@ -31,7 +31,8 @@ _ERRORS = {
 EXPORTED = ("silu_dot_fwd_bwd_quant_fuse", "silu_dot_fwd_bwd_quant_fuse_fp8", "silu_fwd_quant", "silu_fwd_quant_q8_1",
             "kquant_swiglu_q8_1_rows", "i8_gemm_group_scaled", "siluquant_prepare", "siluquant_strerror", "siluquant_algorithmic_bytes",
             "siluquant_eval_sigmoid", "siluquant_eval_intermediates", "rms_norm_quant", "rms_norm_bwd",
-            "rms_norm_bwd_workspace_bytes", "mxfp4_quant", "mxfp4_gemm", "mxfp4_dequant", "group_dequant")
+            "rms_norm_bwd_workspace_bytes", "mxfp4_quant", "mxfp4_gemm", "mxfp4_dequant", "group_dequant",
+            "dropout_add", "layer_norm_quant", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes")
 
 _lib = None
 
@@ -69,10 +70,15 @@ def lib() -> ctypes.CDLL:
                          (L.mxfp4_quant, [vp, vp, vp, vp, vp, i64, i64, vp]),
                          (L.mxfp4_gemm, [vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]),
                          (L.mxfp4_dequant, [vp, vp, vp, i64, i64, vp]),
-                         (L.group_dequant, [vp, vp, vp, i64, i64, i64, ci, vp])):
+                         (L.group_dequant, [vp, vp, vp, i64, i64, i64, ci, vp]),
+                         (L.dropout_add, [vp, ci, vp, vp, i64, i64, cf, vp, i64, vp]),
+                         (L.layer_norm_quant, [vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, cf, cf, vp,
+                                               i64, vp]),
+                         (L.layer_norm_bwd, [vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, cf, vp, i64,
+                                             vp])):
             fn.argtypes, fn.restype = args, ci
-        L.rms_norm_bwd_workspace_bytes.argtypes = [i64, i64]
-        L.rms_norm_bwd_workspace_bytes.restype = i64
+        for fn in (L.rms_norm_bwd_workspace_bytes, L.layer_norm_bwd_workspace_bytes):
+            fn.argtypes, fn.restype = [i64, i64], i64
         L.siluquant_eval_sigmoid.argtypes = [vp, vp, i64, vp]
         L.siluquant_eval_sigmoid.restype = ctypes.c_int
         L.siluquant_eval_intermediates.argtypes = [vp, vp, vp, vp, i64, i64, vp]
@@ -364,11 +370,12 @@ _torch = None  # torch and what of it every call needs, once the first call has 
 
 
 def _need_torch():
-    global _torch, _f32, _bf16, _u8, _i8, _e4m3, _device_of_thread, _raw_stream
+    global _torch, _f32, _bf16, _u8, _i8, _i64, _e4m3, _device_of_thread, _raw_stream
     import torch
 
     torch.cuda.init()
     _f32, _bf16, _u8, _i8, _e4m3 = torch.float32, torch.bfloat16, torch.uint8, torch.int8, torch.float8_e4m3fn
+    _i64 = torch.int64
     # what current_device() and current_stream() wrap, without the wrapping (3 us a call)
     _device_of_thread = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -567,6 +574,124 @@ def group_dequant(q, s, out, group_size: int = GROUP):
     _want("s", s, _f32, (R, -(-K // group_size)), idx)
     _enqueue(lib().group_dequant, "group_dequant", idx, q.data_ptr(), s.data_ptr(), out.data_ptr(), R, K, group_size,
              fmt)
+
+
+# ---- the same block in bf16: layer norm, dropout ----
+
+
+def _want_drop(p, rng, offset, idx):
+    if not 0.0 <= p < 1.0:
+        raise ValueError("p must be at least 0 and less than 1, got %r" % (p,))
+    if p > 0.0:
+        if rng is None:
+            raise ValueError("p > 0 needs rng, an int64 tensor of two numbers")
+        _want("rng", rng, _i64, (2,), idx)
+    if not -2**63 <= offset < 2**63:
+        raise ValueError("offset must be a 64-bit number, got %r" % (offset,))
+
+
+def dropout_add(x, out, p: float, rng, residual=None, offset: int = 0):
+    """out = bf16(residual + dropout(x)): every element of x bf16 or fp32 [T, D] is
+    dropped with probability p, and what is kept multiplied by 1 / (1 - p).  The
+    mask is a function of the place, rng (int64 [2] on the device: a seed, and a
+    number that changes from step to step) and offset (which dropout of the step),
+    so the same call on the gradient of out, without residual, is the backward
+    pass.  out bf16 [T, D] may be residual itself, or x itself.  Enqueued on the
+    current stream of x's device; returns None."""
+    T, D, idx = _rank2("x", x)
+    _want2("x", x, _bf16, _f32, (T, D), idx)
+    _want("out", out, _bf16, (T, D), idx)
+    if residual is not None:
+        _want("residual", residual, _bf16, (T, D), idx)
+    _want_drop(p, rng, offset, idx)
+    _enqueue(lib().dropout_add, "dropout_add", idx, x.data_ptr(), F32 if x.dtype is _f32 else BF16, _ptr(residual),
+             out.data_ptr(), T, D, p, _ptr(rng), offset)
+
+
+def layer_norm_quant(x, weight, bias=None, y_q=None, y_s=None, residual=None, h=None, mean=None, rstd=None, y_bf16=None,
+                     eps: float = 1e-5, group_size: int = GROUP, p: float = 0.0, rng=None, offset: int = 0):
+    """h = bf16(residual + dropout(x)) as dropout_add, y = bf16((h - mean) * rstd *
+    weight + bias), and the codes and scales of y by groups of group_size channels.
+
+    x bf16 or fp32 [T, D]; weight and bias bf16 [D]; residual bf16 [T, D].  Written
+    where given: y_q [T, D] (int8; or E4M3 as uint8 or float8_e4m3fn) together with
+    y_s fp32 [T, ceil(D/group_size)], y_bf16 [T, D], h bf16 [T, D] (may be residual
+    itself), mean and rstd fp32 [T].  At least one of y_q and y_bf16 is needed.
+    Enqueued on the current stream of x's device; returns None."""
+    T, D, idx = _rank2("x", x)
+    if group_size not in GROUPS:
+        raise ValueError("group_size must be one of %s" % (GROUPS,))
+    _want2("x", x, _bf16, _f32, (T, D), idx)
+    _want("weight", weight, _bf16, (D,), idx)
+    if bias is not None:
+        _want("bias", bias, _bf16, (D,), idx)
+    if (y_q is None) != (y_s is None) or (y_q is None and y_bf16 is None):
+        raise ValueError("y_q and y_s go together, and one of y_q and y_bf16 is needed")
+    fmt = CODE_INT8
+    if y_q is not None:
+        fmt = _code_format("y_q", y_q)
+        _want("y_q", y_q, y_q.dtype, (T, D), idx)
+        _want("y_s", y_s, _f32, (T, -(-D // group_size)), idx)
+    for name, t in (("residual", residual), ("h", h), ("y_bf16", y_bf16)):
+        if t is not None:
+            _want(name, t, _bf16, (T, D), idx)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _want(name, t, _f32, (T,), idx)
+    _want_drop(p, rng, offset, idx)
+    _enqueue(lib().layer_norm_quant, "layer_norm_quant", idx, x.data_ptr(), F32 if x.dtype is _f32 else BF16,
+             _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(y_q), _ptr(y_s), _ptr(y_bf16), _ptr(h), _ptr(mean),
+             _ptr(rstd), T, D, group_size, fmt, eps, p, _ptr(rng), offset)
+
+
+def layer_norm_bwd_workspace(T: int, D: int, device):
+    """A workspace tensor for layer_norm_bwd at this size (any larger one will do)."""
+    import torch
+
+    n = int(lib().layer_norm_bwd_workspace_bytes(int(T), int(D)))
+    if n < 0:
+        raise ValueError("no such size: T=%d D=%d" % (T, D))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _workspace(workspace, idx):
+    """Its size in bytes; 0 for none."""
+    if workspace is None:
+        return 0
+    if workspace.get_device() != idx or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on cuda:%d" % idx)
+    return workspace.numel() * workspace.element_size()
+
+
+def layer_norm_bwd(dy, h, weight, mean, rstd, dx, dw=None, db=None, d_h=None, dx_drop=None, workspace=None,
+                   p: float = 0.0, rng=None, offset: int = 0):
+    """Gradients of layer_norm_quant: dx bf16 [T, D] for h (the residual's; x's too
+    where nothing was dropped; d_h bf16 [T, D], the gradient that reaches h
+    otherwise, is added, and dx may be d_h itself), dx_drop bf16 [T, D] for x through
+    the dropout of p, rng and offset, and dw and db fp32 [D], each where given.  dy
+    bf16 or fp32 [T, D]; h, weight, mean, rstd as in the forward call.  workspace:
+    from layer_norm_bwd_workspace, needed for dw, for db and for D > 16384.
+    Enqueued on the current stream of dy's device; returns None."""
+    T, D, idx = _rank2("dy", dy)
+    _want2("dy", dy, _bf16, _f32, (T, D), idx)
+    _want("weight", weight, _bf16, (D,), idx)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _want(name, t, _f32, (T,), idx)
+    _want("h", h, _bf16, (T, D), idx)
+    _want("dx", dx, _bf16, (T, D), idx)
+    for name, t in (("dw", dw), ("db", db)):
+        if t is not None:
+            _want(name, t, _f32, (D,), idx)
+    if d_h is not None:
+        _want("d_h", d_h, _bf16, (T, D), idx)
+    if dx_drop is not None:
+        if p == 0.0:
+            raise ValueError("dx_drop needs the p, rng and offset of the dropout")
+        _want("dx_drop", dx_drop, _bf16, (T, D), idx)
+        _want_drop(p, rng, offset, idx)
+    _enqueue(lib().layer_norm_bwd, "layer_norm_bwd", idx, dy.data_ptr(), F32 if dy.dtype is _f32 else BF16, h.data_ptr(),
+             weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(d_h), dx.data_ptr(), _ptr(dx_drop), _ptr(dw),
+             _ptr(db), _ptr(workspace), _workspace(workspace, idx), T, D, p, _ptr(rng), offset)
 
 
 def empty_outputs(T: int, H: int, device, group: int = GROUP, fp8: bool = False):

@@ -20,6 +20,7 @@ __attribute__((visibility("hidden"))) hipError_t load_i8gemm();
 __attribute__((visibility("hidden"))) hipError_t load_rmsnorm();
 __attribute__((visibility("hidden"))) hipError_t load_mxfp4();
 __attribute__((visibility("hidden"))) hipError_t load_mxfp4gemm();
+__attribute__((visibility("hidden"))) hipError_t load_layernorm();
 
 }  // namespace code_objects
 
