@@ -352,7 +352,7 @@ int mxfp4_dequant(const void* q, const void* s, void* out, int64_t R, int64_t K,
 int group_dequant(const void* q, const float* s, void* out, int64_t R, int64_t K, int64_t group, int code_format,
                   hipStream_t stream);
 
-/* ---- the same block in bf16: layer norm, dropout ---- */
+/* ---- the same block in bf16: layer norm, dropout, gated projection ---- */
 
 /*
  * A dropout's mask is made where it is used and never stored.  Element (t, d) of
@@ -433,6 +433,51 @@ int layer_norm_bwd(const void* dy, int dy_dtype, const void* h, const void* weig
                    const void* d_h, void* dx, void* dx_drop, float* dw, float* db, void* workspace,
                    int64_t workspace_bytes, int64_t T, int64_t D, float p, const int64_t* rng, int64_t offset,
                    hipStream_t stream);
+
+/*
+ * swiglu_gemm -- the gate and up projections, the activation and the product of a
+ * gated feed-forward block in one kernel, on the matrix cores:
+ *
+ *   gate = x . Wg^T,  up = x . Wu^T  (fp32 sums of exact products)
+ *   y[t, h] = bf16(gate[t, h] / (1 + exp(-gate[t, h])) * up[t, h])
+ *
+ *   x   bf16 [T, D]
+ *   w   bf16 [2H, D]: Wg's H rows, then Wu's
+ *   y   bf16 [T, H], from the sums as they are
+ *   gu  bf16 [T, 2H]: [gate | up], rounded; or NULL.  What swiglu_gemm_bwd needs,
+ *       and the x of silu_dot_fwd_bwd_quant_fuse and of silu_fwd_quant (whose y is
+ *       that of the rounded gate and up).
+ * All 16-byte aligned.  Sizes: any T <= 2^31, H and D multiples of 8 up to 2^20
+ *   (rows of whole 16-byte pieces); T == 0 or H == 0 is a no-op, D == 0 gives
+ *   zeros.  ceil(T/64) * ceil(2H/64), ceil(T/64) * ceil(D/64) and ceil(2H/64) *
+ *   ceil(D/64) are at most 2^30.
+ * An infinity or a NaN in a row of x or of w makes of the rows or columns it meets
+ * what the formulas do: gate = -infinity gives NaN (0 times infinity).
+ */
+int swiglu_gemm(const void* x, const void* w, void* y, void* gu, int64_t T, int64_t H, int64_t D, hipStream_t stream);
+
+/*
+ * swiglu_gemm_bwd -- the gradients of that.  With s = 1 / (1 + exp(-gate)):
+ *
+ *   d_gu[t] = bf16([dy * up * s * (1 + gate * (1 - s)) | dy * (gate * s)])
+ *   dx = d_gu . W;   dw = d_gu^T . x      (fp32 sums)
+ *
+ *   dy    bf16 [T, H];  gu, x, w as swiglu_gemm wrote and read them
+ *   d_gu  bf16 [T, 2H]; may be gu itself.  Rounded to bf16, as the matrix cores
+ *         take it; dx and dw are those of the rounded numbers.
+ *   dx    bf16 or fp32 [T, D] by dx_dtype, or NULL where it is not wanted (w is
+ *         then not looked at)
+ *   dw    bf16 or fp32 [2H, D] by dw_dtype, or NULL (x is then not looked at)
+ *   workspace  swiglu_gemm_bwd_workspace_bytes(T, H, D) bytes, which may be 0,
+ *         16-byte aligned.  Its contents before and after a call mean nothing.
+ *         The sums do not depend on timing.
+ * All 16-byte aligned; sizes as swiglu_gemm.  T == 0 writes zeros to dw, H == 0 to
+ * dx.  A workspace that is too small returns SILUQUANT_ERR_BAD_SHAPE.
+ */
+int64_t swiglu_gemm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t D);
+int swiglu_gemm_bwd(const void* dy, const void* gu, const void* x, const void* w, void* d_gu, void* dx, int dx_dtype,
+                    void* dw, int dw_dtype, void* workspace, int64_t workspace_bytes, int64_t T, int64_t H, int64_t D,
+                    hipStream_t stream);
 
 /* Optional: makes the HIP runtime load the library's kernels on the current
  * device now, which it otherwise does at the first launch.  No entry point

@@ -32,7 +32,8 @@ EXPORTED = ("silu_dot_fwd_bwd_quant_fuse", "silu_dot_fwd_bwd_quant_fuse_fp8", "s
             "kquant_swiglu_q8_1_rows", "i8_gemm_group_scaled", "siluquant_prepare", "siluquant_strerror", "siluquant_algorithmic_bytes",
             "siluquant_eval_sigmoid", "siluquant_eval_intermediates", "rms_norm_quant", "rms_norm_bwd",
             "rms_norm_bwd_workspace_bytes", "mxfp4_quant", "mxfp4_gemm", "mxfp4_dequant", "group_dequant",
-            "dropout_add", "layer_norm_quant", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes")
+            "dropout_add", "layer_norm_quant", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "swiglu_gemm",
+            "swiglu_gemm_bwd", "swiglu_gemm_bwd_workspace_bytes")
 
 _lib = None
 
@@ -75,10 +76,14 @@ def lib() -> ctypes.CDLL:
                          (L.layer_norm_quant, [vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, cf, cf, vp,
                                                i64, vp]),
                          (L.layer_norm_bwd, [vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, cf, vp, i64,
-                                             vp])):
+                                             vp]),
+                         (L.swiglu_gemm, [vp, vp, vp, vp, i64, i64, i64, vp]),
+                         (L.swiglu_gemm_bwd, [vp, vp, vp, vp, vp, vp, ci, vp, ci, vp, i64, i64, i64, i64, vp])):
             fn.argtypes, fn.restype = args, ci
         for fn in (L.rms_norm_bwd_workspace_bytes, L.layer_norm_bwd_workspace_bytes):
             fn.argtypes, fn.restype = [i64, i64], i64
+        L.swiglu_gemm_bwd_workspace_bytes.argtypes = [i64, i64, i64]
+        L.swiglu_gemm_bwd_workspace_bytes.restype = i64
         L.siluquant_eval_sigmoid.argtypes = [vp, vp, i64, vp]
         L.siluquant_eval_sigmoid.restype = ctypes.c_int
         L.siluquant_eval_intermediates.argtypes = [vp, vp, vp, vp, i64, i64, vp]
@@ -576,7 +581,7 @@ def group_dequant(q, s, out, group_size: int = GROUP):
              fmt)
 
 
-# ---- the same block in bf16: layer norm, dropout ----
+# ---- the same block in bf16: layer norm, dropout, gated projection ----
 
 
 def _want_drop(p, rng, offset, idx):
@@ -692,6 +697,59 @@ def layer_norm_bwd(dy, h, weight, mean, rstd, dx, dw=None, db=None, d_h=None, dx
     _enqueue(lib().layer_norm_bwd, "layer_norm_bwd", idx, dy.data_ptr(), F32 if dy.dtype is _f32 else BF16, h.data_ptr(),
              weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(d_h), dx.data_ptr(), _ptr(dx_drop), _ptr(dw),
              _ptr(db), _ptr(workspace), _workspace(workspace, idx), T, D, p, _ptr(rng), offset)
+
+
+def swiglu_gemm(x, w, y, gu=None):
+    """y = silu(x Wg^T) * (x Wu^T), both projections, the activation and the product
+    in one kernel: x bf16 [T, D], w = [Wg; Wu] bf16 [2H, D], y bf16 [T, H]
+    overwritten; gu bf16 [T, 2H], where given, receives [gate | up], which the
+    backward pass needs.  H and D are multiples of 8.  Enqueued on the current
+    stream of x's device; returns None."""
+    T, D, idx = _rank2("x", x)
+    rows = _rank2("w", w)[0]
+    H = rows // 2
+    if rows % 2 or H % 8 or D % 8:
+        raise ValueError("w must be [2H, D] with H and D multiples of 8, got shape %s" % (tuple(w.shape),))
+    _want("x", x, _bf16, (T, D), idx)
+    _want("w", w, _bf16, (rows, D), idx)
+    _want("y", y, _bf16, (T, H), idx)
+    if gu is not None:
+        _want("gu", gu, _bf16, (T, rows), idx)
+    _enqueue(lib().swiglu_gemm, "swiglu_gemm", idx, x.data_ptr(), w.data_ptr(), y.data_ptr(), _ptr(gu), T, H, D)
+
+
+def swiglu_gemm_bwd_workspace(T: int, H: int, D: int, device):
+    """A workspace tensor for swiglu_gemm_bwd at this size (any larger one will do); may be empty."""
+    import torch
+
+    n = int(lib().swiglu_gemm_bwd_workspace_bytes(int(T), int(H), int(D)))
+    if n < 0:
+        raise ValueError("no such size: T=%d H=%d D=%d" % (T, H, D))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def swiglu_gemm_bwd(dy, gu, x, w, d_gu, dx=None, dw=None, workspace=None):
+    """Gradients of swiglu_gemm: d_gu bf16 [T, 2H] for [gate | up] (may be gu itself),
+    dx bf16 or fp32 [T, D] = d_gu W and dw bf16 or fp32 [2H, D] = d_gu^T x, each where
+    given.  dy bf16 [T, H]; gu, x, w as in the forward call.  workspace: from
+    swiglu_gemm_bwd_workspace.  Enqueued on the current stream of dy's device;
+    returns None."""
+    T, H, idx = _rank2("dy", dy)
+    D = _rank2("x", x)[1]
+    if H % 8 or D % 8:
+        raise ValueError("H and D must be multiples of 8, got %d and %d" % (H, D))
+    _want("dy", dy, _bf16, (T, H), idx)
+    _want("gu", gu, _bf16, (T, 2 * H), idx)
+    _want("x", x, _bf16, (T, D), idx)
+    _want("w", w, _bf16, (2 * H, D), idx)
+    _want("d_gu", d_gu, _bf16, (T, 2 * H), idx)
+    if dx is not None:
+        _want2("dx", dx, _bf16, _f32, (T, D), idx)
+    if dw is not None:
+        _want2("dw", dw, _bf16, _f32, (2 * H, D), idx)
+    _enqueue(lib().swiglu_gemm_bwd, "swiglu_gemm_bwd", idx, dy.data_ptr(), gu.data_ptr(), x.data_ptr(), w.data_ptr(),
+             d_gu.data_ptr(), _ptr(dx), F32 if dx is not None and dx.dtype is _f32 else BF16, _ptr(dw),
+             F32 if dw is not None and dw.dtype is _f32 else BF16, _ptr(workspace), _workspace(workspace, idx), T, H, D)
 
 
 def empty_outputs(T: int, H: int, device, group: int = GROUP, fp8: bool = False):

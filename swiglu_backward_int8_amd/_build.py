@@ -2,7 +2,7 @@
 
 sigmoid_table.py writes the kernels' sigmoid table into _build/, then hipcc
 compiles the HIP sources (the fused SwiGLU passes, the group-scaled int8 GEMM,
-the norms, the dropout and the microscaled 4-bit operators) into one shared
+the norms, the dropout, the gated projection and the microscaled 4-bit operators) into one shared
 library next to this file.
 Flags that matter for the numbers the library produces:
   -ffp-contract=off                  no fused multiply-add: the arithmetic order
@@ -23,7 +23,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 GEN = os.path.join(PKG, "_build")  # generated sources (not tracked)
 SRCS = [os.path.join(PKG, "csrc", n + ".hip") for n in ("siluquant", "i8gemm", "rmsnorm", "mxfp4", "mxfp4gemm",
-                                                               "layernorm")]
+                                                               "layernorm", "swiglugemm")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsiluquant.so")
 ARCH = "gfx950"

@@ -21,6 +21,7 @@ __attribute__((visibility("hidden"))) hipError_t load_rmsnorm();
 __attribute__((visibility("hidden"))) hipError_t load_mxfp4();
 __attribute__((visibility("hidden"))) hipError_t load_mxfp4gemm();
 __attribute__((visibility("hidden"))) hipError_t load_layernorm();
+__attribute__((visibility("hidden"))) hipError_t load_swiglugemm();
 
 }  // namespace code_objects
 

@@ -2932,7 +2932,7 @@ __attribute__((visibility("default"))) int siluquant_prepare(void) {
   using namespace code_objects;
   if (load(silu_quant_bwd_kernel<Fmt::kInt8, 128>) != hipSuccess || load_i8gemm() != hipSuccess ||
       load_rmsnorm() != hipSuccess || load_mxfp4() != hipSuccess || load_mxfp4gemm() != hipSuccess ||
-      load_layernorm() != hipSuccess)
+      load_layernorm() != hipSuccess || load_swiglugemm() != hipSuccess)
     return SILUQUANT_ERR_DEVICE;
   return SILUQUANT_OK;
 }
