@@ -106,79 +106,551 @@ __global__ __launch_bounds__(256) void swiglu_gate_bwd_kernel(const GateArgs a) 
 }
 
 // ---- products ----
+//
+// C [M, N] = sum over k of A[m, k] * B[n, k].  An operand is stored by rows, [rows,
+// K], or by k, [K, rows]; the three products of this file are
+//   kGated  A = x by rows,    B = the rows of Wg and Wu, whose results meet in a lane
+//   kDx     A = d_gu by rows, B = W by k
+//   kDw     A = d_gu by k,    B = x by k
+enum Product { kGated = 0, kDx = 1, kDw = 2 };
 
-// C [M, N] = sum over k of A[m, k] * B[n, k].  A k-major operand is stored as [K,
-// rows]; the others as [rows, K].  ld: elements from one stored row to the next.
 struct GemmArgs {
-  const uint16_t *A, *B, *B2;  // B2: the up projection's rows (forward)
+  const uint16_t *A, *B;
   void* C;
-  uint16_t* gu;  // forward: [M, 2N], may be null
-  int64_t M, N, K;
-  int64_t lda, ldb;
+  uint16_t* gu;    // kGated: [M, 2N], may be null
+  int64_t M, N, K;  // kGated: N = H, half the rows of B
+  int lda, ldb;    // elements from one stored row to the next
+  int tiles_m, tiles_n;
 };
 
-constexpr int kStep = 32, kPitch = kStep + 8;  // values of K per step; a row in LDS
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-template <bool kKMajor>
-__device__ __forceinline__ void stage(uint16_t* to, const uint16_t* from, int64_t ld, int64_t row0, int64_t rows, int64_t k0,
-                                      int64_t K) {
-  for (int i = threadIdx.x; i < 64 * kStep; i += 256) {
-    const int r = kKMajor ? i & 63 : i / kStep, k = kKMajor ? i >> 6 : i % kStep;
-    uint16_t v = 0;
-    if (row0 + r < rows && k0 + k < K) v = kKMajor ? from[(k0 + k) * ld + row0 + r] : from[(row0 + r) * ld + k0 + k];
-    to[r * kPitch + k] = v;
-  }
+// ---- tiles through LDS ----
+//
+// A workgroup owns a tile of kTileA x kTileB results, its waves (2 x kWavesB) kFA x
+// kFB blocks of 32 x 32 each.  A stage is 64 values of k of every row of the tile: it
+// goes from memory straight into LDS (buffer loads with the lds flag), double
+// buffered.
+//
+// An operand stored by rows lies in LDS as rows of 128 bytes, eight 16-byte chunks,
+// chunk c of row r at c ^ swz(r): the 16 lanes that read a chunk of consecutive rows
+// fall on distinct banks.  One stored by k lies there as 64 rows of its tile's width;
+// the transposing LDS reads hand a lane four k of its column, 16 lanes reading 32
+// bytes of each of four rows, and runs of 64 bytes of row r are exchanged by r & 3, so
+// that the 32 lanes that are served together fall on all banks.
+//
+// The order of k within a sum is free as long as A and B agree: lane half h takes
+// k = 8 (4 h + j) .. + 7 of a stage in step j, which is chunk 4 h + j of a row.
+constexpr int kStageK = 64, kRowBytes = 2 * kStageK;
+constexpr int kRasterRows = 4;  // tile rows that are walked column by column together
+
+__device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+// Buffer resource words: base, 32-bit record count (loads at or past it read as
+// zeros), raw addressing.
+__device__ __forceinline__ i32x4 rsrc_words(uint64_t base, int bytes) {
+  return (i32x4){__builtin_amdgcn_readfirstlane((int)(uint32_t)base), __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xFFFF),
+                 __builtin_amdgcn_readfirstlane(bytes), 0x00020000};
 }
 
-template <bool kAk, bool kBk, bool kGated, bool kF32>
-__global__ __launch_bounds__(256) void swiglu_simple_kernel(const GemmArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t s_a[64 * kPitch], s_b[(kGated ? 2 : 1) * 64 * kPitch];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32, lrow = lane & 31, half = lane >> 5;
-  const int64_t tiles_n = (a.N + 63) / 64;
-  const int64_t m0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * 64;
-  f32x16 acc = {}, up = {};
-  for (int64_t k0 = 0; k0 < a.K; k0 += kStep) {
-    stage<kAk>(s_a, a.A, a.lda, m0, a.M, k0, a.K);
-    stage<kBk>(s_b, a.B, a.ldb, n0, a.N, k0, a.K);
-    if (kGated) stage<kBk>(s_b + 64 * kPitch, a.B2, a.ldb, n0, a.N, k0, a.K);
-    __syncthreads();
+// Each lane reads 16 bytes at voff + soff (voff is checked against the record
+// count, each 4 bytes for themselves); the wave writes them, lane by lane, to
+// consecutive LDS bytes from address lds (M0) on.  Written as asm so that the
+// compiler does not wait for them before every LDS read; the kernel waits itself.
+// The leading s_nop gives the wait states that the compiler cannot, since it does
+// not look inside: one between the write of M0 and its use; and, with kSlow, five
+// between a vector instruction's write of a scalar register and a load that reads it.
+template <bool kSlow>
+__device__ __forceinline__ void lds_load16(i32x4 rs, uint32_t lds, uint32_t voff, uint32_t soff) {
+  if (kSlow)
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                   "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory");
+  else
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rs), "s"(__builtin_amdgcn_readfirstlane(soff)),
+                   "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory");
+}
+
+// Four k of a lane's column; p: the lane's 8 bytes of the 32 that 4 lanes read of a row.
+__device__ __forceinline__ u32x2 read_transposed(const char* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (__attribute__((address_space(3))) s16x4*)p));
+}
+
+__device__ __forceinline__ f32x16 mfma(const u32x4& a, const u32x4& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <int kFA, int kWavesB, int kBufs>
+struct TileShape {
+  static constexpr int kFB = 4;
+  static constexpr int kWaves = 2 * kWavesB, kThreads = 64 * kWaves;
+  static constexpr int kTileA = 64 * kFA, kTileB = 32 * kWavesB * kFB;  // rows of A and of B
+  static constexpr int kStage = (kTileA + kTileB) * kRowBytes;
+  static constexpr int kPerCu = 2 * kBufs * kStage <= 160 * 1024 ? 2 : 1;  // workgroups that fit a CU's LDS
+  static constexpr int kPerSimd = kPerCu * kWaves < 4 ? 1 : kPerCu * kWaves / 4;         // waves
+};
+
+// Where an operand's stage comes from.  By rows: the resource stays, k advances with
+// the scalar offset.  By k: the base advances, and the record count ends at K.
+template <bool kByK>
+struct Source {
+  i32x4 rs;
+  uint32_t soff;
+  // by k:
+  uint64_t base;
+  uint32_t step;         // bytes from one stage to the next
+  int left;              // stages, this one among them
+  int all, last;         // record counts: of a stage, and of the one in which K ends
+  __device__ __forceinline__ void by_rows(const uint16_t* p, int64_t row, int rows, int64_t row_bytes) {
+    rs = rsrc_words(reinterpret_cast<uint64_t>(p) + row * row_bytes, (int)(rows * row_bytes));
+    soff = 0;
+  }
+  __device__ __forceinline__ void count() { rs = rsrc_words(base, left > 1 ? all : left == 1 ? last : 0); }
+  __device__ __forceinline__ void by_k(const uint16_t* p, int64_t column, int64_t K, int row_bytes) {
+    const int from = (int)(2 * column);  // into a row
+    base = reinterpret_cast<uint64_t>(p) + from;
+    step = (uint32_t)(kStageK * row_bytes);
+    left = (int)((K + kStageK - 1) / kStageK);
+    all = kStageK * row_bytes - from, last = (int)(K - (int64_t)(left - 1) * kStageK) * row_bytes - from;
+    soff = 0;
+    count();
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (kByK) {
+      base += step, --left;
+      count();
+    } else {
+      soff += kRowBytes;
+    }
+  }
+  __device__ __forceinline__ void none() { rs.z = 0, left = 0; }  // reads zeros from here on
+};
+
+template <int kFA, int kWavesB, int kBufs, Product kProduct, bool kKeep, bool kF32>
+__global__ __launch_bounds__(128 * kWavesB, (TileShape<kFA, kWavesB, kBufs>::kPerSimd)) void
+swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
+  using Shape = TileShape<kFA, kWavesB, kBufs>;
+  constexpr int kFB = Shape::kFB, kWaves = Shape::kWaves, kTileA = Shape::kTileA, kTileB = Shape::kTileB;
+  constexpr bool kAByK = kProduct == kDw, kBByK = kProduct != kGated;
+  constexpr int kStage = Shape::kStage;                     // A's bytes, then B's
+  constexpr int kLoadsA = kTileA / 8 / kWaves, kLoadsB = kTileB / 8 / kWaves;  // wave-wide loads of 1 KB per stage
+  constexpr int kLoads = kLoadsA + kLoadsB;
+  constexpr int kTileN = kProduct == kGated ? kTileB / 2 : kTileB;             // columns of C
+  __shared__ __attribute__((aligned(16))) char s_tile[kBufs * kStage];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave / kWavesB) * 32 * kFA, wn = (wave % kWavesB) * 32 * kFB;
+  const int lrow = lane & 31, half = lane >> 5;
+  const int stages = (int)((a.K + kStageK - 1) / kStageK);
+
+  // Each XCD takes a contiguous range of tiles, in groups of kRasterRows tile rows
+  // walked column by column, so that the tiles resident on one XCD share their
+  // operands in its L2.
+  int64_t m0, n0;
+  int rows_a, rows_n;
+  Source<kAByK> sa;
+  Source<kBByK> sb;
+  Source<false> sb2;  // the up projection's rows
+  auto tile_at = [&](int group, int in_group) {
+    const int first_m = group * kRasterRows;
+    const int gsz = min(a.tiles_m - first_m, kRasterRows);
+    const int tn = gsz == 4 ? in_group >> 2 : gsz == 2 ? in_group >> 1 : gsz == 1 ? in_group : in_group / 3;
+    m0 = (int64_t)(first_m + in_group - tn * gsz) * kTileA, n0 = (int64_t)tn * kTileN;
+    rows_a = a.M - m0 < kTileA ? (int)(a.M - m0) : kTileA;
+    rows_n = a.N - n0 < kTileN ? (int)(a.N - n0) : kTileN;
+    if constexpr (kAByK)
+      sa.by_k(a.A, m0, a.K, 2 * a.lda);
+    else
+      sa.by_rows(a.A, m0, rows_a, 2ll * a.lda);
+    if constexpr (kBByK) {
+      sb.by_k(a.B, n0, a.K, 2 * a.ldb);
+    } else {
+      sb.by_rows(a.B, n0, rows_n, 2ll * a.ldb);
+      sb2.by_rows(a.B, a.N + n0, rows_n, 2ll * a.ldb);
+    }
+  };
+  static_assert(kRasterRows == 4, "tile_at divides by 1 to 4");
+  const int slots = gridDim.x >> 3, first_tile = (blockIdx.x & 7) * per_xcd;
+  const int end_tile = min(first_tile + per_xcd, a.tiles_m * a.tiles_n);
+  int at_tile = first_tile + (blockIdx.x >> 3);
+  if (at_tile >= end_tile) return;
+  const int per_group = kRasterRows * a.tiles_n;
+  int group = at_tile / per_group, in_group = at_tile - group * per_group;
+  tile_at(group, in_group);
+
+  // A wave's load i of an operand fills 1 KB of LDS, lane L its bytes 16 L and on.
+  // By rows: eight rows; lane L writes row L / 8, physical chunk L % 8, and so reads
+  // chunk (L % 8) ^ swz.  By k: the rows that 1 KB holds, runs of four chunks exchanged
+  // by the row.  Where gate and up rows share a tile, the loads take them in turn, and
+  // the rows lie so that a wave's 32 kFB rows are its gate columns and then the same
+  // up columns.
+  auto row_of_b = [&](int i) {  // LDS row of B's load i
+    if constexpr (kProduct == kGated) {
+      const int col = 8 * ((i >> 1) + kLoadsB / 2 * wave);
+      return (col / (16 * kFB)) * 32 * kFB + (i & 1) * 16 * kFB + col % (16 * kFB);
+    } else {
+      return 8 * (kLoadsB * wave + i);
+    }
+  };
+  uint32_t voff_a[kLoadsA], voff_b[kLoadsB], past_a = 0, past_b = 0;
+  auto place = [&](bool by_k, int lds_row, int global_row, int width, int ld, uint32_t& voff, uint32_t& past, int i) {
+    if (by_k) {
+      const int byte = 128 * lds_row + 16 * lane, k = byte / width, c = (byte % width / 16) ^ (4 * (k & 3));
+      voff = (uint32_t)(2 * k * ld + 16 * c);
+    } else {
+      const int c = (lane & 7) ^ swz(lds_row + (lane >> 3));
+      voff = (uint32_t)((global_row + (lane >> 3)) * 2 * ld + 16 * c);
+      past |= (uint32_t)((stages - 1) * kStageK + 8 * c >= a.K) << i;  // in the last stage
+    }
+  };
 #pragma unroll
-    for (int j = 0; j < kStep; j += 16) {
-      const bf16x8 fa = *reinterpret_cast<const bf16x8*>(s_a + (wm + lrow) * kPitch + j + 8 * half);
-      const bf16x8 fb = *reinterpret_cast<const bf16x8*>(s_b + (wn + lrow) * kPitch + j + 8 * half);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb, fa, acc, 0, 0, 0);
-      if (kGated) {
-        const bf16x8 fu = *reinterpret_cast<const bf16x8*>(s_b + (64 + wn + lrow) * kPitch + j + 8 * half);
-        up = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fu, fa, up, 0, 0, 0);
+  for (int i = 0; i < kLoadsA; ++i) {
+    const int r = 8 * (kLoadsA * wave + i);
+    place(kAByK, r, r, 2 * kTileA, a.lda, voff_a[i], past_a, i);
+  }
+#pragma unroll
+  for (int i = 0; i < kLoadsB; ++i)
+    place(kBByK, row_of_b(i), 8 * ((i >> 1) + kLoadsB / 2 * wave), 2 * kTileB, a.ldb, voff_b[i], past_b, i);
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(&s_tile[0]);
+  // Load l of stage s, for which the sources stand.  Bit i of `past` sends load i of an
+  // operand stored by rows past the record count, where zeros are read: chunks past K,
+  // and all of a stage past the last one (its zeros land in a buffer that nobody
+  // reads; the loop below has no branches but its own).
+  auto past_of = [&](int s, uint32_t last) { return s < stages - 1 ? 0u : s == stages - 1 ? last : ~0u; };
+  auto issue = [&](auto slow, int s, int l) {
+    constexpr bool kSlow = decltype(slow)::value;
+    const uint32_t at = lds0 + (s & (kBufs - 1)) * kStage;
+    // A's and B's loads in turn as long as there are both
+    constexpr int kPairs = kLoadsA < kLoadsB ? kLoadsA : kLoadsB;
+    const bool of_b = l < 2 * kPairs ? l & 1 : kLoadsB > kLoadsA;
+    const int i = l < 2 * kPairs ? l >> 1 : l - kPairs;
+    if (of_b) {
+      const uint32_t off = kBByK ? voff_b[i] : voff_b[i] | ((past_of(s, past_b) << (31 - i)) & 0x80000000u);
+      const uint32_t to = at + kTileA * kRowBytes + row_of_b(i) * kRowBytes;
+      if (kProduct == kGated && (i & 1))
+        lds_load16<kSlow>(sb2.rs, to, off, sb.soff);
+      else
+        lds_load16<kSlow>(sb.rs, to, off, sb.soff);
+    } else {
+      const uint32_t off = kAByK ? voff_a[i] : voff_a[i] | ((past_of(s, past_a) << (31 - i)) & 0x80000000u);
+      lds_load16<kSlow>(sa.rs, at + 8 * (kLoadsA * wave + i) * kRowBytes, off, sa.soff);
+    }
+  };
+  auto advance = [&] { sa.advance(), sb.advance(); };
+
+  // Step j of a stage reads k = 8 (4 half + j) .. + 7 of the wave's rows.  By rows:
+  // chunk 4 half + j; block i's row is 32 i further, which flips bit 2 of the chunk for
+  // odd i.  By k: rows 32 half + 8 j and on, in two reads of four; block i is 64 i bytes
+  // further, exchanged like the runs.
+  auto base_of = [&](bool by_k, int w0, int width) {
+    if (by_k) {
+      const int r = (lane >> 2) & 3;
+      return (32 * half + r) * width + 64 * ((w0 / 32) ^ r) + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+    }
+    return (w0 + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(w0 + lrow));
+  };
+  const int base_a = base_of(kAByK, wm, 2 * kTileA), base_b = kTileA * kRowBytes + base_of(kBByK, wn, 2 * kTileB);
+  static_assert(kTileA * kRowBytes % 512 == 0, "B's offset leaves the bits that are exchanged alone");
+  u32x4 fa[2][kFA], fb[2][kFB];
+  constexpr int kReads = kFA + kFB;
+  // Read n of a step's operands, in the order in which they are needed.
+  auto read = [&](int s, int j, int n) {
+    const char* t = s_tile + (s & (kBufs - 1)) * kStage;
+    const bool of_b = n != 1 && n <= kFB;
+    const int i = n == 0 || n == 1 ? 0 : of_b ? n - 1 : n - kFB;
+    u32x4& to = of_b ? fb[j & 1][i] : fa[j & 1][i];
+    const int base = of_b ? base_b : base_a;
+    if (of_b ? kBByK : kAByK) {
+      const int width = 2 * (of_b ? kTileB : kTileA);
+      const u32x2 lo = read_transposed(t + (base ^ (64 * i)) + 8 * j * width), hi = read_transposed(t + (base ^ (64 * i)) + (8 * j + 4) * width);
+      to = (u32x4){lo.x, lo.y, hi.x, hi.y};
+    } else {
+      to = *reinterpret_cast<const u32x4*>(t + (base ^ (16 * j) ^ (64 * (i & 1))) + 32 * kRowBytes * i);
+    }
+  };
+
+  f32x16 acc[kFA][kFB];
+
+  // Step j of a stage: its multiplications, and after each of them (32 cycles of
+  // the matrix core, 8 issues of the one wave that feeds it) a little of
+  // everything else, in the order written: reads of the next step's operands,
+  // loads of a later stage.
+  constexpr int kSlots = kFA * kFB;
+  auto step = [&](auto which, auto&& between) {
+    constexpr int j = decltype(which)::value;
+#pragma unroll
+    for (int t = 0; t < kSlots; ++t) {
+      const int i = t / kFB, k = t % kFB;
+      acc[i][k] = mfma(fb[j & 1][k], fa[j & 1][i], acc[i][k]);
+      between(t);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Part n of `of`, spread over a step's slots from slot `from` on: f(n) at its slot.
+  auto spread = [&](int t, int of, int from, auto&& f) {
+#pragma unroll
+    for (int n = 0; n < of; ++n)
+      if (t == std::min(kSlots - 1, n * kSlots / of + from)) f(n);
+  };
+  using std::integral_constant;
+
+  // A tile's first loads: all stages but one of the buffers.
+  constexpr int kFirst = (kBufs - 1) * kLoads;
+  auto start = [&](int l) {
+    if (l > 0 && l % kLoads == 0) advance();
+    issue(std::true_type{}, l / kLoads, l % kLoads);
+  };
+
+  // The results of a wave leave through a patch of LDS (in the last buffer's
+  // place), 32 rows of 128 bytes at a time, two pieces in turn: 16-byte chunk c
+  // of row r at c ^ swz(r), the halves of a chunk swapped for rows with bit 4.
+  constexpr int kPer = kF32 ? 4 : 8;                        // columns per chunk
+  constexpr int kPartsB = kProduct == kGated ? kFB / 2 : 32 * kFB / (8 * kPer);  // runs of columns
+  constexpr int kPieces = kPartsB * kFA;                    // of 32 rows x 128 bytes (gated: two such, of gate and up in fp32)
+  static_assert(kStage / kWaves >= 2 * 32 * 128 * (kProduct == kGated ? 2 : 1), "two pieces fit");
+  char* patch = s_tile + (kBufs - 1) * kStage + wave * (kStage / kWaves);
+  constexpr int kPerPiece = (kFirst + kPieces - 1) / kPieces;  // the next tile's first loads that go out with each piece
+
+#pragma unroll
+  for (int l = 0; l < kFirst; ++l) start(l);
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < kFA; ++i)
+#pragma unroll
+      for (int k = 0; k < kFB; ++k) acc[i][k] = (f32x16){};
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    __syncthreads();
+    // Before the last step of a stage every wave has read all of it: there the
+    // next stage's loads are waited for, and after the barrier the loads of the
+    // stage after it go into the buffer that has just been read, spread over
+    // that last step and the first one of the next stage.
+    advance();
+#pragma unroll
+    for (int l = 0; l < kLoads / 2; ++l) issue(std::true_type{}, kBufs - 1, l);
+#pragma unroll
+    for (int n = 0; n < kReads; ++n) read(0, 0, n);
+#pragma unroll 1
+    for (int s = 0; s < stages; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+      step(integral_constant<int, 0>{}, [&](int t) {
+        spread(t, kReads, 0, [&](int n) { read(s, 1, n); });
+        spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs - 1, kLoads / 2 + l); });
+      });
+      step(integral_constant<int, 1>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(s, 2, n); }); });
+      step(integral_constant<int, 2>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(s, 3, n); }); });
+      // with four buffers the loads of two later stages may be on their way
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"((kBufs - 2) * kLoads) : "memory");
+      __syncthreads();
+      advance();
+      __builtin_amdgcn_sched_barrier(0);
+      step(integral_constant<int, 3>{}, [&](int t) {
+        spread(t, kReads, 0, [&](int n) { read(s + 1, 0, n); });
+        spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs, l); });
+      });
+    }
+    // the loads past the last stage write LDS: they end before it is used again
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+    __syncthreads();
+    const int64_t row0 = m0 + wm, col0 = n0 + (kProduct == kGated ? wn / 2 : wn), rows = a.M - row0, columns = a.N - col0;
+    const bool whole = rows_a == kTileA && rows_n == kTileN;
+    at_tile += slots;
+    const bool more = at_tile < end_tile;
+    if (more) {
+      in_group += slots;
+      while (in_group >= per_group) in_group -= per_group, ++group;
+      tile_at(group, in_group);
+    } else {
+      sa.none(), sb.none(), sb2.none();  // the first loads of no tile read nothing
+    }
+
+    // The B rows come first in the instruction, so that a lane holds four
+    // consecutive columns: D[row 8 q + 4 half + e][column lrow], q = r / 4, e =
+    // r % 4.  A wave's LDS operations are carried out in their order and its patch is
+    // its own, so nothing waits but the stores for what they store.
+    // The lane's number comes anew for every tile: else the compiler computes all
+    // addresses below before the first tile and has no registers left for them.
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    auto put = [&, lrow = l & 31, half = l >> 5](int turn, int i, int part) {
+      char* to = patch + (turn & 1) * 32 * 128 + lrow * 128;
+#pragma unroll
+      for (int k = 0; k < kPer / 4; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& d = acc[i][part * (kPer / 4) + k];
+          if constexpr (kF32)
+            *reinterpret_cast<f32x4*>(to + 16 * ((2 * q + half) ^ swz(lrow))) =
+                (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+          else
+            *reinterpret_cast<u32x2*>(to + 16 * ((4 * k + q) ^ swz(lrow)) + 8 * (half ^ (lrow >> 4))) =
+                (u32x2){pack_bf16(d[4 * q], d[4 * q + 1]), pack_bf16(d[4 * q + 2], d[4 * q + 3])};
+        }
+    };
+    const int r = l >> 3;
+    u32x4 out[2][4] = {};  // set, or else it is kept from tile to tile
+    auto get = [&](int turn) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = 8 * x + r;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(patch + (turn & 1) * 32 * 128 + row * 128 + 16 * ((l & 7) ^ swz(row)));
+        out[turn & 1][x] = !kF32 && x >= 2 ? (u32x4){v.z, v.w, v.x, v.y} : v;
+      }
+    };
+    auto loads = [&](int t) {
+#pragma unroll
+      for (int n = kPerPiece * t; n < kPerPiece * (t + 1); ++n)
+        if (n < kFirst) start(n);
+    };
+    // Whole lines are streamed: left in L2, a round's results drive out the operands.
+    // Rows that start inside lines are not: their lines have to meet in L2.
+    const bool streamed = whole && (a.N * (16 / kPer) & 63) == 0 && (reinterpret_cast<uintptr_t>(a.C) & 63) == 0;
+    auto store = [](char* to, const u32x4& v, bool streamed) {
+      if (streamed)
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
+      else
+        *reinterpret_cast<u32x4*>(to) = v;
+    };
+    if constexpr (kProduct == kGated) {
+      // Gate and up go through LDS as they are; four lanes read a row of 32 columns of
+      // both, eight columns a lane, and store y and what is kept of gate and up.
+      auto put_pair = [&, lrow = l & 31, half = l >> 5](int t) {
+        char* to = patch + (t & 1) * 2 * 32 * 128 + lrow * 128;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& d = acc[t / kPartsB][t % kPartsB + p * kPartsB];
+            *reinterpret_cast<f32x4*>(to + p * 32 * 128 + 16 * ((2 * q + half) ^ swz(lrow))) =
+                (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
+          }
+      };
+      auto finish = [&](int t) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = 16 * x + (l >> 2), down = 32 * (t / kPartsB) + row, column = 32 * (t % kPartsB) + 8 * (l & 3);
+          const char* from = patch + (t & 1) * 2 * 32 * 128 + row * 128;
+          float g[8], u[8], y[8];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int at = 16 * ((2 * (l & 3) + c) ^ swz(row));
+            const f32x4 gv = *reinterpret_cast<const f32x4*>(from + at), uv = *reinterpret_cast<const f32x4*>(from + 32 * 128 + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[4 * c + e] = gv[e], u[4 * c + e] = uv[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = Sigmoid(g[e]).times(g[e]) * u[e];
+          auto pack8 = [](const float (&v)[8]) {
+            return (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+          };
+          if (whole || (down < rows && column < columns)) {  // H is a multiple of 8: whole chunks
+            store(static_cast<char*>(a.C) + ((row0 + down) * a.N + col0 + column) * 2, pack8(y), streamed);
+            if (kKeep) {
+              char* const to = reinterpret_cast<char*>(a.gu) + ((row0 + down) * 2 * a.N + col0 + column) * 2;
+              store(to, pack8(g), streamed);
+              store(to + 2 * a.N, pack8(u), streamed);
+            }
+          }
+        }
+      };
+#pragma unroll
+      for (int t = 0; t <= kPieces; ++t) {
+        if (t < kPieces) loads(t), put_pair(t);
+        if (t > 0) finish(t - 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      // where a lane's chunk of row 0 goes
+      char* const to0 = static_cast<char*>(a.C) + ((row0 + r) * a.N + col0 + kPer * (l & 7)) * (16 / kPer);
+      auto place = [&](int block, int part, int x) { return to0 + (32 * block + 8 * x) * a.N * (16 / kPer) + 128 * part; };
+      auto store_whole = [&](auto streamed) {
+        constexpr bool kStreamed = decltype(streamed)::value;
+        auto row_of = [](int n) { return kStreamed ? n % kFA : n / kPartsB; };
+        auto part_of = [](int n) { return kStreamed ? n / kFA : n % kPartsB; };
+#pragma unroll
+        for (int t = 0; t < kPieces + 2; ++t) {
+          loads(t);
+          if (t < kPieces) put(t, row_of(t), part_of(t));
+          if (t >= 2) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) store(place(row_of(t - 2), part_of(t - 2), x), out[t & 1][x], kStreamed);
+          }
+          if (t >= 1 && t <= kPieces) get(t - 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if (streamed) {
+        store_whole(std::true_type{});
+      } else if (whole) {
+        store_whole(std::false_type{});
+      } else {
+#pragma unroll
+        for (int t = 0; t < kPieces; ++t) {
+          loads(t);
+          put(t, t / kPartsB, t % kPartsB);
+          get(t);
+          const int part = t % kPartsB, first = 32 * (t / kPartsB) + r;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (first + 8 * x < rows && 8 * kPer * part + kPer * (l & 7) < columns)  // N is a multiple of 8: whole chunks
+              store(place(t / kPartsB, part, x), out[t & 1][x], false);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
-    __syncthreads();
+    if (!more) break;
   }
-  const int64_t m = m0 + wm + lrow;
-  auto one = [](float v) { return (uint16_t)pack_bf16(v, 0.0f); };
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int64_t n = n0 + wn + 8 * (r / 4) + 4 * half + r % 4;
-    if (m >= a.M || n >= a.N) continue;
-    if (kGated) {
-      static_cast<uint16_t*>(a.C)[m * a.N + n] = one(Sigmoid(acc[r]).times(acc[r]) * up[r]);
-      if (a.gu) a.gu[m * 2 * a.N + n] = one(acc[r]), a.gu[m * 2 * a.N + a.N + n] = one(up[r]);
-    } else if (kF32) {
-      static_cast<float*>(a.C)[m * a.N + n] = acc[r];
-    } else {
-      static_cast<uint16_t*>(a.C)[m * a.N + n] = one(acc[r]);
-    }
-  }
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // nothing writes LDS after the workgroup's end
 }
 
-template <bool kAk, bool kBk, bool kGated>
-void launch_product(const GemmArgs& a, bool f32, hipStream_t stream) {
-  const dim3 grid((unsigned)(((a.M + 63) / 64) * ((a.N + 63) / 64))), block(256);
-  if (f32)
-    hipLaunchKernelGGL((swiglu_simple_kernel<kAk, kBk, kGated, true>), grid, block, 0, stream, a);
+template <int kFA, int kWavesB, int kBufs, Product kProduct, bool kKeep, bool kF32>
+void launch_tile(GemmArgs a, int cus, hipStream_t stream) {
+  using Shape = TileShape<kFA, kWavesB, kBufs>;
+  a.tiles_m = (int)((a.M + Shape::kTileA - 1) / Shape::kTileA);
+  const int tile_n = kProduct == kGated ? Shape::kTileB / 2 : Shape::kTileB;
+  a.tiles_n = (int)((a.N + tile_n - 1) / tile_n);
+  const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
+  const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * Shape::kPerCu)), block(Shape::kThreads);
+  hipLaunchKernelGGL((swiglu_tile_kernel<kFA, kWavesB, kBufs, kProduct, kKeep, kF32>), grid, block, 0, stream, a, per_xcd);
+}
+
+// Zeros, where there is nothing to sum.
+__global__ __launch_bounds__(256) void swiglu_zero_kernel(u32x4* p, int64_t n) {
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = (u32x4){0, 0, 0, 0};
+}
+void launch_zero(void* p, int64_t bytes, hipStream_t stream) {  // a multiple of 16
+  if (p && bytes > 0)
+    hipLaunchKernelGGL(swiglu_zero_kernel, dim3((unsigned)std::min<int64_t>((bytes / 16 + 255) / 256, 1 << 16)), dim3(256), 0, stream,
+                       static_cast<u32x4*>(p), bytes / 16);
+}
+
+template <Product kProduct, bool kKeep, bool kF32>
+void launch_product(const GemmArgs& a, int cus, hipStream_t stream) {
+  if (a.K == 0) {
+    launch_zero(a.C, a.M * a.N * (kF32 ? 4 : 2), stream);
+    launch_zero(a.gu, 4 * a.M * a.N, stream);
+    return;
+  }
+  const int64_t columns = kProduct == kGated ? 2 * a.N : a.N;
+  auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((columns + t - 1) / t); };
+  if (tiles(256) >= cus)
+    launch_tile<4, 2, 2, kProduct, kKeep, kF32>(a, cus, stream);
   else
-    hipLaunchKernelGGL((swiglu_simple_kernel<kAk, kBk, kGated, false>), grid, block, 0, stream, a);
+    launch_tile<2, 1, 2, kProduct, kKeep, kF32>(a, cus, stream);
+}
+
+bool device_cus(int* cus) {
+  int dev = 0;
+  return hipGetDevice(&dev) == hipSuccess &&
+         hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && *cus > 0;
 }
 
 constexpr int64_t kMaxT = int64_t(1) << 31, kMaxD = int64_t(1) << 20, kMaxH = int64_t(1) << 20;
@@ -208,9 +680,11 @@ __attribute__((visibility("default"))) int swiglu_gemm(const void* x, const void
     for (const Span& i : in)
       if (overlap(o, i)) return SILUQUANT_ERR_OVERLAP;
   if (overlap(out[0], out[1])) return SILUQUANT_ERR_OVERLAP;
-  const uint16_t* wg = static_cast<const uint16_t*>(w);
-  launch_product<false, false, true>({static_cast<const uint16_t*>(x), wg, wg + H * D, y, static_cast<uint16_t*>(gu), T, H, D, D, D},
-                                     false, stream);
+  int cus = 0;
+  if (!device_cus(&cus)) return SILUQUANT_ERR_DEVICE;
+  const GemmArgs a = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), y, static_cast<uint16_t*>(gu), T, H, D,
+                      (int)D, (int)D, 0, 0};
+  gu ? launch_product<kGated, true, false>(a, cus, stream) : launch_product<kGated, false, false>(a, cus, stream);
   return launched();
 }
 
@@ -251,10 +725,16 @@ __attribute__((visibility("default"))) int swiglu_gemm_bwd(const void* dy, const
     const int64_t groups = (T * (H / 8) + 255) / 256;
     hipLaunchKernelGGL(swiglu_gate_bwd_kernel, dim3((unsigned)std::min<int64_t>(groups, 1 << 20)), dim3(256), 0, stream, a);
   }
-  if (dx)
-    launch_product<false, true, false>({d, static_cast<const uint16_t*>(w), nullptr, dx, nullptr, T, D, 2 * H, 2 * H, D}, dx32, stream);
-  if (dw)
-    launch_product<true, true, false>({d, static_cast<const uint16_t*>(x), nullptr, dw, nullptr, 2 * H, D, T, 2 * H, D}, dw32, stream);
+  int cus = 0;
+  if (!device_cus(&cus)) return SILUQUANT_ERR_DEVICE;
+  if (dx) {
+    const GemmArgs a = {d, static_cast<const uint16_t*>(w), dx, nullptr, T, D, 2 * H, (int)(2 * H), (int)D, 0, 0};
+    dx32 ? launch_product<kDx, false, true>(a, cus, stream) : launch_product<kDx, false, false>(a, cus, stream);
+  }
+  if (dw) {
+    const GemmArgs a = {d, static_cast<const uint16_t*>(x), dw, nullptr, 2 * H, D, T, (int)(2 * H), (int)D, 0, 0};
+    dw32 ? launch_product<kDw, false, true>(a, cus, stream) : launch_product<kDw, false, false>(a, cus, stream);
+  }
   return launched();
 }
 
