@@ -121,6 +121,7 @@ struct GemmArgs {
   int64_t M, N, K;  // kGated: N = H, half the rows of B
   int lda, ldb;    // elements from one stored row to the next
   int tiles_m, tiles_n;
+  int64_t split_k;  // values of K per slice, K for one slice; slice blockIdx.y writes its own C [M, N] behind the others'
 };
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -188,13 +189,20 @@ __device__ __forceinline__ f32x16 mfma(const u32x4& a, const u32x4& b, const f32
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-template <int kFA, int kWavesB, int kBufs>
+template <int kFA, int kFB, int kWavesB, int kBufs, bool kGatedTile>
 struct TileShape {
-  static constexpr int kFB = 4;
   static constexpr int kWaves = 2 * kWavesB, kThreads = 64 * kWaves;
   static constexpr int kTileA = 64 * kFA, kTileB = 32 * kWavesB * kFB;  // rows of A and of B
   static constexpr int kStage = (kTileA + kTileB) * kRowBytes;
-  static constexpr int kPerCu = 2 * kBufs * kStage <= 160 * 1024 ? 2 : 1;  // workgroups that fit a CU's LDS
+  // The results' way out: per wave, one or two pieces of 32 rows x 128 bytes (gated: of
+  // gate and of up), in the last buffer's place or in one of their own.
+  static constexpr int kPiece = 32 * 128 * (kGatedTile ? 2 : 1);
+  static constexpr int kTurns = kStage >= 2 * kWaves * kPiece || kFA == 1 ? 2 : 1;
+  static constexpr bool kOwnPatch = kStage < kTurns * kWaves * kPiece;
+  static constexpr bool kUneven = kBufs == 3;  // two buffers of A's, three of B's
+  static constexpr int kBuffers = kUneven ? 2 * kTileA * kRowBytes + 3 * kTileB * kRowBytes : kBufs * kStage;
+  static constexpr int kLds = kBuffers + (kOwnPatch ? kTurns * kWaves * kPiece : 0);
+  static constexpr int kPerCu = 2 * kLds <= 160 * 1024 ? 2 : 1;  // workgroups that fit a CU's LDS
   static constexpr int kPerSimd = kPerCu * kWaves < 4 ? 1 : kPerCu * kWaves / 4;         // waves
 };
 
@@ -234,22 +242,32 @@ struct Source {
   __device__ __forceinline__ void none() { rs.z = 0, left = 0; }  // reads zeros from here on
 };
 
-template <int kFA, int kWavesB, int kBufs, Product kProduct, bool kKeep, bool kF32>
-__global__ __launch_bounds__(128 * kWavesB, (TileShape<kFA, kWavesB, kBufs>::kPerSimd)) void
-swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
-  using Shape = TileShape<kFA, kWavesB, kBufs>;
-  constexpr int kFB = Shape::kFB, kWaves = Shape::kWaves, kTileA = Shape::kTileA, kTileB = Shape::kTileB;
+template <int kFA, int kFB, int kWavesB, int kBufs, Product kProduct, bool kKeep, bool kF32>
+__global__ __launch_bounds__(128 * kWavesB, (TileShape<kFA, kFB, kWavesB, kBufs, kProduct == kGated>::kPerSimd)) void
+swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
+  using Shape = TileShape<kFA, kFB, kWavesB, kBufs, kProduct == kGated>;
+  constexpr int kWaves = Shape::kWaves, kTileA = Shape::kTileA, kTileB = Shape::kTileB;
   constexpr bool kAByK = kProduct == kDw, kBByK = kProduct != kGated;
+  constexpr bool kUneven = Shape::kUneven;
   constexpr int kStage = Shape::kStage;                     // A's bytes, then B's
   constexpr int kLoadsA = kTileA / 8 / kWaves, kLoadsB = kTileB / 8 / kWaves;  // wave-wide loads of 1 KB per stage
   constexpr int kLoads = kLoadsA + kLoadsB;
   constexpr int kTileN = kProduct == kGated ? kTileB / 2 : kTileB;             // columns of C
-  __shared__ __attribute__((aligned(16))) char s_tile[kBufs * kStage];
+  __shared__ __attribute__((aligned(16))) char s_tile[Shape::kLds];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave / kWavesB) * 32 * kFA, wn = (wave % kWavesB) * 32 * kFB;
   const int lrow = lane & 31, half = lane >> 5;
+  GemmArgs a = all;
+  if (kProduct != kGated && kF32 && blockIdx.y > 0) {
+    const int64_t k0 = blockIdx.y * a.split_k;
+    a.A += kAByK ? k0 * a.lda : k0;
+    a.B += k0 * a.ldb;
+    a.C = static_cast<float*>(a.C) + blockIdx.y * a.M * a.N;
+    a.K -= k0;
+  }
+  if (kProduct != kGated && kF32 && a.K > a.split_k) a.K = a.split_k;
   const int stages = (int)((a.K + kStageK - 1) / kStageK);
 
   // Each XCD takes a contiguous range of tiles, in groups of kRasterRows tile rows
@@ -278,6 +296,7 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
       sb2.by_rows(a.B, a.N + n0, rows_n, 2ll * a.ldb);
     }
   };
+  static_assert(!kAByK || kFA > 1, "runs are exchanged among four");
   static_assert(kRasterRows == 4, "tile_at divides by 1 to 4");
   const int slots = gridDim.x >> 3, first_tile = (blockIdx.x & 7) * per_xcd;
   const int end_tile = min(first_tile + per_xcd, a.tiles_m * a.tiles_n);
@@ -326,24 +345,34 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
   // and all of a stage past the last one (its zeros land in a buffer that nobody
   // reads; the loop below has no branches but its own).
   auto past_of = [&](int s, uint32_t last) { return s < stages - 1 ? 0u : s == stages - 1 ? last : ~0u; };
+  auto issue_a = [&](auto slow, int s, uint32_t at, int i) {
+    const uint32_t off = kAByK ? voff_a[i] : voff_a[i] | ((past_of(s, past_a) << (31 - i)) & 0x80000000u);
+    lds_load16<decltype(slow)::value>(sa.rs, at + 8 * (kLoadsA * wave + i) * kRowBytes, off, sa.soff);
+  };
+  auto issue_b = [&](auto slow, int s, uint32_t at, int i) {
+    const uint32_t off = kBByK ? voff_b[i] : voff_b[i] | ((past_of(s, past_b) << (31 - i)) & 0x80000000u);
+    const uint32_t to = at + row_of_b(i) * kRowBytes;
+    if (kProduct == kGated && (i & 1))
+      lds_load16<decltype(slow)::value>(sb2.rs, to, off, sb.soff);
+    else
+      lds_load16<decltype(slow)::value>(sb.rs, to, off, sb.soff);
+  };
+  // Where stage s of an operand lies in LDS.  Three buffers are told by turn_b, the
+  // present stage's (0, 1, 2 in turn).
+  constexpr int kABytes = kTileA * kRowBytes, kBBytes = kTileB * kRowBytes;
+  uint32_t turn_b = 0;
+  auto a_at = [&](int s) { return (uint32_t)(kUneven ? (s & 1) * kABytes : (s & (kBufs - 1)) * kStage); };
+  auto b_at = [&](int s) { return (uint32_t)((s & (kBufs - 1)) * kStage + kABytes); };
+  auto b_turn = [&](uint32_t ahead) {  // of the stage `ahead` (0 to 2) behind the present one
+    const uint32_t t = turn_b + ahead;
+    return 2 * kABytes + (t >= 3 ? t - 3 : t) * kBBytes;
+  };
   auto issue = [&](auto slow, int s, int l) {
-    constexpr bool kSlow = decltype(slow)::value;
-    const uint32_t at = lds0 + (s & (kBufs - 1)) * kStage;
     // A's and B's loads in turn as long as there are both
     constexpr int kPairs = kLoadsA < kLoadsB ? kLoadsA : kLoadsB;
     const bool of_b = l < 2 * kPairs ? l & 1 : kLoadsB > kLoadsA;
     const int i = l < 2 * kPairs ? l >> 1 : l - kPairs;
-    if (of_b) {
-      const uint32_t off = kBByK ? voff_b[i] : voff_b[i] | ((past_of(s, past_b) << (31 - i)) & 0x80000000u);
-      const uint32_t to = at + kTileA * kRowBytes + row_of_b(i) * kRowBytes;
-      if (kProduct == kGated && (i & 1))
-        lds_load16<kSlow>(sb2.rs, to, off, sb.soff);
-      else
-        lds_load16<kSlow>(sb.rs, to, off, sb.soff);
-    } else {
-      const uint32_t off = kAByK ? voff_a[i] : voff_a[i] | ((past_of(s, past_a) << (31 - i)) & 0x80000000u);
-      lds_load16<kSlow>(sa.rs, at + 8 * (kLoadsA * wave + i) * kRowBytes, off, sa.soff);
-    }
+    of_b ? issue_b(slow, s, lds0 + b_at(s), i) : issue_a(slow, s, lds0 + a_at(s), i);
   };
   auto advance = [&] { sa.advance(), sb.advance(); };
 
@@ -358,17 +387,17 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
     }
     return (w0 + lrow) * kRowBytes + 16 * ((4 * half) ^ swz(w0 + lrow));
   };
-  const int base_a = base_of(kAByK, wm, 2 * kTileA), base_b = kTileA * kRowBytes + base_of(kBByK, wn, 2 * kTileB);
-  static_assert(kTileA * kRowBytes % 512 == 0, "B's offset leaves the bits that are exchanged alone");
+  const int base_a = base_of(kAByK, wm, 2 * kTileA), base_b = base_of(kBByK, wn, 2 * kTileB);
   u32x4 fa[2][kFA], fb[2][kFB];
   constexpr int kReads = kFA + kFB;
   // Read n of a step's operands, in the order in which they are needed.
-  auto read = [&](int s, int j, int n) {
-    const char* t = s_tile + (s & (kBufs - 1)) * kStage;
+  // at_a, at_b: where the stage's operands lie.
+  auto read = [&](uint32_t at_a, uint32_t at_b, int j, int n) {
     const bool of_b = n != 1 && n <= kFB;
     const int i = n == 0 || n == 1 ? 0 : of_b ? n - 1 : n - kFB;
     u32x4& to = of_b ? fb[j & 1][i] : fa[j & 1][i];
     const int base = of_b ? base_b : base_a;
+    const char* t = s_tile + (of_b ? at_b : at_a);
     if (of_b ? kBByK : kAByK) {
       const int width = 2 * (of_b ? kTileB : kTileA);
       const u32x2 lo = read_transposed(t + (base ^ (64 * i)) + 8 * j * width), hi = read_transposed(t + (base ^ (64 * i)) + (8 * j + 4) * width);
@@ -404,10 +433,19 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
   using std::integral_constant;
 
   // A tile's first loads: all stages but one of the buffers.
-  constexpr int kFirst = (kBufs - 1) * kLoads;
+  constexpr int kFirst = kUneven ? kLoadsA + 2 * kLoadsB : (kBufs - 1) * kLoads;
   auto start = [&](int l) {
-    if (l > 0 && l % kLoads == 0) advance();
-    issue(std::true_type{}, l / kLoads, l % kLoads);
+    if constexpr (kUneven) {
+      const int b = l - kLoadsA;
+      if (l == kFirst - kLoadsB) sb.advance();
+      if (b < 0)
+        issue_a(std::true_type{}, 0, lds0, l);
+      else
+        issue_b(std::true_type{}, b / kLoadsB, lds0 + 2 * kABytes + b / kLoadsB * kBBytes, b % kLoadsB);
+    } else {
+      if (l > 0 && l % kLoads == 0) advance();
+      issue(std::true_type{}, l / kLoads, l % kLoads);
+    }
   };
 
   // The results of a wave leave through a patch of LDS (in the last buffer's
@@ -416,8 +454,13 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
   constexpr int kPer = kF32 ? 4 : 8;                        // columns per chunk
   constexpr int kPartsB = kProduct == kGated ? kFB / 2 : 32 * kFB / (8 * kPer);  // runs of columns
   constexpr int kPieces = kPartsB * kFA;                    // of 32 rows x 128 bytes (gated: two such, of gate and up in fp32)
-  static_assert(kStage / kWaves >= 2 * 32 * 128 * (kProduct == kGated ? 2 : 1), "two pieces fit");
-  char* patch = s_tile + (kBufs - 1) * kStage + wave * (kStage / kWaves);
+  constexpr int kTurns = Shape::kTurns, kPieceBytes = Shape::kPiece;
+  static_assert(kTurns == 2 || kProduct == kGated, "the others alternate");
+  // uneven: half of the waves in A's second buffer, half in B's third
+  static_assert(!kUneven || (kWaves == 4 && kABytes == kBBytes && kTurns * kPieceBytes <= kABytes / 2), "two waves each");
+  char* patch = s_tile + (Shape::kOwnPatch ? Shape::kBuffers + wave * kTurns * kPieceBytes
+                          : kUneven ? (wave < 2 ? kABytes : 2 * kABytes + kBBytes) + wave * (kABytes / 2)
+                                    : (kBufs - 1) * kStage + wave * (kStage / kWaves));
   constexpr int kPerPiece = (kFirst + kPieces - 1) / kPieces;  // the next tile's first loads that go out with each piece
 
 #pragma unroll
@@ -434,28 +477,60 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
     // stage after it go into the buffer that has just been read, spread over
     // that last step and the first one of the next stage.
     advance();
+    if constexpr (kUneven) {
+      // A's loads are one stage ahead, in its last step; B's two, in the first two.
+      turn_b = 0;
 #pragma unroll
-    for (int l = 0; l < kLoads / 2; ++l) issue(std::true_type{}, kBufs - 1, l);
+      for (int i = 0; i < kLoadsA; ++i) issue_a(std::true_type{}, 1, lds0 + kABytes, i);
 #pragma unroll
-    for (int n = 0; n < kReads; ++n) read(0, 0, n);
+      for (int n = 0; n < kReads; ++n) read(0, b_turn(0), 0, n);
 #pragma unroll 1
-    for (int s = 0; s < stages; ++s) {
-      __builtin_amdgcn_sched_barrier(0);
-      step(integral_constant<int, 0>{}, [&](int t) {
-        spread(t, kReads, 0, [&](int n) { read(s, 1, n); });
-        spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs - 1, kLoads / 2 + l); });
-      });
-      step(integral_constant<int, 1>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(s, 2, n); }); });
-      step(integral_constant<int, 2>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(s, 3, n); }); });
-      // with four buffers the loads of two later stages may be on their way
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"((kBufs - 2) * kLoads) : "memory");
-      __syncthreads();
-      advance();
-      __builtin_amdgcn_sched_barrier(0);
-      step(integral_constant<int, 3>{}, [&](int t) {
-        spread(t, kReads, 0, [&](int n) { read(s + 1, 0, n); });
-        spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs, l); });
-      });
+      for (int s = 0; s < stages; ++s) {
+        const uint32_t now_a = a_at(s), now_b = b_turn(0), next_b = b_turn(1), load_b = lds0 + b_turn(2);
+        __builtin_amdgcn_sched_barrier(0);
+        step(integral_constant<int, 0>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(now_a, now_b, 1, n); });
+          spread(t, kLoadsB / 2, 1, [&](int i) { issue_b(std::false_type{}, s + 2, load_b, i); });
+        });
+        step(integral_constant<int, 1>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(now_a, now_b, 2, n); });
+          spread(t, kLoadsB / 2, 1, [&](int i) { issue_b(std::false_type{}, s + 2, load_b, kLoadsB / 2 + i); });
+        });
+        step(integral_constant<int, 2>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(now_a, now_b, 3, n); }); });
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(kLoadsB) : "memory");
+        __syncthreads();
+        advance();
+        turn_b = turn_b == 2 ? 0 : turn_b + 1;
+        __builtin_amdgcn_sched_barrier(0);
+        step(integral_constant<int, 3>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(a_at(s + 1), next_b, 0, n); });
+          spread(t, kLoadsA, 1, [&](int i) { issue_a(std::false_type{}, s + 2, lds0 + now_a, i); });
+        });
+      }
+    } else {
+#pragma unroll
+      for (int l = 0; l < kLoads / 2; ++l) issue(std::true_type{}, kBufs - 1, l);
+#pragma unroll
+      for (int n = 0; n < kReads; ++n) read(a_at(0), b_at(0), 0, n);
+#pragma unroll 1
+      for (int s = 0; s < stages; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+        step(integral_constant<int, 0>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(a_at(s), b_at(s), 1, n); });
+          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs - 1, kLoads / 2 + l); });
+        });
+        step(integral_constant<int, 1>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(a_at(s), b_at(s), 2, n); }); });
+        step(integral_constant<int, 2>{}, [&](int t) { spread(t, kReads, 0, [&](int n) { read(a_at(s), b_at(s), 3, n); }); });
+        // with four buffers the loads of two later stages may be on their way
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"((kBufs - 2) * kLoads) : "memory");
+        __syncthreads();
+        advance();
+        __builtin_amdgcn_sched_barrier(0);
+        step(integral_constant<int, 3>{}, [&](int t) {
+          spread(t, kReads, 0, [&](int n) { read(a_at(s + 1), b_at(s + 1), 0, n); });
+          spread(t, kLoads / 2, 1, [&](int l) { issue(std::false_type{}, s + kBufs, l); });
+        });
+      }
     }
     // the loads past the last stage write LDS: they end before it is used again
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
@@ -523,7 +598,7 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
       // Gate and up go through LDS as they are; four lanes read a row of 32 columns of
       // both, eight columns a lane, and store y and what is kept of gate and up.
       auto put_pair = [&, lrow = l & 31, half = l >> 5](int t) {
-        char* to = patch + (t & 1) * 2 * 32 * 128 + lrow * 128;
+        char* to = patch + (t & (kTurns - 1)) * kPieceBytes + lrow * 128;
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -537,7 +612,7 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int row = 16 * x + (l >> 2), down = 32 * (t / kPartsB) + row, column = 32 * (t % kPartsB) + 8 * (l & 3);
-          const char* from = patch + (t & 1) * 2 * 32 * 128 + row * 128;
+          const char* from = patch + (t & (kTurns - 1)) * kPieceBytes + row * 128;
           float g[8], u[8], y[8];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -563,8 +638,10 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
       };
 #pragma unroll
       for (int t = 0; t <= kPieces; ++t) {
-        if (t < kPieces) loads(t), put_pair(t);
+        if (t < kPieces) loads(t);
+        if (t < kPieces && kTurns == 2) put_pair(t);
         if (t > 0) finish(t - 1);
+        if (t < kPieces && kTurns == 1) put_pair(t);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -611,15 +688,86 @@ swiglu_tile_kernel(const GemmArgs a, int per_xcd) {
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // nothing writes LDS after the workgroup's end
 }
 
-template <int kFA, int kWavesB, int kBufs, Product kProduct, bool kKeep, bool kF32>
+template <int kFA, int kFB, int kWavesB, int kBufs, Product kProduct, bool kKeep, bool kF32>
 void launch_tile(GemmArgs a, int cus, hipStream_t stream) {
-  using Shape = TileShape<kFA, kWavesB, kBufs>;
+  using Shape = TileShape<kFA, kFB, kWavesB, kBufs, kProduct == kGated>;
   a.tiles_m = (int)((a.M + Shape::kTileA - 1) / Shape::kTileA);
   const int tile_n = kProduct == kGated ? Shape::kTileB / 2 : Shape::kTileB;
   a.tiles_n = (int)((a.N + tile_n - 1) / tile_n);
   const int per_xcd = (int)(((int64_t)a.tiles_m * a.tiles_n + 7) / 8);
-  const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * Shape::kPerCu)), block(Shape::kThreads);
-  hipLaunchKernelGGL((swiglu_tile_kernel<kFA, kWavesB, kBufs, kProduct, kKeep, kF32>), grid, block, 0, stream, a, per_xcd);
+  const dim3 grid(8 * std::min(per_xcd, std::max(1, cus / 8) * Shape::kPerCu), (unsigned)((a.K + a.split_k - 1) / a.split_k)), block(Shape::kThreads);
+  hipLaunchKernelGGL((swiglu_tile_kernel<kFA, kFB, kWavesB, kBufs, kProduct, kKeep, kF32>), grid, block, 0, stream, a, per_xcd);
+}
+
+// ---- few rows: operands straight from memory into registers ----
+//
+// The gated product of up to 16 rows of x.  A workgroup owns 16 rows of Wg and the same
+// of Wu; its waves take K 128 values at a time in turn, and their sums meet in LDS.
+// Nothing is shared between waves, so nothing waits: the weight streams through
+// once, 64 bytes of a row with each load, a line with two.  Rows past M or N are read
+// as the last row and not stored.
+constexpr int kStreamK = 128, kStreamWaves = 8;
+template <bool kKeep>
+__global__ __launch_bounds__(64 * kStreamWaves) void swiglu_stream_kernel(const GemmArgs a) {
+  __shared__ f32x4 s_sum[kStreamWaves - 1][2][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, kb = lane >> 4;
+  const int64_t n0 = 16ll * blockIdx.x, row = n0 + r < a.N ? n0 + r : a.N - 1;
+  const uint16_t* const from_g = a.B + row * a.ldb + 8 * kb;
+  const uint16_t* const from_u = a.B + (a.N + row) * a.ldb + 8 * kb;
+  const uint16_t* const from_x = a.A + (r < a.M ? r : a.M - 1) * a.lda + 8 * kb;
+  f32x4 gate = {}, up = {};
+  auto chunk = [&](int64_t k0, auto whole) {
+    u32x4 fg[4], fu[4], fx[4];
+    auto load = [&](const uint16_t* p, int j) {
+      if (decltype(whole)::value || k0 + 32 * j + 8 * kb < a.K) return *reinterpret_cast<const u32x4*>(p + k0 + 32 * j);  // K is a multiple of 8
+      return (u32x4){0, 0, 0, 0};
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fg[j] = load(from_g, j), fu[j] = load(from_u, j);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fx[j] = load(from_x, j);
+    // The weight's rows come first in the instruction: a lane holds four columns of C.
+    auto mfma16 = [](const u32x4& a, const u32x4& b, const f32x4& c) {
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) gate = mfma16(fg[j], fx[j], gate), up = mfma16(fu[j], fx[j], up);
+  };
+  const int64_t whole = a.K / kStreamK;
+  for (int64_t c = wave; c < whole; c += kStreamWaves) chunk(c * kStreamK, std::true_type{});
+  if (a.K % kStreamK != 0 && whole % kStreamWaves == wave) chunk(whole * kStreamK, std::false_type{});
+  if (wave > 0) s_sum[wave - 1][0][lane] = gate, s_sum[wave - 1][1][lane] = up;
+  __syncthreads();
+  if (wave > 0) return;
+  for (int v = 0; v < kStreamWaves - 1; ++v) gate += s_sum[v][0][lane], up += s_sum[v][1][lane];
+  const int64_t n = n0 + 4 * kb;
+  if (r >= a.M || n >= a.N) return;
+  f32x4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = Sigmoid(gate[e]).times(gate[e]) * up[e];
+  auto pack4 = [](const f32x4& v) { return (u32x2){pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)}; };
+  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.C) + r * a.N + n) = pack4(y);
+  if (kKeep) {
+    *reinterpret_cast<u32x2*>(a.gu + r * 2 * a.N + n) = pack4(gate);
+    *reinterpret_cast<u32x2*>(a.gu + r * 2 * a.N + a.N + n) = pack4(up);
+  }
+}
+
+// ---- slices of K joined ----
+
+// out = the sum of the slices' fp32 results, in their order; n values, a multiple of 8.
+template <bool kF32>
+__global__ __launch_bounds__(256) void swiglu_join_kernel(const float* part, void* out, int slices, int64_t n) {
+  for (int64_t i = 4 * (blockIdx.x * 256ll + threadIdx.x); i < n; i += 4 * gridDim.x * 256ll) {
+    f32x4 sum = *reinterpret_cast<const f32x4*>(part + i);
+    for (int s = 1; s < slices; ++s) sum += *reinterpret_cast<const f32x4*>(part + s * n + i);
+    if (kF32)
+      *reinterpret_cast<f32x4*>(static_cast<float*>(out) + i) = sum;
+    else
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i) = (u32x2){pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w)};
+  }
 }
 
 // Zeros, where there is nothing to sum.
@@ -632,19 +780,96 @@ void launch_zero(void* p, int64_t bytes, hipStream_t stream) {  // a multiple of
                        static_cast<u32x4*>(p), bytes / 16);
 }
 
+// Which tiles a product of C [M, columns] over K takes (columns: the stored rows of B
+// that it reads, 2H for the gated one), and in how many slices of K.
+struct Plan {
+  enum Tiles { k256, k128, k128Two, k64 } tiles;
+  int slices;
+};
+//
+// The times that decide are measured ones, in us: tiles of 256 x 256 take 1.0 a stage
+// on an idle chip and 1.4 where every CU has one, and 7 for their ends; the others
+// 0.5 to 0.58, 0.68 to 1.13 (two a CU) and 0.4 to 0.45.  Per kernel, all four measured
+// (256, 128, 128 two a CU, 64 x 128): dx of 512 x 22016 x 4096 before slices 514, 200,
+// 326, 153 us; dw of 22016 x 4096 x 1024 172, 225, 195 us; gated 777 x 1376 x 2048 44, 19,
+// 25, 27 us, 300 x 1376 x 2048 44, 18.5, 24, 14.5 us.
+Plan plan(int64_t M, int64_t columns, int64_t K, bool by_k, bool sliced) {
+  constexpr double kCus = 256;
+  const double stages = (double)((K + kStageK - 1) / kStageK);
+  Plan best = {Plan::k256, 1};
+  double least = 1e300;
+  // per_cu: workgroups at once; stage, full: us of a stage alone and what it takes more when every place is taken;
+  // tile: us of a tile's ends
+  auto look = [&](Plan::Tiles t, int tm, int tn, int per_cu, double stage, double full, double tile) {
+    const double tiles = (double)((M + tm - 1) / tm) * (double)((columns + tn - 1) / tn);
+    for (int slices = 1; slices <= (sliced ? 16 : 1); slices *= 2) {
+      if (slices > 1 && (stages < 4 * slices || tiles * slices > per_cu * kCus)) break;
+      const double busy = tiles * slices / (per_cu * kCus), rounds = __builtin_ceil(busy);
+      double us = rounds * (__builtin_ceil(stages / slices) * (stage + full * std::min(1.0, busy)) + tile);
+      if (slices > 1) us += 4.0 + (4.0 * slices + 4.0) * (double)M * (double)columns / 3e6;
+      if (us < least) least = us, best = {t, slices};
+    }
+  };
+  look(Plan::k256, 256, 256, 1, 1.0, 0.4, 7.0);
+  look(Plan::k128, 128, 128, 1, 0.5, 0.08, 2.1);
+  look(Plan::k128Two, 128, 128, 2, 0.68, 0.45, 2.0);
+  if (!by_k) look(Plan::k64, 64, 128, 1, 0.4, 0.05, 1.5);
+  return best;
+}
+
 template <Product kProduct, bool kKeep, bool kF32>
-void launch_product(const GemmArgs& a, int cus, hipStream_t stream) {
+void launch_tiles(const GemmArgs& a, Plan::Tiles tiles, int cus, hipStream_t stream) {
+  if (tiles == Plan::k256) return launch_tile<4, 4, 2, 3, kProduct, kKeep, kF32>(a, cus, stream);
+  if constexpr (kProduct != kDw) {
+    if (tiles == Plan::k64) return launch_tile<1, 2, 2, 4, kProduct, kKeep, kF32>(a, cus, stream);
+  }
+  if (tiles == Plan::k128Two) return launch_tile<2, 2, 2, 2, kProduct, kKeep, kF32>(a, cus, stream);
+  launch_tile<2, 2, 2, 4, kProduct, kKeep, kF32>(a, cus, stream);
+}
+
+template <bool kKeep>
+void launch_gated(const GemmArgs& a, int cus, hipStream_t stream) {
   if (a.K == 0) {
-    launch_zero(a.C, a.M * a.N * (kF32 ? 4 : 2), stream);
+    launch_zero(a.C, 2 * a.M * a.N, stream);
     launch_zero(a.gu, 4 * a.M * a.N, stream);
     return;
   }
-  const int64_t columns = kProduct == kGated ? 2 * a.N : a.N;
-  auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((columns + t - 1) / t); };
-  if (tiles(256) >= cus)
-    launch_tile<4, 2, 2, kProduct, kKeep, kF32>(a, cus, stream);
+  // Up to 8 rows the stream; up to 16 as long as tiles of 64 x 64 columns would leave half of the CUs without one (H =
+  // 11008, D = 4096: 1 row 36.7 us, tiles 41.4; 8 rows 41.2 and 41.6; 16 rows 46.2 and 41.8; H = 1376, D = 2048: 8 rows
+  // 7.0 and 13.9 us).
+  if (a.M <= 8 || (a.M <= 16 && a.N <= 64 * 128)) {
+    hipLaunchKernelGGL((swiglu_stream_kernel<kKeep>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * kStreamWaves), 0, stream, a);
+    return;
+  }
+  launch_tiles<kGated, kKeep, false>(a, plan(a.M, 2 * a.N, a.K, false, false).tiles, cus, stream);
+}
+
+template <Product kProduct>
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  return plan(M, N, K, kProduct == kDw, true);
+}
+int64_t slice_bytes(const Plan& p, int64_t M, int64_t N) { return p.slices > 1 ? 4 * p.slices * M * N : 0; }
+
+template <Product kProduct>
+void launch_product(GemmArgs a, bool f32, void* workspace, int cus, hipStream_t stream) {
+  if (a.K == 0) return launch_zero(a.C, a.M * a.N * (f32 ? 4 : 2), stream);
+  const Plan p = plan_of<kProduct>(a.M, a.N, a.K);
+  if (p.slices == 1) {
+    a.split_k = a.K;
+    f32 ? launch_tiles<kProduct, false, true>(a, p.tiles, cus, stream) : launch_tiles<kProduct, false, false>(a, p.tiles, cus, stream);
+    return;
+  }
+  void* const C = a.C;
+  const int64_t n = a.M * a.N, stages = (a.K + kStageK - 1) / kStageK;
+  a.C = workspace;
+  a.split_k = (stages + p.slices - 1) / p.slices * kStageK;
+  launch_tiles<kProduct, false, true>(a, p.tiles, cus, stream);
+  const int slices = (int)((a.K + a.split_k - 1) / a.split_k);
+  const dim3 grid((unsigned)std::min<int64_t>((n / 4 + 255) / 256, 1 << 16));
+  if (f32)
+    hipLaunchKernelGGL((swiglu_join_kernel<true>), grid, dim3(256), 0, stream, static_cast<const float*>(workspace), C, slices, n);
   else
-    launch_tile<2, 1, 2, kProduct, kKeep, kF32>(a, cus, stream);
+    hipLaunchKernelGGL((swiglu_join_kernel<false>), grid, dim3(256), 0, stream, static_cast<const float*>(workspace), C, slices, n);
 }
 
 bool device_cus(int* cus) {
@@ -683,13 +908,15 @@ __attribute__((visibility("default"))) int swiglu_gemm(const void* x, const void
   int cus = 0;
   if (!device_cus(&cus)) return SILUQUANT_ERR_DEVICE;
   const GemmArgs a = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), y, static_cast<uint16_t*>(gu), T, H, D,
-                      (int)D, (int)D, 0, 0};
-  gu ? launch_product<kGated, true, false>(a, cus, stream) : launch_product<kGated, false, false>(a, cus, stream);
+                      (int)D, (int)D, 0, 0, D};
+  gu ? launch_gated<true>(a, cus, stream) : launch_gated<false>(a, cus, stream);
   return launched();
 }
 
 __attribute__((visibility("default"))) int64_t swiglu_gemm_bwd_workspace_bytes(int64_t T, int64_t H, int64_t D) {
-  return sizes(T, H, D) ? 0 : -1;
+  if (!sizes(T, H, D)) return -1;
+  if (T == 0 || H == 0 || D == 0) return 0;
+  return std::max(slice_bytes(plan_of<kDx>(T, D, 2 * H), T, D), slice_bytes(plan_of<kDw>(2 * H, D, T), 2 * H, D));
 }
 
 __attribute__((visibility("default"))) int swiglu_gemm_bwd(const void* dy, const void* gu, const void* x, const void* w,
@@ -704,7 +931,7 @@ __attribute__((visibility("default"))) int swiglu_gemm_bwd(const void* dy, const
   if (T == 0 || D == 0) dx = nullptr;
   if (H == 0 || D == 0) dw = nullptr;
   if (!some && !dx && !dw) return SILUQUANT_OK;
-  const int64_t need = swiglu_gemm_bwd_workspace_bytes(T, H, D);
+  const int64_t need = dx || dw ? swiglu_gemm_bwd_workspace_bytes(T, H, D) : 0;
   if ((some && (!dy || !gu || !d_gu)) || (dw && T > 0 && !x) || (dx && H > 0 && !w) || (need > 0 && !workspace))
     return SILUQUANT_ERR_NULL_PTR;
   if (workspace_bytes < need) return SILUQUANT_ERR_BAD_SHAPE;
@@ -727,14 +954,12 @@ __attribute__((visibility("default"))) int swiglu_gemm_bwd(const void* dy, const
   }
   int cus = 0;
   if (!device_cus(&cus)) return SILUQUANT_ERR_DEVICE;
-  if (dx) {
-    const GemmArgs a = {d, static_cast<const uint16_t*>(w), dx, nullptr, T, D, 2 * H, (int)(2 * H), (int)D, 0, 0};
-    dx32 ? launch_product<kDx, false, true>(a, cus, stream) : launch_product<kDx, false, false>(a, cus, stream);
-  }
-  if (dw) {
-    const GemmArgs a = {d, static_cast<const uint16_t*>(x), dw, nullptr, 2 * H, D, T, (int)(2 * H), (int)D, 0, 0};
-    dw32 ? launch_product<kDw, false, true>(a, cus, stream) : launch_product<kDw, false, false>(a, cus, stream);
-  }
+  if (dx)
+    launch_product<kDx>({d, static_cast<const uint16_t*>(w), dx, nullptr, T, D, 2 * H, (int)(2 * H), (int)D, 0, 0, 0}, dx32, workspace,
+                        cus, stream);
+  if (dw)
+    launch_product<kDw>({d, static_cast<const uint16_t*>(x), dw, nullptr, 2 * H, D, T, (int)(2 * H), (int)D, 0, 0, 0}, dw32, workspace,
+                        cus, stream);
   return launched();
 }
 
