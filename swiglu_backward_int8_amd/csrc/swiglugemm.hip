@@ -40,26 +40,26 @@ struct Sigmoid {
   __device__ __forceinline__ float rest() const { return (below ? 1.0f : h * h) * r; }             // 1 - s
 };
 
-// The same to the last bit or so, for |g| up to 80: the exponent's argument in two
-// parts, the reciprocal corrected once.  d_gu is an operand of two products, and an
-// error of 1e-7 rounds one value in ten thousand to its other neighbour in bf16.
+// s and 1 - s to the last bit or so, for |g| up to 80: the exponent's argument in two
+// parts, and the reciprocal corrected by what it and 1 + e leave over.  d_gu is an
+// operand of two products, and an error of 1e-7 rounds one value in ten thousand to
+// its other neighbour in bf16.
 struct NearSigmoid {
-  float e, r;
-  bool below;
+  float s, rest;
   static constexpr float kMost = 80.0f;
   __device__ __forceinline__ explicit NearSigmoid(float g) {
     constexpr float kHi = -1.44269504088896341f, kLo = (float)(-1.44269504088896341 - (double)kHi), kLn2 = 0.69314718056f;
     const float a = __builtin_fabsf(g), t = a * kHi;
-    const float rest = __builtin_fmaf(a, kLo, __builtin_fmaf(a, kHi, -t));
-    e = __builtin_amdgcn_exp2f(t);
-    e = __builtin_fmaf(e, rest * kLn2, e);
-    const float d = 1.0f + e;
-    r = __builtin_amdgcn_rcpf(d);
-    r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-    below = g < 0.0f;
+    const float left = __builtin_fmaf(a, kLo, __builtin_fmaf(a, kHi, -t));
+    float e = __builtin_amdgcn_exp2f(t);
+    e = __builtin_fmaf(e, left * kLn2, e);
+    const float d = 1.0f + e, d_left = e - (d - 1.0f);
+    float r = __builtin_amdgcn_rcpf(d);
+    r = __builtin_fmaf(__builtin_fmaf(-d_left, r, __builtin_fmaf(-d, r, 1.0f)), r, r);
+    const float er = e * r;
+    s = g < 0.0f ? er : r;
+    rest = g < 0.0f ? r : er;
   }
-  __device__ __forceinline__ float times(float v) const { return v * (below ? e * r : r); }
-  __device__ __forceinline__ float rest() const { return below ? r : e * r; }
 };
 
 // ---- d_gu ----
@@ -82,21 +82,26 @@ __global__ __launch_bounds__(256) void swiglu_gate_bwd_kernel(const GateArgs a) 
     unpack(d, load_bf16<kFull, true>(a.dy + t * a.H + col, 8));
     unpack(g, load_bf16<kFull, true>(from, 8));
     unpack(u, load_bf16<kFull, true>(from + a.H, 8));
-    auto grads = [&](auto sigmoid) {
+    // dy * up and dy * gate are exact, products of two bf16 numbers, as long as they do not pass fp32's range
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf(g[k]), 0x1p-100f * __builtin_fabsf(d[k])));
+    if (__any(top > NearSigmoid::kMost)) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const decltype(sigmoid) s(g[k]);
+        const Sigmoid s(g[k]);
         dg[k] = s.times(d[k] * u[k]) * __builtin_fmaf(g[k], s.rest(), 1.0f);
         du[k] = d[k] * s.times(g[k]);
       }
-    };
-    float top = 0.0f;
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = __builtin_fmaxf(top, __builtin_fabsf(g[k]));
-    if (__any(top > NearSigmoid::kMost))
-      grads(Sigmoid(0.0f));
-    else
-      grads(NearSigmoid(0.0f));
+      for (int k = 0; k < 8; ++k) {
+        const NearSigmoid s(g[k]);
+        dg[k] = (d[k] * u[k]) * (s.s * __builtin_fmaf(g[k], s.rest, 1.0f));
+        du[k] = (d[k] * g[k]) * s.s;
+      }
+    }
     auto pack8 = [](const float (&v)[8]) {
       return Piece{{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}};
     };
