@@ -1,4 +1,4 @@
-"""One pre-norm SwiGLU block through the library, in 8 and in 4 bits.
+"""One pre-norm SwiGLU block through the library, in 8, 4 and 16 bits.
 
     h   = x + residual;  y = h / rms(h) * w          rms_norm_quant
     [gate | up] = y . Wgu^T                          i8_gemm_group_scaled, or mxfp4_gemm
@@ -11,6 +11,15 @@ codes every operand along both axes in one read, so that each of the three
 products of a linear layer contracts over blocks of its own axis; the SwiGLU
 backward pass's int8 codes come back through group_dequant; rms_norm_bwd takes
 the dgrad product's output and joins the residual's gradient.
+
+``train_bf16`` is a training step in bf16, with a layer norm and two dropouts:
+
+    h   = residual + dropout(x);  y = (h - mean) / std(h) * w + b    layer_norm_quant
+    a   = silu(y . Wg^T) * (y . Wu^T)                                swiglu_gemm
+    out = dropout(a) . Wd^T                                          dropout_add, torch's product
+
+Its masks are never stored: the backward pass makes them again from the same
+numbers (rng), which lie on the device, so a captured step can change them.
 
     python examples/mlp_block.py [T D H]
 
@@ -122,6 +131,50 @@ def train_mxfp4(x, residual, w, Wgu, Wd, d_out, d_h):
     return out, d_x, d_w, d_Wgu, d_Wd
 
 
+def train_bf16(x, residual, w, b, Wgu, Wd, d_out, d_h, p, rng):
+    """Forward and backward in bf16.  rng: int64 [2], a seed and the step's number.
+    Returns out and the gradients of x, residual, w, b, Wgu and Wd."""
+    T, D = x.shape
+    H = Wd.shape[1]
+    new = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device=x.device)
+    h, y, mean, rstd = new(T, D), new(T, D), new(T, dtype=torch.float32), new(T, dtype=torch.float32)
+    sq.layer_norm_quant(x, w, b, residual=residual, h=h, mean=mean, rstd=rstd, y_bf16=y, eps=EPS, p=p, rng=rng)
+    a, gu, ad = new(T, H), new(T, 2 * H), new(T, H)
+    sq.swiglu_gemm(y, Wgu, a, gu=gu)
+    sq.dropout_add(a, ad, p, rng, offset=1)
+    out = ad @ Wd.t()
+
+    d_Wd = d_out.t() @ ad
+    d_a = d_out @ Wd
+    sq.dropout_add(d_a, d_a, p, rng, offset=1)
+    d_y, d_Wgu = new(T, D), new(2 * H, D)
+    sq.swiglu_gemm_bwd(d_a, gu, y, Wgu, gu, dx=d_y, dw=d_Wgu, workspace=sq.swiglu_gemm_bwd_workspace(T, H, D, x.device))
+    d_residual, d_x = new(T, D), new(T, D) if p > 0 else None
+    d_w, d_b = new(D, dtype=torch.float32), new(D, dtype=torch.float32)
+    sq.layer_norm_bwd(d_y, h, w, mean, rstd, d_residual, dw=d_w, db=d_b, d_h=d_h, dx_drop=d_x,
+                      workspace=sq.layer_norm_bwd_workspace(T, D, x.device), p=p, rng=rng)
+    return out, d_residual if d_x is None else d_x, d_residual, d_w, d_b, d_Wgu, d_Wd
+
+
+def reference_bf16(x, residual, w, b, Wgu, Wd, d_out, d_h, p, rng):
+    """The same in fp32 through autograd, with the library's masks."""
+    def mask(rows, cols, offset):
+        m = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+        sq.dropout_add(torch.ones_like(m), m, p, rng, offset=offset)
+        return (m > 0).float() / (1 - p)
+
+    T, D = x.shape
+    H = Wd.shape[1]
+    x, residual, w, b, Wgu, Wd = leaves = [t.float().requires_grad_() for t in (x, residual, w, b, Wgu, Wd)]
+    h = residual + x * mask(T, D, 0)
+    c = h - h.mean(1, keepdim=True)
+    y = c * torch.rsqrt(c.square().mean(1, keepdim=True) + EPS) * w + b
+    gate, up = (y @ Wgu.t()).chunk(2, 1)
+    out = (torch.nn.functional.silu(gate) * up * mask(T, H, 1)) @ Wd.t()
+    torch.autograd.backward([out, h], [d_out.float(), d_h.float()])
+    return [out.detach()] + [t.grad for t in leaves]
+
+
 def reference(x, residual, w, Wgu, Wd, d_out, d_h):
     x, w, Wgu, Wd = (t.float().requires_grad_() for t in (x, w, Wgu, Wd))
     h = x + residual.float()
@@ -146,6 +199,10 @@ def main(T=512, D=1024, H=1408, device="cuda:0"):
     errors = {"int8 out": far(out8, want[0]), "int8 h": far(h8, want[1])}
     errors.update(zip(("mxfp4 out", "mxfp4 d_x", "mxfp4 d_w", "mxfp4 d_Wgu", "mxfp4 d_Wd"),
                       (far(a, b) for a, b in zip(got, (want[0],) + want[2:]))))
+    rng = torch.tensor([2024, 7], device=device)
+    args = x, residual, w, rand(D, std=0.1), Wgu, Wd, d_out, d_h, 0.1, rng
+    names = "out d_x d_residual d_w d_b d_Wgu d_Wd".split()
+    errors.update(("bf16 " + n, far(a, b)) for n, a, b in zip(names, train_bf16(*args), reference_bf16(*args)))
     return errors
 
 

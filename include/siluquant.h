@@ -469,8 +469,9 @@ int swiglu_gemm(const void* x, const void* w, void* y, void* gu, int64_t T, int6
  *         then not looked at)
  *   dw    bf16 or fp32 [2H, D] by dw_dtype, or NULL (x is then not looked at)
  *   workspace  swiglu_gemm_bwd_workspace_bytes(T, H, D) bytes, which may be 0,
- *         16-byte aligned.  Its contents before and after a call mean nothing.
- *         The sums do not depend on timing.
+ *         16-byte aligned; only looked at when that is not 0 and dx or dw is
+ *         wanted.  Its contents before and after a call mean nothing.  The sums do
+ *         not depend on timing.
  * All 16-byte aligned; sizes as swiglu_gemm.  T == 0 writes zeros to dw, H == 0 to
  * dx.  A workspace that is too small returns SILUQUANT_ERR_BAD_SHAPE.
  */

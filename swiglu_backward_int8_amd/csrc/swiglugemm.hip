@@ -937,6 +937,10 @@ __attribute__((visibility("default"))) int swiglu_gemm_bwd(const void* dy, const
   if (H == 0 || D == 0) dw = nullptr;
   if (!some && !dx && !dw) return SILUQUANT_OK;
   const int64_t need = dx || dw ? swiglu_gemm_bwd_workspace_bytes(T, H, D) : 0;
+  // what is not needed is not looked at
+  if (!dx) w = nullptr;
+  if (!dw) x = nullptr;
+  if (need == 0) workspace = nullptr, workspace_bytes = 0;
   if ((some && (!dy || !gu || !d_gu)) || (dw && T > 0 && !x) || (dx && H > 0 && !w) || (need > 0 && !workspace))
     return SILUQUANT_ERR_NULL_PTR;
   if (workspace_bytes < need) return SILUQUANT_ERR_BAD_SHAPE;
