@@ -52,6 +52,7 @@ struct LnArgs {
   float* rstd;
   int64_t T;
   int D, lg_lanes, groups;  // lg_lanes: log2 of the lanes per group (4, 8, 16)
+  bool e4m3;
   float eps;
   Dropout drop;
 };
@@ -62,6 +63,38 @@ __device__ __forceinline__ void load_x(float (&v)[8], const void* p, int64_t at,
     load_f32<kKind>(v, static_cast<const float*>(p) + at, n);
   else
     unpack(v, load_bf16<kKind, false>(static_cast<const uint16_t*>(p) + at, n));
+}
+
+// Eight values as they were loaded: bf16 ones take half the registers.
+template <bool kF32, bool kNt>
+struct Loaded;
+template <bool kNt>
+struct Loaded<false, kNt> {
+  Piece p;
+  template <Kind kKind>
+  __device__ __forceinline__ void load(const void* from, int64_t at, uint32_t col, int n) {
+    p = load_bf16<kKind, kNt>(static_cast<const uint16_t*>(from) + at + col, n);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack(v, p); }
+};
+template <bool kNt>
+struct Loaded<true, kNt> {
+  float p[8];
+  template <Kind kKind>
+  __device__ __forceinline__ void load(const void* from, int64_t at, uint32_t col, int n) {
+    load_f32<kKind>(p, static_cast<const float*>(from) + at + col, n);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[i];
+  }
+};
+
+// Makes the compiler unpack a piece again where it is used next: kept unpacked over
+// a reduction, a row takes twice the registers.
+__device__ __forceinline__ void fold(Piece& p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(p.w[i]));
 }
 
 __device__ __forceinline__ Piece pack8(const float (&v)[8]) {
@@ -114,7 +147,7 @@ __device__ __forceinline__ Piece normed(const Piece& h, const Piece& w, const Pi
 // kOneWave: each wave of the workgroup takes rows of its own; otherwise the
 // workgroup shares a row.  Piece c of a lane starts kPieces' width of the lanes
 // further.
-template <bool kOneWave, int kPieces, bool kXF32, Kind kKind, bool kE4M3>
+template <bool kOneWave, int kPieces, bool kXF32, Kind kKind, bool kDrop>
 __global__ __launch_bounds__(kOneWave ? 256 : 1024) void layer_norm_quant_kernel(const LnArgs a) {
   __shared__ float s_stat[2][2][16];  // [row's turn][sum, squares][wave]
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
@@ -122,33 +155,34 @@ __global__ __launch_bounds__(kOneWave ? 256 : 1024) void layer_norm_quant_kernel
   const int first = 8 * (kOneWave ? lane : (int)threadIdx.x), step = 8 * (kOneWave ? 64 : (int)blockDim.x);
   const int64_t rows_at_once = kOneWave ? waves : 1;
   DropKey key = {};
-  if (a.drop.rng) key = drop_key(a.drop);
+  if (kDrop) key = drop_key(a.drop);
   int turn = 0;
   for (int64_t row = blockIdx.x * rows_at_once + (kOneWave ? wave : 0); row < a.T; row += gridDim.x * rows_at_once) {
-    const int64_t at = row * a.D + first;
+    const int64_t at = row * a.D;  // the same in every lane: addresses are a scalar and a 32-bit offset
     const int n0 = a.D - first;
-    float x[kPieces][8];
-    Piece h[kPieces], r[kPieces], w[kPieces], b[kPieces];
-    each_piece<kKind, kPieces>([&](auto kind, int c) { load_x<kXF32, decltype(kind)::value>(x[c], a.x, at + c * step, n0 - c * step); });
+    auto col = [&](int c) { return (uint32_t)(first + c * step); };
+    Loaded<kXF32, false> x[kPieces];
+    Piece h[kPieces], w[kPieces];
+    each_piece<kKind, kPieces>([&](auto kind, int c) { x[c].template load<decltype(kind)::value>(a.x, at, col(c), n0 - c * step); });
     if (a.residual) {
       each_piece<kKind, kPieces>([&](auto kind, int c) {
-        r[c] = load_bf16<decltype(kind)::value, false>(a.residual + at + c * step, n0 - c * step);
+        h[c] = load_bf16<decltype(kind)::value, false>(a.residual + at + col(c), n0 - c * step);
       });
     }
     each_piece<kKind, kPieces>([&](auto kind, int c) {
-      w[c] = load_bf16<decltype(kind)::value, false>(a.weight + first + c * step, n0 - c * step);
-      b[c] = a.bias ? load_bf16<decltype(kind)::value, false>(a.bias + first + c * step, n0 - c * step) : zero_piece();
+      w[c] = load_bf16<decltype(kind)::value, false>(a.weight + col(c), n0 - c * step);
     });
-    if (a.drop.rng) {
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c) drop8(x[c], a.drop, key, row, first + c * step);
-    }
     float sum = 0.0f, sq = 0.0f, mean, rstd;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) {
-      if (a.residual) add(x[c], r[c]);
-      h[c] = pack8(x[c]);
+      float v[8];
+      x[c].get(v);
+      if (kDrop) drop8(v, a.drop, key, row, first + c * step);
+      if (a.residual) add(v, h[c]);
+      h[c] = pack8(v);
       sum += sum8(h[c]);
+      fold(h[c]);
+      if (kDrop) __builtin_amdgcn_sched_barrier(0);  // one piece's generator at a time
     }
     sum = wave_sum(sum);
     // the columns of wave v of the workgroup
@@ -179,10 +213,12 @@ __global__ __launch_bounds__(kOneWave ? 256 : 1024) void layer_norm_quant_kernel
     each_piece<kKind, kPieces>([&](auto kind, int c) {
       constexpr Kind k = decltype(kind)::value;
       const int n = n0 - c * step;
-      if (a.h) store_bf16<k, true>(a.h + at + c * step, h[c], n);
-      const Piece y = normed(h[c], w[c], b[c], mean, rstd);  // zero past the row, where weight and bias are
-      if (a.y) store_bf16<k, true>(a.y + at + c * step, y, n);
-      if (a.q) quantise<kE4M3, k>(a, y, row, first + c * step, n);
+      const Piece b = a.bias ? load_bf16<k, false>(a.bias + col(c), n) : zero_piece();
+      fold(h[c]);
+      if (a.h) store_bf16<k, true>(a.h + at + col(c), h[c], n);
+      const Piece y = normed(h[c], w[c], b, mean, rstd);  // zero past the row, where weight and bias are
+      if (a.y) store_bf16<k, true>(a.y + at + col(c), y, n);
+      if (a.q) a.e4m3 ? quantise<true, k>(a, y, row, first + c * step, n) : quantise<false, k>(a, y, row, first + c * step, n);
     });
   }
 }
@@ -191,7 +227,7 @@ __global__ __launch_bounds__(kOneWave ? 256 : 1024) void layer_norm_quant_kernel
 // time from h where it is kept (a lane reads back what it wrote itself).  The
 // first time every lane joins its pieces' means and squares one by one.
 constexpr int kWideThreads = 1024;
-template <bool kXF32, bool kE4M3>
+template <bool kXF32>
 __global__ __launch_bounds__(kWideThreads) void layer_norm_quant_wide_kernel(const LnArgs a) {
   __shared__ float s_sum[16];
   const int tid = threadIdx.x, wave = tid >> 6, waves = kWideThreads / 64;
@@ -234,7 +270,7 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_quant_wide_kernel(con
       const Piece b = a.bias ? load_bf16<kRagged, false>(a.bias + col, n) : zero_piece();
       const Piece y = normed(h, load_bf16<kRagged, false>(a.weight + col, n), b, mean, rstd);
       if (a.y) store_bf16<kRagged, true>(a.y + at + col, y, n);
-      if (a.q) quantise<kE4M3, kRagged>(a, y, row, col, n);
+      if (a.q) a.e4m3 ? quantise<true, kRagged>(a, y, row, col, n) : quantise<false, kRagged>(a, y, row, col, n);
     }
   }
 }
@@ -257,31 +293,6 @@ struct LnBwdArgs {
   Dropout drop;
 };
 
-// Eight gradients, as they were loaded: bf16 ones take half the registers.
-template <bool kF32>
-struct Grads;
-template <>
-struct Grads<false> {
-  Piece p;
-  template <Kind kKind>
-  __device__ __forceinline__ void load(const void* from, int64_t at, int n) {
-    p = load_bf16<kKind, true>(static_cast<const uint16_t*>(from) + at, n);
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const { unpack(v, p); }
-};
-template <>
-struct Grads<true> {
-  float p[8];
-  template <Kind kKind>
-  __device__ __forceinline__ void load(const void* from, int64_t at, int n) {
-    load_f32<kKind>(p, static_cast<const float*>(from) + at, n);
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = p[i];
-  }
-};
-
 // dx of one piece in fp32.  c1, c2: the row's sum(g) / D and sum(g * n) / D.
 __device__ __forceinline__ void grad8(float (&o)[8], const float (&dy)[8], const Piece& h, const Piece& w, const Piece& d,
                                       float mean, float rstd, float c1, float c2) {
@@ -301,8 +312,8 @@ __device__ __forceinline__ void grad8(float (&o)[8], const float (&dy)[8], const
 // their own, their sums are added in LDS at the end, in wave order, so that the
 // result does not depend on timing.  Workgroups of more than eight waves have 128
 // registers a lane: they read weight and d_h where they use them.
-template <bool kOneWave, int kPieces, int kThreads, bool kDyF32, Kind kKind>
-__global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(const LnBwdArgs a) {
+template <bool kOneWave, int kPieces, int kThreads, bool kDyF32, Kind kKind, bool kDrop>
+__global__ __launch_bounds__(kThreads, kDrop || kKind == kRagged ? 1 : 4) void layer_norm_bwd_kernel(const LnBwdArgs a) {
   constexpr bool kLate = kThreads > 512;
   __shared__ float s_part[kOneWave ? 2 * 512 * kPieces : 1];
   __shared__ float s_stat[2][2][16];
@@ -310,12 +321,13 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(const LnBwdArg
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = 8 * (kOneWave ? lane : (int)threadIdx.x), step = 8 * (kOneWave ? 64 : (int)blockDim.x);
   const int n0 = a.D - first;
+  auto col = [&](int c) { return (uint32_t)(first + c * step); };
   DropKey key = {};
-  if (a.dx_drop) key = drop_key(a.drop);
+  if (kDrop) key = drop_key(a.drop);
   Piece w[kPieces];
   float dw[kPieces][8], db[kPieces][8];
   auto load_weight = [&](auto kind, int c) {
-    w[c] = load_bf16<decltype(kind)::value, false>(a.weight + first + c * step, n0 - c * step);
+    w[c] = load_bf16<decltype(kind)::value, false>(a.weight + col(c), n0 - c * step);
   };
 #pragma unroll
   for (int c = 0; c < kPieces; ++c)
@@ -325,16 +337,16 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(const LnBwdArg
   const int64_t rows_at_once = kOneWave ? waves : 1;
   int turn = 0;
   for (int64_t row = blockIdx.x * rows_at_once + (kOneWave ? wave : 0); row < a.T; row += gridDim.x * rows_at_once) {
-    const int64_t at = row * a.D + first;
+    const int64_t at = row * a.D;
     const float mean = a.mean[row], rstd = a.rstd[row];
-    Grads<kDyF32> dy[kPieces];
+    Loaded<kDyF32, true> dy[kPieces];
     Piece h[kPieces], d[kPieces];
     each_piece<kKind, kPieces>([&](auto kind, int c) {
-      dy[c].template load<decltype(kind)::value>(a.dy, at + c * step, n0 - c * step);
-      h[c] = load_bf16<decltype(kind)::value, true>(a.h + at + c * step, n0 - c * step);
+      dy[c].template load<decltype(kind)::value>(a.dy, at, col(c), n0 - c * step);
+      h[c] = load_bf16<decltype(kind)::value, true>(a.h + at + col(c), n0 - c * step);
     });
     auto load_dh = [&](auto kind, int c) {
-      d[c] = a.d_h ? load_bf16<decltype(kind)::value, true>(a.d_h + at + c * step, n0 - c * step) : zero_piece();
+      d[c] = a.d_h ? load_bf16<decltype(kind)::value, true>(a.d_h + at + col(c), n0 - c * step) : zero_piece();
     };
     each_piece<kKind, kPieces>([&](auto kind, int c) { kLate ? load_weight(kind, c) : load_dh(kind, c); });
     float c1 = 0.0f, c2 = 0.0f;
@@ -369,12 +381,12 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(const LnBwdArg
       if (kLate) load_weight(kind, c), load_dh(kind, c);
       dy[c].get(dv);
       grad8(o, dv, h[c], w[c], d[c], mean, rstd, c1, c2);
-      store_bf16<k, false>(a.dx + at + c * step, pack8(o), n0 - c * step);
-      if (a.dx_drop) {
+      store_bf16<k, false>(a.dx + at + col(c), pack8(o), n0 - c * step);
+      if (kDrop) {
         drop8(o, a.drop, key, row, first + c * step);
-        store_bf16<k, false>(a.dx_drop + at + c * step, pack8(o), n0 - c * step);
+        store_bf16<k, false>(a.dx_drop + at + col(c), pack8(o), n0 - c * step);
+        __builtin_amdgcn_sched_barrier(0);  // one piece's generator at a time
       }
-      __builtin_amdgcn_sched_barrier(0);  // one piece's generator at a time
     });
   }
   if (!a.part_dw && !a.part_db) return;
@@ -563,16 +575,16 @@ int bwd_parts(int64_t T, int64_t D) {
 }
 
 template <bool kOneWave, int kPieces>
-void launch_norm(const LnArgs& a, bool f32, bool e4m3, int waves, hipStream_t stream) {
+void launch_norm(const LnArgs& a, bool f32, int waves, hipStream_t stream) {
   const int64_t groups = kOneWave ? (a.T + waves - 1) / waves : a.T;
   const dim3 grid((unsigned)std::min<int64_t>(groups, kMaxGrid)), block(64 * waves);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
   with_kind<kPieces>(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
     constexpr Kind k = decltype(kind)::value;
     if (f32)
-      e4m3 ? go(layer_norm_quant_kernel<kOneWave, kPieces, true, k, true>) : go(layer_norm_quant_kernel<kOneWave, kPieces, true, k, false>);
+      a.drop.rng ? go(layer_norm_quant_kernel<kOneWave, kPieces, true, k, true>) : go(layer_norm_quant_kernel<kOneWave, kPieces, true, k, false>);
     else
-      e4m3 ? go(layer_norm_quant_kernel<kOneWave, kPieces, false, k, true>) : go(layer_norm_quant_kernel<kOneWave, kPieces, false, k, false>);
+      a.drop.rng ? go(layer_norm_quant_kernel<kOneWave, kPieces, false, k, true>) : go(layer_norm_quant_kernel<kOneWave, kPieces, false, k, false>);
   });
 }
 
@@ -581,8 +593,10 @@ void launch_bwd(const LnBwdArgs& a, bool f32, int grid, int waves, hipStream_t s
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * waves), 0, stream, a); };
   with_kind<kPieces>(a.D, 512 * kPieces * (kOneWave ? 1 : waves), [&](auto kind) {
     constexpr Kind k = decltype(kind)::value;
-    f32 ? go(layer_norm_bwd_kernel<kOneWave, kPieces, kThreads, true, k>)
-        : go(layer_norm_bwd_kernel<kOneWave, kPieces, kThreads, false, k>);
+    if (f32)
+      a.dx_drop ? go(layer_norm_bwd_kernel<kOneWave, kPieces, kThreads, true, k, true>) : go(layer_norm_bwd_kernel<kOneWave, kPieces, kThreads, true, k, false>);
+    else
+      a.dx_drop ? go(layer_norm_bwd_kernel<kOneWave, kPieces, kThreads, false, k, true>) : go(layer_norm_bwd_kernel<kOneWave, kPieces, kThreads, false, k, false>);
   });
 }
 
@@ -627,22 +641,18 @@ __attribute__((visibility("default"))) int layer_norm_quant(const void* x, int x
     for (int i = 0; i < o; ++i)
       if (overlap(out[o], out[i])) return SILUQUANT_ERR_OVERLAP;
   }
-  const bool e4m3 = code_format == SILUQUANT_CODE_E4M3;
   const LnArgs a = {x, static_cast<const uint16_t*>(residual), static_cast<const uint16_t*>(weight),
                     static_cast<const uint16_t*>(bias), static_cast<uint8_t*>(y_q), y_s, static_cast<uint16_t*>(y_bf16),
                     static_cast<uint16_t*>(h), mean, rstd, T, (int)D, group == 32 ? 2 : group == 64 ? 3 : 4, (int)groups,
-                    eps, make_dropout(p, rng, offset)};
+                    code_format == SILUQUANT_CODE_E4M3, eps, make_dropout(p, rng, offset)};
   if (D > kRegisterD) {
     const dim3 grid((unsigned)std::min<int64_t>(T, kMaxGrid)), block(kWideThreads);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
-    if (f32)
-      e4m3 ? go(layer_norm_quant_wide_kernel<true, true>) : go(layer_norm_quant_wide_kernel<true, false>);
-    else
-      e4m3 ? go(layer_norm_quant_wide_kernel<false, true>) : go(layer_norm_quant_wide_kernel<false, false>);
+    f32 ? go(layer_norm_quant_wide_kernel<true>) : go(layer_norm_quant_wide_kernel<false>);
   } else {
-    if (D <= 512) launch_norm<true, 1>(a, f32, e4m3, 4, stream);
-    else if (D <= 1024) launch_norm<true, 2>(a, f32, e4m3, 4, stream);
-    else launch_norm<false, 2>(a, f32, e4m3, (int)((D + 1023) / 1024), stream);
+    if (D <= 512) launch_norm<true, 1>(a, f32, 4, stream);
+    else if (D <= 1024) launch_norm<true, 2>(a, f32, 4, stream);
+    else launch_norm<false, 2>(a, f32, (int)((D + 1023) / 1024), stream);
   }
   return launched();
 }
