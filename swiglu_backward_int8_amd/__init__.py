@@ -637,13 +637,18 @@ def layer_norm_quant(x, weight, bias=None, y_q=None, y_s=None, residual=None, h=
         fmt = _code_format("y_q", y_q)
         _want("y_q", y_q, y_q.dtype, (T, D), idx)
         _want("y_s", y_s, _f32, (T, -(-D // group_size)), idx)
-    for name, t in (("residual", residual), ("h", h), ("y_bf16", y_bf16)):
-        if t is not None:
-            _want(name, t, _bf16, (T, D), idx)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            _want(name, t, _f32, (T,), idx)
-    _want_drop(p, rng, offset, idx)
+    if residual is not None:
+        _want("residual", residual, _bf16, (T, D), idx)
+    if h is not None:
+        _want("h", h, _bf16, (T, D), idx)
+    if y_bf16 is not None:
+        _want("y_bf16", y_bf16, _bf16, (T, D), idx)
+    if mean is not None:
+        _want("mean", mean, _f32, (T,), idx)
+    if rstd is not None:
+        _want("rstd", rstd, _f32, (T,), idx)
+    if p != 0.0 or rng is not None:
+        _want_drop(p, rng, offset, idx)
     _enqueue(lib().layer_norm_quant, "layer_norm_quant", idx, x.data_ptr(), F32 if x.dtype is _f32 else BF16,
              _ptr(residual), weight.data_ptr(), _ptr(bias), _ptr(y_q), _ptr(y_s), _ptr(y_bf16), _ptr(h), _ptr(mean),
              _ptr(rstd), T, D, group_size, fmt, eps, p, _ptr(rng), offset)
@@ -680,13 +685,14 @@ def layer_norm_bwd(dy, h, weight, mean, rstd, dx, dw=None, db=None, d_h=None, dx
     T, D, idx = _rank2("dy", dy)
     _want2("dy", dy, _bf16, _f32, (T, D), idx)
     _want("weight", weight, _bf16, (D,), idx)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _want(name, t, _f32, (T,), idx)
+    _want("mean", mean, _f32, (T,), idx)
+    _want("rstd", rstd, _f32, (T,), idx)
     _want("h", h, _bf16, (T, D), idx)
     _want("dx", dx, _bf16, (T, D), idx)
-    for name, t in (("dw", dw), ("db", db)):
-        if t is not None:
-            _want(name, t, _f32, (D,), idx)
+    if dw is not None:
+        _want("dw", dw, _f32, (D,), idx)
+    if db is not None:
+        _want("db", db, _f32, (D,), idx)
     if d_h is not None:
         _want("d_h", d_h, _bf16, (T, D), idx)
     if dx_drop is not None:

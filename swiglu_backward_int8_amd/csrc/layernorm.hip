@@ -463,10 +463,10 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(const LnBwdArg
       float dv[8], o[8];
       r.dy[c].get(dv);
       grad8(o, dv, r.h[c], w[c], r.d[c], mean, rstd, c1, c2);
-      store_bf16<k, false>(a.dx + at + col(c), pack8(o), n0 - c * step);
+      store_bf16<k, true>(a.dx + at + col(c), pack8(o), n0 - c * step);
       if (kDrop) {
         drop8(o, a.drop, key, row, first + c * step);
-        store_bf16<k, false>(a.dx_drop + at + col(c), pack8(o), n0 - c * step);
+        store_bf16<k, true>(a.dx_drop + at + col(c), pack8(o), n0 - c * step);
         __builtin_amdgcn_sched_barrier(0);  // one piece's generator at a time
       }
     });
@@ -510,10 +510,10 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(const LnBwdArg
 }
 
 // dw[d] and db[d]: the sums of the partial rows (dw's by the workgroups with
-// blockIdx.y 0, db's with 1): 16 columns per workgroup, 64 strips of rows (every
-// 64th), each in row order, and then the strips in pairs, halving their number,
+// blockIdx.y 0, db's with 1): 32 columns per workgroup, 32 strips of rows (every
+// 32nd), each in row order, and then the strips in pairs, halving their number,
 // always the same ones.
-constexpr int kSumStrips = 64, kSumCols = 16;
+constexpr int kSumStrips = 32, kSumCols = 32;  // lines of 128 bytes (16 columns, 64 strips: 16384 x 4096 128 us in place of 125)
 struct SumArgs {
   const float* part[2];
   float* out[2];  // null: not wanted
