@@ -202,9 +202,10 @@ struct TileShape {
   // The results' way out: per wave, one or two pieces of 32 rows x 128 bytes (gated: of
   // gate and of up), in the last buffer's place or in one of their own.
   static constexpr int kPiece = 32 * 128 * (kGatedTile ? 2 : 1);
-  static constexpr int kTurns = kStage >= 2 * kWaves * kPiece || kFA == 1 ? 2 : 1;
-  static constexpr bool kOwnPatch = kStage < kTurns * kWaves * kPiece;
   static constexpr bool kUneven = kBufs == 3;  // two buffers of A's, three of B's
+  static constexpr int kPatch = kUneven ? kTileB * kRowBytes : kStage;  // bytes in that place
+  static constexpr int kTurns = kPatch >= 2 * kWaves * kPiece || kFA == 1 ? 2 : 1;
+  static constexpr bool kOwnPatch = kPatch < kTurns * kWaves * kPiece;
   static constexpr int kBuffers = kUneven ? 2 * kTileA * kRowBytes + 3 * kTileB * kRowBytes : kBufs * kStage;
   static constexpr int kLds = kBuffers + (kOwnPatch ? kTurns * kWaves * kPiece : 0);
   static constexpr int kPerCu = 2 * kLds <= 160 * 1024 ? 2 : 1;  // workgroups that fit a CU's LDS
@@ -437,19 +438,19 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
   };
   using std::integral_constant;
 
-  // A tile's first loads: all stages but one of the buffers.
-  constexpr int kFirst = kUneven ? kLoadsA + 2 * kLoadsB : (kBufs - 1) * kLoads;
+  // A tile's first loads: all buffers but the last (uneven: B's last).
+  constexpr int kFirst = kUneven ? 2 * kLoads : (kBufs - 1) * kLoads;
   auto start = [&](int l) {
+    if (l > 0 && l % kLoads == 0) advance();
+    const int s = l / kLoads;
     if constexpr (kUneven) {
-      const int b = l - kLoadsA;
-      if (l == kFirst - kLoadsB) sb.advance();
-      if (b < 0)
-        issue_a(std::true_type{}, 0, lds0, l);
+      const int i = l % kLoads;
+      if (i < kLoadsA)
+        issue_a(std::true_type{}, s, lds0 + a_at(s), i);
       else
-        issue_b(std::true_type{}, b / kLoadsB, lds0 + 2 * kABytes + b / kLoadsB * kBBytes, b % kLoadsB);
+        issue_b(std::true_type{}, s, lds0 + 2 * kABytes + s * kBBytes, i - kLoadsA);
     } else {
-      if (l > 0 && l % kLoads == 0) advance();
-      issue(std::true_type{}, l / kLoads, l % kLoads);
+      issue(std::true_type{}, s, l % kLoads);
     }
   };
 
@@ -461,12 +462,16 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
   constexpr int kPieces = kPartsB * kFA;                    // of 32 rows x 128 bytes (gated: two such, of gate and up in fp32)
   constexpr int kTurns = Shape::kTurns, kPieceBytes = Shape::kPiece;
   static_assert(kTurns == 2 || kProduct == kGated, "the others alternate");
-  // uneven: half of the waves in A's second buffer, half in B's third
-  static_assert(!kUneven || (kWaves == 4 && kABytes == kBBytes && kTurns * kPieceBytes <= kABytes / 2), "two waves each");
   char* patch = s_tile + (Shape::kOwnPatch ? Shape::kBuffers + wave * kTurns * kPieceBytes
-                          : kUneven ? (wave < 2 ? kABytes : 2 * kABytes + kBBytes) + wave * (kABytes / 2)
-                                    : (kBufs - 1) * kStage + wave * (kStage / kWaves));
-  constexpr int kPerPiece = (kFirst + kPieces - 1) / kPieces;  // the next tile's first loads that go out with each piece
+                                           : Shape::kBuffers - Shape::kPatch + wave * (Shape::kPatch / kWaves));
+  // The next tile's first loads go out with the first half of the pieces.  What is
+  // stored after the last of them, if the tile is whole, need not have ended when the
+  // next tile begins.
+  constexpr int kPerPiece = std::max(8, (kFirst + kPieces - 1) / kPieces);
+  constexpr int kPerStore = kProduct == kGated ? (kKeep ? 6 : 2) : 4;  // stores of a piece, kBehind pieces later on
+  constexpr int kBehind = kProduct == kGated ? 1 : 2;
+  constexpr int kStoresAfter = std::min(63, kPerStore * (kPieces + kBehind - std::max(kBehind, (kFirst - 1) / kPerPiece + 1)));
+  bool stored_whole = false;
 
 #pragma unroll
   for (int l = 0; l < kFirst; ++l) start(l);
@@ -475,18 +480,20 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
     for (int i = 0; i < kFA; ++i)
 #pragma unroll
       for (int k = 0; k < kFB; ++k) acc[i][k] = (f32x16){};
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    if (stored_whole)
+      asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kStoresAfter) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     __syncthreads();
     // Before the last step of a stage every wave has read all of it: there the
     // next stage's loads are waited for, and after the barrier the loads of the
     // stage after it go into the buffer that has just been read, spread over
     // that last step and the first one of the next stage.
-    advance();
     if constexpr (kUneven) {
-      // A's loads are one stage ahead, in its last step; B's two, in the first two.
+      // A's loads of two stages on are in a stage's last step, when its buffer has been
+      // read; B's in the first two steps, one buffer further.
+      sb.advance();
       turn_b = 0;
-#pragma unroll
-      for (int i = 0; i < kLoadsA; ++i) issue_a(std::true_type{}, 1, lds0 + kABytes, i);
 #pragma unroll
       for (int n = 0; n < kReads; ++n) read(0, b_turn(0), 0, n);
 #pragma unroll 1
@@ -513,6 +520,7 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
         });
       }
     } else {
+      advance();
 #pragma unroll
       for (int l = 0; l < kLoads / 2; ++l) issue(std::true_type{}, kBufs - 1, l);
 #pragma unroll
@@ -689,6 +697,7 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
       }
     }
     if (!more) break;
+    stored_whole = whole;
   }
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // nothing writes LDS after the workgroup's end
 }
