@@ -598,15 +598,7 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
       for (int n = kPerPiece * t; n < kPerPiece * (t + 1); ++n)
         if (n < kFirst) start(n);
     };
-    // Whole lines are streamed: left in L2, a round's results drive out the operands.
-    // Rows that start inside lines are not: their lines have to meet in L2.
-    const bool streamed = whole && (a.N * (16 / kPer) & 63) == 0 && (reinterpret_cast<uintptr_t>(a.C) & 63) == 0;
-    auto store = [](char* to, const u32x4& v, bool streamed) {
-      if (streamed)
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
-      else
-        *reinterpret_cast<u32x4*>(to) = v;
-    };
+    auto store = [](char* to, const u32x4& v) { *reinterpret_cast<u32x4*>(to) = v; };
     if constexpr (kProduct == kGated) {
       // Gate and up go through LDS as they are; four lanes read a row of 32 columns of
       // both, eight columns a lane, and store y and what is kept of gate and up.
@@ -621,7 +613,7 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
                 (f32x4){d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
           }
       };
-      auto finish = [&](int t) {
+      auto finish = [&](int t, auto whole) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int row = 16 * x + (l >> 2), down = 32 * (t / kPartsB) + row, column = 32 * (t % kPartsB) + 8 * (l & 3);
@@ -639,48 +631,46 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
           auto pack8 = [](const float (&v)[8]) {
             return (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
           };
-          if (whole || (down < rows && column < columns)) {  // H is a multiple of 8: whole chunks
-            store(static_cast<char*>(a.C) + ((row0 + down) * a.N + col0 + column) * 2, pack8(y), streamed);
+          if (decltype(whole)::value || (down < rows && column < columns)) {  // H is a multiple of 8: whole chunks
+            store(static_cast<char*>(a.C) + ((row0 + down) * a.N + col0 + column) * 2, pack8(y));
             if (kKeep) {
               char* const to = reinterpret_cast<char*>(a.gu) + ((row0 + down) * 2 * a.N + col0 + column) * 2;
-              store(to, pack8(g), streamed);
-              store(to + 2 * a.N, pack8(u), streamed);
+              store(to, pack8(g));
+              store(to + 2 * a.N, pack8(u));
             }
           }
         }
       };
+      auto all_pieces = [&](auto whole) {
 #pragma unroll
-      for (int t = 0; t <= kPieces; ++t) {
-        if (t < kPieces) loads(t);
-        if (t < kPieces && kTurns == 2) put_pair(t);
-        if (t > 0) finish(t - 1);
-        if (t < kPieces && kTurns == 1) put_pair(t);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+        for (int t = 0; t <= kPieces; ++t) {
+          if (t < kPieces) loads(t);
+          if (t < kPieces && kTurns == 2) put_pair(t);
+          if (t > 0) finish(t - 1, whole);
+          if (t < kPieces && kTurns == 1) put_pair(t);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if (whole)
+        all_pieces(std::true_type{});
+      else
+        all_pieces(std::false_type{});
     } else {
       // where a lane's chunk of row 0 goes
       char* const to0 = static_cast<char*>(a.C) + ((row0 + r) * a.N + col0 + kPer * (l & 7)) * (16 / kPer);
       auto place = [&](int block, int part, int x) { return to0 + (32 * block + 8 * x) * a.N * (16 / kPer) + 128 * part; };
-      auto store_whole = [&](auto streamed) {
-        constexpr bool kStreamed = decltype(streamed)::value;
-        auto row_of = [](int n) { return kStreamed ? n % kFA : n / kPartsB; };
-        auto part_of = [](int n) { return kStreamed ? n / kFA : n % kPartsB; };
+      if (whole) {
 #pragma unroll
         for (int t = 0; t < kPieces + 2; ++t) {
           loads(t);
-          if (t < kPieces) put(t, row_of(t), part_of(t));
+          if (t < kPieces) put(t, t / kPartsB, t % kPartsB);
           if (t >= 2) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) store(place(row_of(t - 2), part_of(t - 2), x), out[t & 1][x], kStreamed);
+            for (int x = 0; x < 4; ++x) store(place((t - 2) / kPartsB, (t - 2) % kPartsB, x), out[t & 1][x]);
           }
           if (t >= 1 && t <= kPieces) get(t - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
-      };
-      if (streamed) {
-        store_whole(std::true_type{});
-      } else if (whole) {
-        store_whole(std::false_type{});
       } else {
 #pragma unroll
         for (int t = 0; t < kPieces; ++t) {
@@ -691,7 +681,7 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             if (first + 8 * x < rows && 8 * kPer * part + kPer * (l & 7) < columns)  // N is a multiple of 8: whole chunks
-              store(place(t / kPartsB, part, x), out[t & 1][x], false);
+              store(place(t / kPartsB, part, x), out[t & 1][x]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }

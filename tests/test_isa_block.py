@@ -6,6 +6,9 @@ gated projection (CPU only: hipcc compiles the sources with the library's flags)
   waits for loads into LDS count memory operations.
 * Nothing in front of a load into LDS breaks the wait states of its scalars, on any
   path (the check itself is tested with the microscaled product's).
+* A tile's start waits until no more than N memory operations are left, in the order of
+  their issue, where the tile before it was whole: at least N stores come after the last
+  of its loads into LDS.
 * The matrix and the transposing LDS instructions are there.
 """
 
@@ -14,7 +17,7 @@ import re
 import pytest
 
 import isa
-from test_isa_waits import hazards, pytestmark  # noqa: F401
+from test_isa_waits import counted_waits, hazards, pytestmark  # noqa: F401
 
 
 @pytest.mark.parametrize("source", ["layernorm", "swiglugemm"])
@@ -43,6 +46,34 @@ def test_loads_into_lds_wait_for_their_scalars_on_every_path():
         assert not bad, (name, bad[:3])
         total += loads
     assert total > 1000
+
+
+def stores_behind_the_loads(kernel):
+    """For each run of instructions without a branch that loads into LDS and stores after
+    that (a whole tile's end): the stores after its last load."""
+    out = []
+    for block in kernel.blocks():
+        loads = [i for i, c in enumerate(block) if isa.into_lds(*c)]
+        behind = sum(op == "global_store_dwordx4" for op, _ in block[loads[-1]:]) if loads else 0
+        out += [behind] if behind else []
+    return out
+
+
+def test_stores_that_the_tiles_do_not_wait_for():
+    for name, kernel in isa.kernels("swiglugemm").items():
+        if "swiglu_tile_kernel" in name:
+            # the loop's count, where loads are left on their way, stands with one of LDS operations
+            waits, stores = counted_waits(kernel), stores_behind_the_loads(kernel)
+            assert len(waits) == 1 and len(stores) == 1, (name, waits, stores)
+            assert stores[0] >= waits[0] > 0, (name, waits, stores)
+
+
+def test_the_count_sees_a_store_too_few():
+    load, store, branch = "buffer_load_dwordx4 v1, s[4:7], 0 offen lds", "global_store_dwordx4 v[2:3], v[4:7], off", "s_cbranch_scc1 .L1"
+    lines = [".L1:", load, branch, load, store, store, load, store, store, branch, store, "s_endpgm"]
+    assert stores_behind_the_loads(isa.Kernel(lines)) == [2]
+    assert stores_behind_the_loads(isa.Kernel(lines[:7] + lines[8:])) == [1]
+    assert stores_behind_the_loads(isa.Kernel(lines[:9] + [load] + lines[9:])) == []
 
 
 def test_instructions():
