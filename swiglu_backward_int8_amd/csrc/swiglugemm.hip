@@ -723,7 +723,7 @@ void launch_tile(GemmArgs a, int cus, hipStream_t stream) {
 
 // ---- few rows: operands straight from memory into registers ----
 //
-// The gated product of up to 16 rows of x.  A workgroup owns 16 rows of Wg and the same
+// The gated product of up to 64 rows of x.  A workgroup owns 16 rows of Wg and the same
 // of Wu; its waves take K 128 values at a time in turn, and their sums meet in LDS.
 // Nothing is shared between waves, so nothing waits: the weight streams through
 // once, 64 bytes of a row with each load, a line with two.  Rows past M or N are read
@@ -731,19 +731,22 @@ void launch_tile(GemmArgs a, int cus, hipStream_t stream) {
 // (180 MB) takes 36.6 us, 4.9 TB/s, where a large copy moves 5.1.  Sixteen rows of Wg a
 // workgroup make 688 workgroups of it; with 32 they were 344, and took half as long again.
 constexpr int kStreamK = 128, kStreamWaves = 8;
-template <bool kKeep>
+template <int kBlocks, bool kKeep>  // kBlocks: 16 rows of x each
 __global__ __launch_bounds__(64 * kStreamWaves) void swiglu_stream_kernel(const GemmArgs a) {
-  __shared__ f32x4 s_sum[kStreamWaves - 1][2][64];
+  static_assert(kBlocks <= kStreamWaves, "a wave stores a block");
+  __shared__ f32x4 s_sum[kStreamWaves][kBlocks][2][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kb = lane >> 4;
   const int64_t n0 = 16ll * blockIdx.x, row = n0 + r < a.N ? n0 + r : a.N - 1;
   const uint16_t* const from_g = a.B + row * a.ldb + 8 * kb;
   const uint16_t* const from_u = a.B + (a.N + row) * a.ldb + 8 * kb;
-  const uint16_t* const from_x = a.A + (r < a.M ? r : a.M - 1) * a.lda + 8 * kb;
-  f32x4 gate = {}, up = {};
+  const uint16_t* from_x[kBlocks];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) from_x[b] = a.A + std::min<int64_t>(16 * b + r, a.M - 1) * a.lda + 8 * kb;
+  f32x4 gate[kBlocks] = {}, up[kBlocks] = {};
   auto chunk = [&](int64_t k0, auto whole) {
-    u32x4 fg[4], fu[4], fx[4];
+    u32x4 fg[4], fu[4], fx[kBlocks][4];
     auto load = [&](const uint16_t* p, int j) {
       if (decltype(whole)::value || k0 + 32 * j + 8 * kb < a.K) return *reinterpret_cast<const u32x4*>(p + k0 + 32 * j);  // K is a multiple of 8
       return (u32x4){0, 0, 0, 0};
@@ -751,31 +754,38 @@ __global__ __launch_bounds__(64 * kStreamWaves) void swiglu_stream_kernel(const 
 #pragma unroll
     for (int j = 0; j < 4; ++j) fg[j] = load(from_g, j), fu[j] = load(from_u, j);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fx[j] = load(from_x, j);
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fx[b][j] = load(from_x[b], j);
     // The weight's rows come first in the instruction: a lane holds four columns of C.
     auto mfma16 = [](const u32x4& a, const u32x4& b, const f32x4& c) {
       return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) gate = mfma16(fg[j], fx[j], gate), up = mfma16(fu[j], fx[j], up);
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) gate[b] = mfma16(fg[j], fx[b][j], gate[b]), up[b] = mfma16(fu[j], fx[b][j], up[b]);
   };
   const int64_t whole = a.K / kStreamK;
   for (int64_t c = wave; c < whole; c += kStreamWaves) chunk(c * kStreamK, std::true_type{});
   if (a.K % kStreamK != 0 && whole % kStreamWaves == wave) chunk(whole * kStreamK, std::false_type{});
-  if (wave > 0) s_sum[wave - 1][0][lane] = gate, s_sum[wave - 1][1][lane] = up;
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) s_sum[wave][b][0][lane] = gate[b], s_sum[wave][b][1][lane] = up[b];
   __syncthreads();
-  if (wave > 0) return;
-  for (int v = 0; v < kStreamWaves - 1; ++v) gate += s_sum[v][0][lane], up += s_sum[v][1][lane];
-  const int64_t n = n0 + 4 * kb;
-  if (r >= a.M || n >= a.N) return;
+  if (wave >= kBlocks) return;
+  f32x4 g = s_sum[0][wave][0][lane], u = s_sum[0][wave][1][lane];
+#pragma unroll
+  for (int v = 1; v < kStreamWaves; ++v) g += s_sum[v][wave][0][lane], u += s_sum[v][wave][1][lane];
+  const int64_t m = 16 * wave + r, n = n0 + 4 * kb;
+  if (m >= a.M || n >= a.N) return;
   f32x4 y;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = Sigmoid(gate[e]).times(gate[e]) * up[e];
+  for (int e = 0; e < 4; ++e) y[e] = Sigmoid(g[e]).times(g[e]) * u[e];
   auto pack4 = [](const f32x4& v) { return (u32x2){pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)}; };
-  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.C) + r * a.N + n) = pack4(y);
+  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.C) + m * a.N + n) = pack4(y);
   if (kKeep) {
-    *reinterpret_cast<u32x2*>(a.gu + r * 2 * a.N + n) = pack4(gate);
-    *reinterpret_cast<u32x2*>(a.gu + r * 2 * a.N + a.N + n) = pack4(up);
+    *reinterpret_cast<u32x2*>(a.gu + m * 2 * a.N + n) = pack4(g);
+    *reinterpret_cast<u32x2*>(a.gu + m * 2 * a.N + a.N + n) = pack4(u);
   }
 }
 
@@ -859,11 +869,18 @@ void launch_gated(const GemmArgs& a, int cus, hipStream_t stream) {
     launch_zero(a.gu, 4 * a.M * a.N, stream);
     return;
   }
-  // Up to 8 rows the stream; up to 16 as long as tiles of 64 x 64 columns would leave half of the CUs without one (H =
-  // 11008, D = 4096: 1 row 36.7 us, tiles 41.4; 8 rows 41.2 and 41.6; 16 rows 46.2 and 41.8; H = 1376, D = 2048: 8 rows
-  // 7.0 and 13.9 us).
-  if (a.M <= 8 || (a.M <= 16 && a.N <= 64 * 128)) {
-    hipLaunchKernelGGL((swiglu_stream_kernel<kKeep>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * kStreamWaves), 0, stream, a);
+  // Up to 8 rows the stream, and up to 64 as long as its tiles of 64 x 64 columns leave CUs without one.  In us, stream and
+  // tiles (H x D): 1 row of 11008 x 4096 36.7 and 41.4, 8 rows 41.2 and 41.6, 16 rows 46.2 and 41.8; 16 rows of 1376 x 2048 7.6
+  // and 14.3, 32 rows 9.4 and 14.3, of 4096 x 4096 16.9 and 24.2, of 5504 x 2048 17.8 and 14.5; 48 rows of 1376 x 2048 12.2 and
+  // 14.3, 64 rows of 4096 x 1024 8.2 and 9.4, of 2048 x 4096 24.0 and 24.3, of 5504 x 2048 26.6 and 14.5.
+  if (a.M <= 8 || (a.M <= 16 && a.N <= 8192) || (a.M <= 32 && a.N <= 4096) || (a.M <= 64 && a.N <= 4096 && a.K <= 2048)) {
+    const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kStreamWaves);
+    if (a.M <= 16)
+      hipLaunchKernelGGL((swiglu_stream_kernel<1, kKeep>), grid, block, 0, stream, a);
+    else if (a.M <= 32)
+      hipLaunchKernelGGL((swiglu_stream_kernel<2, kKeep>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((swiglu_stream_kernel<4, kKeep>), grid, block, 0, stream, a);
     return;
   }
   launch_tiles<kGated, kKeep, false>(a, plan(a.M, 2 * a.N, a.K, false, false).tiles, cus, stream);

@@ -86,7 +86,7 @@ def test_instructions():
         assert ("ds_read_b64_tr_b16" in ops) == by_k, name
         assert any(isa.into_lds(*c) and c[0] == "buffer_load_dwordx4" for c in kernel.code), name
     stream = [k for n, k in isa.kernels("swiglugemm").items() if "swiglu_stream_kernel" in n]
-    assert len(stream) == 2
+    assert len(stream) == 2 * 3  # with and without gu, by the rows of x
     for kernel in stream:
         ops = [op for op, _ in kernel.code]
         assert "v_mfma_f32_16x16x32_bf16" in ops and "global_load_dwordx4" in ops

@@ -73,7 +73,7 @@ def check_y(y, gate, up, e_gate, e_up):
 SHAPES = [(1, 8, 8), (1, 64, 64), (1, 1024, 1000), (2, 72, 4096), (3, 8, 16), (5, 72, 40), (8, 264, 1376), (16, 128, 256), (17, 136, 200),
           (33, 512, 72), (40, 1000, 512), (64, 128, 256), (65, 200, 1024), (100, 2048, 128), (130, 264, 520), (200, 64, 2048), (256, 256, 64),
           (257, 520, 1032), (300, 1376, 264), (513, 72, 328), (777, 1376, 512), (1001, 1408, 1032), (2100, 1032, 136), (4, 11008, 4096),
-          (31, 4096, 2048), (2050, 2056, 1096), (5000, 520, 264), (4097, 4104, 72)]
+          (31, 4096, 2048), (32, 136, 1000), (33, 72, 136), (47, 1376, 2048), (64, 4096, 264), (64, 4104, 128), (2050, 2056, 1096), (5000, 520, 264), (4097, 4104, 72)]
 
 
 @pytest.mark.parametrize("T,H,D", SHAPES)
