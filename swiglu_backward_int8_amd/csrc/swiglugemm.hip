@@ -992,14 +992,14 @@ __attribute__((visibility("default"))) int swiglu_gemm_bwd(const void* dy, const
     for (int i = 0; i < o; ++i)
       if (overlap(out[o], out[i])) return SILUQUANT_ERR_OVERLAP;
   }
+  int cus = 0;
+  if (!device_cus(&cus)) return SILUQUANT_ERR_DEVICE;
   uint16_t* d = static_cast<uint16_t*>(d_gu);
   if (some) {
     const GateArgs a = {static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(gu), d, T, (int)H};
     const int64_t groups = (T * (H / 8) + 255) / 256;
     hipLaunchKernelGGL(swiglu_gate_bwd_kernel, dim3((unsigned)std::min<int64_t>(groups, 1 << 20)), dim3(256), 0, stream, a);
   }
-  int cus = 0;
-  if (!device_cus(&cus)) return SILUQUANT_ERR_DEVICE;
   if (dx)
     launch_product<kDx>({d, static_cast<const uint16_t*>(w), dx, nullptr, T, D, 2 * H, (int)(2 * H), (int)D, 0, 0, 0}, dx32, workspace,
                         cus, stream);
