@@ -25,9 +25,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // The sigmoid s = 1 / (1 + exp(-g)) in parts that neither overflow nor lose small
 // values: with h = exp(-|g| / 2) and r = 1 / (1 + h^2), s is r for g >= 0 and h^2 r
-// below, and 1 - s the other way round; what a value is multiplied by h^2 for goes
-// through h twice (h^2 alone is 0 from g = -104 on, and has few bits before).  Off
-// by some 1e-7 of itself: for what is rounded to bf16 once, behind it.
+// below; what a value is multiplied by h^2 for goes through h twice (h^2 alone is 0
+// from g = -104 on, and has few bits before).  Off by some 1e-7 of itself: for what is
+// rounded to bf16 once, behind it.
 struct Sigmoid {
   float h, r;
   bool below;
@@ -37,35 +37,33 @@ struct Sigmoid {
     below = g < 0.0f;
   }
   __device__ __forceinline__ float times(float v) const { return (below ? (v * h) * h : v) * r; }  // v * s
-  __device__ __forceinline__ float rest() const { return (below ? 1.0f : h * h) * r; }             // 1 - s
-};
-
-// s and 1 - s to the last bit or so, for |g| up to 80: the exponent's argument in two
-// parts, and the reciprocal corrected by what it and 1 + e leave over.  d_gu is an
-// operand of two products, and an error of 1e-7 rounds one value in ten thousand to
-// its other neighbour in bf16.
-struct NearSigmoid {
-  float s, rest;
-  static constexpr float kMost = 80.0f;
-  __device__ __forceinline__ explicit NearSigmoid(float g) {
-    constexpr float kHi = -1.44269504088896341f, kLo = (float)(-1.44269504088896341 - (double)kHi), kLn2 = 0.69314718056f;
-    const float a = __builtin_fabsf(g), t = a * kHi;
-    const float left = __builtin_fmaf(a, kLo, __builtin_fmaf(a, kHi, -t));
-    float e = __builtin_amdgcn_exp2f(t);
-    e = __builtin_fmaf(e, left * kLn2, e);
-    const float d = 1.0f + e, d_left = e - (d - 1.0f);
-    float r = __builtin_amdgcn_rcpf(d);
-    r = __builtin_fmaf(__builtin_fmaf(-d_left, r, __builtin_fmaf(-d, r, 1.0f)), r, r);
-    const float er = e * r;
-    s = g < 0.0f ? er : r;
-    rest = g < 0.0f ? r : er;
-  }
 };
 
 // ---- d_gu ----
 //
-// Reads dy, gate and up once and writes d_gu: 16384 x 11008, 1.8 GB, in 337 us, 5.35 TB/s
-// (a large copy: 5.1).
+// In fp64 but for what is small: d_gu is an operand of two products, and arithmetic in
+// fp32 rounds one value in a hundred thousand to its other neighbour in bf16 (13 in a
+// million; this one 0.1).  fp64's range also holds every product and every sigmoid on
+// the way.  Reads dy, gate and up once and writes d_gu: 16384 x 11008, 1.8 GB, in 337 us,
+// 5.35 TB/s (a large copy: 5.1), its arithmetic and memory about even; in fp32 296.
+
+// exp(-a) for a >= 0, good to 1.1e-8 for every bf16 a up to 700: a = k ln 2 - r, |r| <= ln 2 / 2, where k times the
+// first 13 bits of ln 2 and its distance from a (of 8 bits, up to 800) are exact in fp32;
+// 1 + r in fp64 and the rest of the series, a sixteenth of it at most, in fp32.  Past 800 it
+// is 0 in fp64 too; a NaN is the caller's to keep.
+__device__ __forceinline__ double exp_minus(float a) {
+  constexpr float kHi = 0.693115234375f, kLo = (float)(0.69314718055994530942 - 0.693115234375);
+  a = __builtin_fminf(a, 800.0f);
+  const float k = __builtin_rintf(a * 1.44269504f), r = __builtin_fmaf(k, kHi, -a), left = k * kLo, q = r + left;
+  float p = 1.0f / 40320;
+  p = __builtin_fmaf(p, q, 1.0f / 5040);
+  p = __builtin_fmaf(p, q, 1.0f / 720);
+  p = __builtin_fmaf(p, q, 1.0f / 120);
+  p = __builtin_fmaf(p, q, 1.0f / 24);
+  p = __builtin_fmaf(p, q, 1.0f / 6);
+  p = __builtin_fmaf(p, q, 0.5f);
+  return __builtin_amdgcn_ldexp(1.0 + ((double)r + (double)__builtin_fmaf(p * q, q, left)), -(int)k);
+}
 
 struct GateArgs {
   const uint16_t* dy;  // [T, H]
@@ -85,25 +83,15 @@ __global__ __launch_bounds__(256) void swiglu_gate_bwd_kernel(const GateArgs a) 
     unpack(d, load_bf16<kFull, true>(a.dy + t * a.H + col, 8));
     unpack(g, load_bf16<kFull, true>(from, 8));
     unpack(u, load_bf16<kFull, true>(from + a.H, 8));
-    // dy * up and dy * gate are exact, products of two bf16 numbers, as long as they do not pass fp32's range
-    float top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf(g[k]), 0x1p-100f * __builtin_fabsf(d[k])));
-    if (__any(top > NearSigmoid::kMost)) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const Sigmoid s(g[k]);
-        dg[k] = s.times(d[k] * u[k]) * __builtin_fmaf(g[k], s.rest(), 1.0f);
-        du[k] = d[k] * s.times(g[k]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const NearSigmoid s(g[k]);
-        dg[k] = (d[k] * u[k]) * (s.s * __builtin_fmaf(g[k], s.rest, 1.0f));
-        du[k] = (d[k] * g[k]) * s.s;
-      }
+    for (int k = 0; k < 8; ++k) {
+      // s and 1 - s, neither as a difference
+      const double e = exp_minus(__builtin_fabsf(g[k])), m = 1.0 + e;
+      double r = __builtin_amdgcn_rcpf((float)m);  // and a step of Newton's
+      r = __builtin_fma(__builtin_fma(-m, r, 1.0), r, r);
+      const double er = e * r, s = g[k] < 0.0f ? er : r, rest = g[k] < 0.0f ? r : er;
+      dg[k] = (float)(((double)d[k] * u[k]) * (s * __builtin_fma((double)g[k], rest, 1.0)));
+      du[k] = (float)((double)d[k] * (s * g[k]));
     }
     auto pack8 = [](const float (&v)[8]) {
       return Piece{{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}};

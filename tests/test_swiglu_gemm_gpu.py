@@ -231,6 +231,49 @@ def test_extreme_gates(T, H, D):
     check_products(d_gu, x, w, dx, dw)
 
 
+def formula(dy, gu):
+    """d_gu in 64 bits."""
+    gate, up = gu.double().chunk(2, 1)
+    s = 1 / (1 + torch.exp(-gate))
+    return torch.cat([dy.double() * up * s * (1 + gate * (1 - s)), dy.double() * gate * s], 1)
+
+
+def test_d_gu_is_the_rounded_formula():
+    # d_gu's fp32 values are off by 5e-9 of themselves on average before they are rounded, and so are another fp32 number in
+    # at most 5e-9 / 2^-25 = 0.17 of the cases; that rounds to another bf16 number where one of the two is the middle between
+    # two of them, 2 of 2^16, half of the times: 2.6e-6 of all.  (Rounding an fp32 computation: 1e-5.)
+    T, H = 2048, 1024
+    g = torch.Generator(device=DEV).manual_seed(5)
+    gu = (torch.randn((T, 2 * H), generator=g, device=DEV) * 2).to(bf16)
+    dy = torch.randn((T, H), generator=g, device=DEV).to(bf16)
+    x, w = normal(T, H, 8, 0)
+    d_gu = run_backward(dy, gu, x, w, want=(False, False))[0]
+    assert (d_gu != formula(dy, gu).float().to(bf16)).sum() <= 2.6e-6 * d_gu.numel()
+
+
+def test_d_gu_at_the_ends_of_the_range():
+    # every combination: products past fp32's range that the sigmoid brings back, infinities, NaN, both zeros
+    inf, nan = float("inf"), float("nan")
+    values = torch.tensor([0.0, -0.0, 1.0, -1.0, 2.0**-126, 2.0**-133, -2.0**127, 2.0**127, 88.5, -88.5, 104.0, -104.0, -150.0, -700.0,
+                           -800.0, -1000.0, 1000.0, 0.01, inf, -inf, nan, -1.28125, -1.2734375, -20.0], device=DEV)
+    dy, gate, up = (v.reshape(-1) for v in torch.meshgrid(values, values, values, indexing="ij"))
+    T = dy.numel()
+    dy, gu = dy.to(bf16).reshape(T // 8, 8).contiguous(), torch.cat([gate.reshape(-1, 8), up.reshape(-1, 8)], 1).to(bf16)
+    x, w = normal(T // 8, 8, 8, 0)
+    d_gu = run_backward(dy, gu, x, w, want=(False, False))[0]
+    gate, up = gu.double().chunk(2, 1)
+    # in an order that no product of finite numbers leaves fp64's range in, and no small value is lost in
+    e = torch.exp(-gate.abs())
+    s, rest = torch.where(gate < 0, e, 1.0) / (1 + e), torch.where(gate < 0, 1.0, e) / (1 + e)
+    want = torch.cat([dy.double() * up * (s * (1 + gate * rest)), dy.double() * (gate * s)], 1).float()
+    got = d_gu.float()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.isnan(want).any() and torch.isinf(want).any()
+    off = (got.double() - want.double()).abs()
+    # half a step of bf16, 2^-134 among the denormal numbers, and what passes the largest one is infinite
+    ok = torch.isnan(want) | (got == want) | (got == want.to(bf16).float()) | (off <= HALF * 1.001 * want.double().abs() + 2.0**-134 * 1.001)
+    assert ok.all(), (got[~ok][:5], want[~ok][:5])
+
+
 def test_gradients_against_differences():
     # loss = sum(dy * y(x, w)) in 64 bits, central differences in x and w; gate and up as they are (gu rounds them
     # by 2^-9 at most, which the gradients follow smoothly)
