@@ -85,12 +85,12 @@ __global__ __launch_bounds__(256) void swiglu_gate_bwd_kernel(const GateArgs a) 
     unpack(u, load_bf16<kFull, true>(from + a.H, 8));
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      // s and 1 - s, neither as a difference
+      // s * (1 + gate * (1 - s)) as s + gate * w: w = s * (1 - s) is the same for -gate
       const double e = exp_minus(__builtin_fabsf(g[k])), m = 1.0 + e;
       double r = __builtin_amdgcn_rcpf((float)m);  // and a step of Newton's
       r = __builtin_fma(__builtin_fma(-m, r, 1.0), r, r);
-      const double er = e * r, s = g[k] < 0.0f ? er : r, rest = g[k] < 0.0f ? r : er;
-      dg[k] = (float)(((double)d[k] * u[k]) * (s * __builtin_fma((double)g[k], rest, 1.0)));
+      const double er = e * r, s = g[k] < 0.0f ? er : r, w = er * r;
+      dg[k] = (float)(((double)d[k] * u[k]) * __builtin_fma((double)g[k], w, s));
       du[k] = (float)((double)d[k] * (s * g[k]));
     }
     auto pack8 = [](const float (&v)[8]) {
