@@ -44,8 +44,9 @@ struct Sigmoid {
 // In fp64 but for what is small: d_gu is an operand of two products, and arithmetic in
 // fp32 rounds one value in a hundred thousand to its other neighbour in bf16 (13 in a
 // million; this one 0.1).  fp64's range also holds every product and every sigmoid on
-// the way.  Reads dy, gate and up once and writes d_gu: 16384 x 11008, 1.8 GB, in 337 us,
-// 5.35 TB/s (a large copy: 5.1), its arithmetic and memory about even; in fp32 296.
+// the way.  Reads dy, gate and up once and writes d_gu: 16384 x 11008, 1.8 GB, in 309 us
+// before the products, 5.8 TB/s (a large copy: 5.1), its arithmetic and memory about even;
+// in fp32 296.
 
 // exp(-a) for a >= 0, good to 1.1e-8 for every bf16 a up to 700: a = k ln 2 - r, |r| <= ln 2 / 2, where k times the
 // first 13 bits of ln 2 and its distance from a (of 8 bits, up to 800) are exact in fp32;
