@@ -618,8 +618,8 @@ struct DropArgs {
   const void* x;
   const uint16_t* residual;  // may be null
   uint16_t* out;             // may be x (bf16) or residual
-  int64_t T;
-  int D, pieces;  // per row
+  int64_t T, first;          // first: the launch's first piece
+  int D, pieces;             // pieces: per row
   Dropout drop;
 };
 // Sixteen values a lane, four counters' words: 16384 x 4096 in 48 us, 5.6 TB/s (with a
@@ -632,7 +632,7 @@ __global__ __launch_bounds__(kDropThreads) void dropout_add_kernel(const DropArg
   DropKey key = {};
   if (a.drop.rng) key = drop_key(a.drop);
   // the workgroup's first piece, and from there on in 32 bits
-  const int64_t start = (int64_t)blockIdx.x * (kDropThreads * kDropPieces);
+  const int64_t start = a.first + (int64_t)blockIdx.x * (kDropThreads * kDropPieces);
   const int64_t row0 = start / a.pieces;
   const uint32_t piece0 = (uint32_t)(start - row0 * a.pieces);
   int64_t row[kDropPieces], at[kDropPieces];
@@ -660,8 +660,9 @@ __global__ __launch_bounds__(kDropThreads) void dropout_add_kernel(const DropArg
 }
 
 constexpr int64_t kMaxD = int64_t(1) << 22, kMaxT = int64_t(1) << 31;
+constexpr int64_t kMaxDropped = int64_t(1) << 40;  // elements of dropout_add
 constexpr int kRegisterD = 16384;  // rows up to here stay in registers
-constexpr int kMaxGrid = 1 << 20;  // workgroups of the forward kernels; further rows are walked
+constexpr int kMaxGrid = 1 << 20;  // workgroups of a launch: the forward kernels walk further rows, the dropout launches again
 
 // Workgroups of the backward pass, each with a partial dw and db row: eight waves
 // per CU, and one workgroup per CU at the least.
@@ -828,11 +829,10 @@ __attribute__((visibility("default"))) int layer_norm_bwd(const void* dy, int dy
 __attribute__((visibility("default"))) int dropout_add(const void* x, int x_dtype, const void* residual, void* out,
                                                        int64_t T, int64_t D, float p, const int64_t* rng, int64_t offset,
                                                        hipStream_t stream) {
-  if (T < 0 || D < 0 || T > kMaxT || D > kMaxD || !probability(p) || (x_dtype != SILUQUANT_F32 && x_dtype != SILUQUANT_BF16))
+  if (T < 0 || D < 0 || T > kMaxT || D > kMaxD || T * D > kMaxDropped || !probability(p) ||
+      (x_dtype != SILUQUANT_F32 && x_dtype != SILUQUANT_BF16))
     return SILUQUANT_ERR_BAD_SHAPE;
   if (T == 0 || D == 0) return SILUQUANT_OK;
-  const int64_t pieces = (D + 7) / 8, at_once = kDropThreads * kDropPieces, groups = (T * pieces + at_once - 1) / at_once;
-  if (groups > INT32_MAX) return SILUQUANT_ERR_BAD_SHAPE;
   if (p == 0.0f) rng = nullptr;  // not looked at
   if (!x || !out || (p > 0.0f && !rng)) return SILUQUANT_ERR_NULL_PTR;
   if (misaligned(x, 16) || misaligned(residual, 16) || misaligned(out, 16) || misaligned(rng, 8)) return SILUQUANT_ERR_MISALIGNED;
@@ -841,9 +841,18 @@ __attribute__((visibility("default"))) int dropout_add(const void* x, int x_dtyp
   if ((overlap(o, {x, T * D * (f32 ? 4 : 2)}) && (f32 || x != out)) || (overlap(o, {residual, 2 * T * D}) && residual != out) ||
       overlap(o, {rng, 16}))
     return SILUQUANT_ERR_OVERLAP;
-  const DropArgs a = {x, static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(out), T, (int)D, (int)pieces,
-                      make_dropout(p, rng, offset)};
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kDropThreads), 0, stream, a); };
+  const int64_t pieces = (D + 7) / 8;
+  DropArgs a = {x, static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(out), T, 0, (int)D, (int)pieces,
+                make_dropout(p, rng, offset)};
+  // A launch has fewer than 2^32 threads.  More of them, each of whole workgroups, cost nothing at that size; a loop
+  // over the pieces in the kernel made the ordinary sizes slower (16384 x 11008 125 us, so 121).
+  auto go = [&](auto kernel) {
+    constexpr int64_t kAtOnce = kDropThreads * kDropPieces;
+    for (const int64_t groups = (T * pieces + kAtOnce - 1) / kAtOnce; a.first < T * pieces; a.first += kMaxGrid * kAtOnce) {
+      const dim3 grid((unsigned)std::min<int64_t>(groups - a.first / kAtOnce, kMaxGrid));
+      hipLaunchKernelGGL(kernel, grid, dim3(kDropThreads), 0, stream, a);
+    }
+  };
   if (D % 8 == 0)
     f32 ? go(dropout_add_kernel<true, kFull>) : go(dropout_add_kernel<false, kFull>);
   else if (D >= 8)
