@@ -303,7 +303,7 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_quant_wide_kernel(con
       if (a.h) store_bf16<kRagged, true>(a.h + at + col, h, n);
       if (n > 0) {
         const float k = (float)n, m = sum8(h) / k, d = m - mean, part = k / (count + k);
-        sq = squares<kRagged>(sq, h, m, n) + d * d * (count * part);
+        sq = squares<kRagged>(sq, h, m, n) + (count > 0.0f ? d * d * (count * part) : 0.0f);  // at first d is all of m
         mean = __builtin_fmaf(d, part, mean);
         count += k;
       }
