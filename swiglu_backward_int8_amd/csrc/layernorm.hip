@@ -188,6 +188,16 @@ __device__ __forceinline__ Piece normed(const Piece& h, const Piece& w, const Pi
   return pack8(v);
 }
 
+// Zeros in a partial piece's places past the row, for its group's scale: what a row
+// makes of the zeros there is (0 - mean) * rstd * 0, NaN where the first product overflows.
+__device__ __forceinline__ Piece cut(Piece v, int n) {
+  if (n < 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = n > 2 * i + 1 ? v.w[i] : n > 2 * i ? v.w[i] & 0xffffu : 0;
+  }
+  return v;
+}
+
 // kOneWave: each wave of the workgroup takes rows of its own; otherwise the
 // workgroup shares a row.  Piece c of a lane starts kPieces' width of the lanes
 // further.
@@ -268,9 +278,13 @@ __global__ __launch_bounds__(kOneWave ? 256 : 1024) void layer_norm_quant_kernel
       const Piece b = a.bias ? load_bf16<k, false>(a.bias + col(c), n) : zero_piece();
       fold(h[c]);
       if (a.h) store_bf16<k, true>(a.h + at + col(c), h[c], n);
-      const Piece y = normed(h[c], w[c], b, mean, rstd);  // zero past the row, where weight and bias are
+      // an empty piece's y is zero, whatever the row's offset
+      Piece y = normed(h[c], w[c], b, k == kWhole && n <= 0 ? 0.0f : mean, rstd);
       if (a.y) store_bf16<k, true>(a.y + at + col(c), y, n);
-      if (a.q) a.e4m3 ? quantise<true, k>(a, y, row, first + c * step, n) : quantise<false, k>(a, y, row, first + c * step, n);
+      if (a.q) {
+        if (k >= kRagged) y = cut(y, n);
+        a.e4m3 ? quantise<true, k>(a, y, row, first + c * step, n) : quantise<false, k>(a, y, row, first + c * step, n);
+      }
     });
   }
 }
@@ -320,9 +334,12 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_quant_wide_kernel(con
       const int col = 8 * (i * kWideThreads + tid), n = a.D - col;
       const Piece h = a.h ? load_bf16<kRagged, false>(a.h + at + col, n) : h_piece(col);
       const Piece b = a.bias ? load_bf16<kRagged, false>(a.bias + col, n) : zero_piece();
-      const Piece y = normed(h, load_bf16<kRagged, false>(a.weight + col, n), b, mean, rstd);
+      Piece y = normed(h, load_bf16<kRagged, false>(a.weight + col, n), b, n > 0 ? mean : 0.0f, rstd);
       if (a.y) store_bf16<kRagged, true>(a.y + at + col, y, n);
-      if (a.q) a.e4m3 ? quantise<true, kRagged>(a, y, row, col, n) : quantise<false, kRagged>(a, y, row, col, n);
+      if (a.q) {
+        if (a.D & 7) y = cut(y, n);
+        a.e4m3 ? quantise<true, kRagged>(a, y, row, col, n) : quantise<false, kRagged>(a, y, row, col, n);
+      }
     }
   }
 }
