@@ -463,8 +463,10 @@ __global__ __launch_bounds__(kThreads) void layer_norm_bwd_kernel(const LnBwdArg
       unpack(wv, w[c]);
       r.dy[c].get(dv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // places past the row have dy = 0
-        const float n = (hv[i] - mean) * rstd, g = dv[i] * wv[i];
+      for (int i = 0; i < 8; ++i) {  // places past the row have dy = 0, and n = 0 (-mean * rstd may overflow)
+        const int left = n0 - c * step;
+        const bool in = c < kPieces - 1 || kKind == kFull || (kKind == kWhole ? left > 0 : i < left);
+        const float n = in ? (hv[i] - mean) * rstd : 0.0f, g = dv[i] * wv[i];
         dw[c][i] = __builtin_fmaf(dv[i], n, dw[c][i]);
         db[c][i] += dv[i];
         c1 += g;
@@ -586,7 +588,7 @@ __global__ __launch_bounds__(kWideThreads) void layer_norm_bwd_sums_kernel(const
       for (int i = 0; i < 8; ++i) {
         const float g = dy[i] * wv[i];
         c1 += g;
-        c2 = __builtin_fmaf(g, (hv[i] - mean) * rstd, c2);
+        c2 = __builtin_fmaf(g, i < a.D - col ? (hv[i] - mean) * rstd : 0.0f, c2);  // past the row -mean * rstd may overflow
       }
     }
     c1 = group_sum(c1, s_sum, wave, waves), c2 = group_sum(c2, s_sum, wave, waves);
