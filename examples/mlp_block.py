@@ -19,7 +19,9 @@ the dgrad product's output and joins the residual's gradient.
     out = dropout(a) . Wd^T                                          dropout_add, torch's product
 
 Its masks are never stored: the backward pass makes them again from the same
-numbers (rng), which lie on the device, so a captured step can change them.
+numbers (rng), which lie on the device, so a captured step can change them.  A mask
+is told by the sum of the step's number and the call's offset, so the dropouts of a
+step lie 2^32 apart: a step's second mask is none that a later step draws.
 
     python examples/mlp_block.py [T D H]
 
@@ -36,6 +38,7 @@ sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."
 import swiglu_backward_int8_amd as sq  # noqa: E402
 
 EPS = 1e-6
+NORM, ACTIVATION = 0 << 32, 1 << 32  # offsets of the dropouts of a step (of a model: 2 * layer + 0 and + 1)
 
 
 class Mx:
@@ -132,27 +135,28 @@ def train_mxfp4(x, residual, w, Wgu, Wd, d_out, d_h):
 
 
 def train_bf16(x, residual, w, b, Wgu, Wd, d_out, d_h, p, rng):
-    """Forward and backward in bf16.  rng: int64 [2], a seed and the step's number.
-    Returns out and the gradients of x, residual, w, b, Wgu and Wd."""
+    """Forward and backward in bf16.  rng: int64 [2], a seed and the step's number
+    (below 2^32).  Returns out and the gradients of x, residual, w, b, Wgu and Wd."""
     T, D = x.shape
     H = Wd.shape[1]
     new = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device=x.device)
     h, y, mean, rstd = new(T, D), new(T, D), new(T, dtype=torch.float32), new(T, dtype=torch.float32)
-    sq.layer_norm_quant(x, w, b, residual=residual, h=h, mean=mean, rstd=rstd, y_bf16=y, eps=EPS, p=p, rng=rng)
+    sq.layer_norm_quant(x, w, b, residual=residual, h=h, mean=mean, rstd=rstd, y_bf16=y, eps=EPS, p=p, rng=rng,
+                        offset=NORM)
     a, gu, ad = new(T, H), new(T, 2 * H), new(T, H)
     sq.swiglu_gemm(y, Wgu, a, gu=gu)
-    sq.dropout_add(a, ad, p, rng, offset=1)
+    sq.dropout_add(a, ad, p, rng, offset=ACTIVATION)
     out = ad @ Wd.t()
 
     d_Wd = d_out.t() @ ad
     d_a = d_out @ Wd
-    sq.dropout_add(d_a, d_a, p, rng, offset=1)
+    sq.dropout_add(d_a, d_a, p, rng, offset=ACTIVATION)
     d_y, d_Wgu = new(T, D), new(2 * H, D)
     sq.swiglu_gemm_bwd(d_a, gu, y, Wgu, gu, dx=d_y, dw=d_Wgu, workspace=sq.swiglu_gemm_bwd_workspace(T, H, D, x.device))
     d_residual, d_x = new(T, D), new(T, D) if p > 0 else None
     d_w, d_b = new(D, dtype=torch.float32), new(D, dtype=torch.float32)
     sq.layer_norm_bwd(d_y, h, w, mean, rstd, d_residual, dw=d_w, db=d_b, d_h=d_h, dx_drop=d_x,
-                      workspace=sq.layer_norm_bwd_workspace(T, D, x.device), p=p, rng=rng)
+                      workspace=sq.layer_norm_bwd_workspace(T, D, x.device), p=p, rng=rng, offset=NORM)
     return out, d_residual if d_x is None else d_x, d_residual, d_w, d_b, d_Wgu, d_Wd
 
 
@@ -166,11 +170,11 @@ def reference_bf16(x, residual, w, b, Wgu, Wd, d_out, d_h, p, rng):
     T, D = x.shape
     H = Wd.shape[1]
     x, residual, w, b, Wgu, Wd = leaves = [t.float().requires_grad_() for t in (x, residual, w, b, Wgu, Wd)]
-    h = residual + x * mask(T, D, 0)
+    h = residual + x * mask(T, D, NORM)
     c = h - h.mean(1, keepdim=True)
     y = c * torch.rsqrt(c.square().mean(1, keepdim=True) + EPS) * w + b
     gate, up = (y @ Wgu.t()).chunk(2, 1)
-    out = (torch.nn.functional.silu(gate) * up * mask(T, H, 1)) @ Wd.t()
+    out = (torch.nn.functional.silu(gate) * up * mask(T, H, ACTIVATION)) @ Wd.t()
     torch.autograd.backward([out, h], [d_out.float(), d_h.float()])
     return [out.detach()] + [t.grad for t in leaves]
 

@@ -368,7 +368,11 @@ int group_dequant(const void* q, const float* s, void* out, int64_t R, int64_t K
  *   rng     int64 [2] in device memory (8-byte aligned): a seed, and a number that
  *           the program changes from step to step.  Read when the kernels run: a
  *           captured call draws a new mask at a replay if they have changed.
- *   offset  added to rng[1] (modulo 2^64): tells the dropouts of a step apart
+ *   offset  added to rng[1] (modulo 2^64): tells the dropouts of a step apart.
+ * Calls with the same seed and the same sum rng[1] + offset draw the same words, so
+ * the sums of all steps and dropouts of a run have to differ: with the step's number
+ * (below 2^32) in rng[1], the i-th dropout of a step takes offset i << 32.  Offset i
+ * itself would be the mask that offset 0 draws i steps later.
  *
  * dropout_add -- out = bf16(residual + dropout(x)), one fp32 product and one fp32
  * sum.  On the gradient of out, without a residual, the backward pass for x.

@@ -601,7 +601,9 @@ def dropout_add(x, out, p: float, rng, residual=None, offset: int = 0):
     mask is a function of the place, rng (int64 [2] on the device: a seed, and a
     number that changes from step to step) and offset (which dropout of the step),
     so the same call on the gradient of out, without residual, is the backward
-    pass.  out bf16 [T, D] may be residual itself, or x itself.  Enqueued on the
+    pass.  What counts is the sum rng[1] + offset: with the step's number (below
+    2^32) in rng[1], the i-th dropout of a step takes offset i << 32, for offset i
+    would be offset 0's mask of i steps later.  out bf16 [T, D] may be residual itself, or x itself.  Enqueued on the
     current stream of x's device; returns None."""
     T, D, idx = _rank2("x", x)
     _want2("x", x, _bf16, _f32, (T, D), idx)

@@ -6,7 +6,9 @@
 // the counter (col / 4, row, rng[1] + offset).  The counter is the place, so the
 // forward and the backward pass, and any division of the rows among lanes, give
 // the same mask.  rng lies in device memory: a captured call draws another mask
-// at every replay if the program has changed the numbers there.
+// at every replay if the program has changed the numbers there.  Two calls with the
+// same sum rng[1] + offset draw the same words: a program keeps the sums of its steps
+// and dropouts apart (the step in the low word, the dropout in the high one).
 #ifndef SILUQUANT_DROPOUT_H
 #define SILUQUANT_DROPOUT_H
 
