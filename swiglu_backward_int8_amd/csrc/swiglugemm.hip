@@ -15,10 +15,12 @@
 #include "code_objects.h"
 #include "rows.h"
 #include "siluquant.h"
+#include "swiglu_plan.h"
 
 namespace {
 
 using namespace rows;
+using namespace swiglu;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -156,7 +158,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 //
 // The order of k within a sum is free as long as A and B agree: lane half h takes
 // k = 8 (4 h + j) .. + 7 of a stage in step j, which is chunk 4 h + j of a row.
-constexpr int kStageK = 64, kRowBytes = 2 * kStageK;
+constexpr int kRowBytes = 2 * kStageK;
 constexpr int kRasterRows = 4;  // tile rows that are walked column by column together
 
 __device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
@@ -804,43 +806,6 @@ void launch_zero(void* p, int64_t bytes, hipStream_t stream) {  // a multiple of
                        static_cast<u32x4*>(p), bytes / 16);
 }
 
-// Which tiles a product of C [M, columns] over K takes (columns: the stored rows of B
-// that it reads, 2H for the gated one), and in how many slices of K.
-struct Plan {
-  enum Tiles { k256, k128, k128Two, k64 } tiles;
-  int slices;
-};
-//
-// The times that decide are measured ones, in us: tiles of 256 x 256 take 1.0 a stage
-// on an idle chip and 1.4 where every CU has one, and 7 for their ends; the others
-// 0.5 to 0.58, 0.68 to 1.13 (two a CU) and 0.4 to 0.45.  Per kernel, all four measured
-// (256, 128, 128 two a CU, 64 x 128): dx of 512 x 22016 x 4096 before slices 514, 200,
-// 326, 153 us; dw of 22016 x 4096 x 1024 172, 225, 195 us; gated 777 x 1376 x 2048 44, 19,
-// 25, 27 us, 300 x 1376 x 2048 44, 18.5, 24, 14.5 us.
-Plan plan(int64_t M, int64_t columns, int64_t K, bool by_k, bool sliced) {
-  constexpr double kCus = 256;
-  const double stages = (double)((K + kStageK - 1) / kStageK);
-  Plan best = {Plan::k256, 1};
-  double least = 1e300;
-  // per_cu: workgroups at once; stage, full: us of a stage alone and what it takes more when every place is taken;
-  // tile: us of a tile's ends
-  auto look = [&](Plan::Tiles t, int tm, int tn, int per_cu, double stage, double full, double tile) {
-    const double tiles = (double)((M + tm - 1) / tm) * (double)((columns + tn - 1) / tn);
-    for (int slices = 1; slices <= (sliced ? 16 : 1); slices *= 2) {
-      if (slices > 1 && (stages < 4 * slices || tiles * slices > per_cu * kCus)) break;
-      const double busy = tiles * slices / (per_cu * kCus), rounds = __builtin_ceil(busy);
-      double us = rounds * (__builtin_ceil(stages / slices) * (stage + full * std::min(1.0, busy)) + tile);
-      if (slices > 1) us += 4.0 + (4.0 * slices + 4.0) * (double)M * (double)columns / 3e6;
-      if (us < least) least = us, best = {t, slices};
-    }
-  };
-  look(Plan::k256, 256, 256, 1, 1.0, 0.4, 7.0);
-  look(Plan::k128, 128, 128, 1, 0.5, 0.08, 2.1);
-  look(Plan::k128Two, 128, 128, 2, 0.68, 0.45, 2.0);
-  if (!by_k) look(Plan::k64, 64, 128, 1, 0.4, 0.05, 1.5);
-  return best;
-}
-
 template <Product kProduct, bool kKeep, bool kF32>
 void launch_tiles(const GemmArgs& a, Plan::Tiles tiles, int cus, hipStream_t stream) {
   if (tiles == Plan::k256) return launch_tile<4, 4, 2, 3, kProduct, kKeep, kF32>(a, cus, stream);
@@ -858,15 +823,11 @@ void launch_gated(const GemmArgs& a, int cus, hipStream_t stream) {
     launch_zero(a.gu, 4 * a.M * a.N, stream);
     return;
   }
-  // Up to 8 rows the stream, and up to 64 as long as its tiles of 64 x 64 columns leave CUs without one.  In us, stream and
-  // tiles (H x D): 1 row of 11008 x 4096 36.7 and 41.4, 8 rows 41.2 and 41.6, 16 rows 46.2 and 41.8; 16 rows of 1376 x 2048 7.6
-  // and 14.3, 32 rows 9.4 and 14.3, of 4096 x 4096 16.9 and 24.2, of 5504 x 2048 17.8 and 14.5; 48 rows of 1376 x 2048 12.2 and
-  // 14.3, 64 rows of 4096 x 1024 8.2 and 9.4, of 2048 x 4096 24.0 and 24.3, of 5504 x 2048 26.6 and 14.5.
-  if (a.M <= 8 || (a.M <= 16 && a.N <= 8192) || (a.M <= 32 && a.N <= 4096) || (a.M <= 64 && a.N <= 4096 && a.K <= 2048)) {
+  if (const int blocks = streamed(a.M, a.N, a.K)) {
     const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kStreamWaves);
-    if (a.M <= 16)
+    if (blocks == 1)
       hipLaunchKernelGGL((swiglu_stream_kernel<1, kKeep>), grid, block, 0, stream, a);
-    else if (a.M <= 32)
+    else if (blocks == 2)
       hipLaunchKernelGGL((swiglu_stream_kernel<2, kKeep>), grid, block, 0, stream, a);
     else
       hipLaunchKernelGGL((swiglu_stream_kernel<4, kKeep>), grid, block, 0, stream, a);
