@@ -1,6 +1,6 @@
 """The sizes of the gated projection's GPU tests reach every kernel that its planner
-can choose: each product, with each of its tiles, in one piece and in slices of K (CPU
-only)."""
+can choose: each product, with each of its tiles, in one piece and in slices of K, with
+one and with several tiles a workgroup (CPU only)."""
 
 import random
 
@@ -13,7 +13,7 @@ import tile_shapes
 
 def kind(kernel):
     """Slices as whether there are any: their number is a dimension of the grid."""
-    return kernel if kernel[1] == "stream" else (kernel[0], kernel[1], kernel[2] > 1)
+    return kernel if kernel[1] == "stream" else (kernel[0], kernel[1], kernel[2] > 1, kernel[3])
 
 
 def kinds(shapes):
@@ -29,7 +29,7 @@ def drawn(n):
 def test_every_kernel_is_reached():
     tested = kinds(gemm.SHAPES + tile_shapes.SHAPES)
     can_be = kinds(drawn(100000))
-    assert len(can_be) == 3 + 4 + 4 * 2 + 3 * 2  # streams; gated, dx and dw tiles, the last two sliced too
+    assert len(can_be) == 3 + 4 * 2 + 4 * 3 + 3 * 3  # streams; gated, dx and dw tiles: one, several, (but gated) sliced
     assert tested == can_be
 
 
@@ -45,8 +45,14 @@ def sizes(product, T, H, D):
 
 @pytest.mark.parametrize("shape", tile_shapes.SHAPES)
 def test_shapes_are_for_what_they_say(shape):
-    product, tiles, slices = tile_shapes.ONE_TILE_EACH[shape]
-    assert (product, tiles, slices) in plans.kernels([shape])[0]
+    several = shape in tile_shapes.SEVERAL_TILES
+    product, tiles, slices = (tile_shapes.SEVERAL_TILES if several else tile_shapes.ONE_TILE_EACH)[shape]
+    assert (product, tiles, slices, several) in plans.kernels([shape])[0]
     M, columns, K = sizes(product, *shape)
     a, b = plans.SHAPE[tiles]
     assert M > a and columns > b and M % a != 0 and columns % b != 0 and K % 64 != 0
+    turns = plans.sequences(tiles, M, columns)
+    m, n = plans.tile_counts(tiles, M, columns)
+    assert sum(map(len, turns)) == m * n
+    pairs = {p for t in turns for p in zip(t, t[1:])}
+    assert {(True, True), (True, False), (False, True)} <= pairs if several else not pairs
