@@ -25,21 +25,17 @@ using namespace swiglu;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// The sigmoid s = 1 / (1 + exp(-g)) in parts that neither overflow nor lose small
-// values: with h = exp(-|g| / 2) and r = 1 / (1 + h^2), s is r for g >= 0 and h^2 r
-// below; what a value is multiplied by h^2 for goes through h twice (h^2 alone is 0
-// from g = -104 on, and has few bits before).  Off by some 1e-7 of itself: for what is
-// rounded to bf16 once, behind it.
-struct Sigmoid {
-  float h, r;
-  bool below;
-  __device__ __forceinline__ explicit Sigmoid(float g) {
-    h = __builtin_amdgcn_exp2f(-0.72134752044f * __builtin_fabsf(g));  // log2(e) / 2
-    r = __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.0f));
-    below = g < 0.0f;
-  }
-  __device__ __forceinline__ float times(float v) const { return (below ? (v * h) * h : v) * r; }  // v * s
-};
+// silu(g) * u = g * s * u with the sigmoid s = 1 / (1 + exp(-g)) in parts that neither
+// overflow nor lose small values: with h = exp(-|g| / 2) and r = 1 / (1 + h^2), s is r for
+// g >= 0 and h^2 r below, where one h comes before u and one behind it (silu alone is a
+// denormal number from g = -87 on, and 0 from -104).  Within 4 (|g| + 4) 2^-24 of itself:
+// the exponent is rounded relative to itself, and h carries that twice (3e-7 in all for g
+// in (-2, 0), 1e-6 at -20, 4e-6 at -80); for what is rounded to bf16 behind it.
+__device__ __forceinline__ float silu_times(float g, float u) {
+  const float h = __builtin_amdgcn_exp2f(-0.72134752044f * __builtin_fabsf(g));  // log2(e) / 2
+  const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.0f)), part = g < 0.0f ? h : 1.0f;
+  return (((g * part) * r) * u) * part;
+}
 
 // ---- d_gu ----
 //
@@ -636,7 +632,7 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
             for (int e = 0; e < 4; ++e) g[4 * c + e] = gv[e], u[4 * c + e] = uv[e];
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = Sigmoid(g[e]).times(g[e]) * u[e];
+          for (int e = 0; e < 8; ++e) y[e] = silu_times(g[e], u[e]);
           auto pack8 = [](const float (&v)[8]) {
             return (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
           };
@@ -771,7 +767,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void swiglu_stream_kernel(const 
   if (m >= a.M || n >= a.N) return;
   f32x4 y;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = Sigmoid(g[e]).times(g[e]) * u[e];
+  for (int e = 0; e < 4; ++e) y[e] = silu_times(g[e], u[e]);
   auto pack4 = [](const f32x4& v) { return (u32x2){pack_bf16(v.x, v.y), pack_bf16(v.z, v.w)}; };
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.C) + m * a.N + n) = pack4(y);
   if (kKeep) {
