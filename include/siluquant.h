@@ -404,6 +404,9 @@ int dropout_add(const void* x, int x_dtype, const void* residual, void* out, int
  * its scales as there; other rows are not affected.  A row of one value has a
  * variance of zero, up to the rounding of its mean: with eps == 0 its y means
  * nothing.
+ * The statistics are fp32 and hold what that does: a row whose squared differences
+ * from its mean sum to more than 3.4e38 has rstd 0 and the bias for y, one whose
+ * values do y NaN; and where eps does not outweigh them, squares below 1e-38 lose bits.
  */
 int layer_norm_quant(const void* x, int x_dtype, const void* residual, const void* weight, const void* bias, void* y_q,
                      float* y_s, void* y_bf16, void* h, float* mean, float* rstd, int64_t T, int64_t D, int64_t group,

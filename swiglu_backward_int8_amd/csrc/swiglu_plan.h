@@ -22,7 +22,10 @@ struct Plan {
 // 0.5 to 0.58, 0.68 to 1.13 (two a CU) and 0.4 to 0.45.  Per kernel, all four measured
 // (256, 128, 128 two a CU, 64 x 128): dx of 512 x 22016 x 4096 before slices 514, 200,
 // 326, 153 us; dw of 22016 x 4096 x 1024 172, 225, 195 us; gated 777 x 1376 x 2048 44, 19,
-// 25, 27 us, 300 x 1376 x 2048 44, 18.5, 24, 14.5 us.
+// 25, 27 us, 300 x 1376 x 2048 44, 18.5, 24, 14.5 us.  The stages' times are those of
+// loads into LDS; there is no term for bytes from memory, so that a few hundred rows of
+// a wide weight are told too low: gated 64, 128, 256, 512 and 2048 rows of 11008 x 4096
+// 29, 38, 65, 88 and 290 us where they take 45, 52, 80, 96 and 305.
 inline Plan plan(int64_t M, int64_t columns, int64_t K, bool by_k, bool sliced) {
   constexpr double kCus = 256;
   const double stages = (double)((K + kStageK - 1) / kStageK);

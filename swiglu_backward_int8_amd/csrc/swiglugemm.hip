@@ -46,10 +46,10 @@ __device__ __forceinline__ float silu_times(float g, float u) {
 // before the products, 5.8 TB/s (a large copy: 5.1), its arithmetic and memory about even;
 // in fp32 296.
 
-// exp(-a) for a >= 0, good to 1.1e-8 for every bf16 a up to 700: a = k ln 2 - r, |r| <= ln 2 / 2, where k times the
-// first 13 bits of ln 2 and its distance from a (of 8 bits, up to 800) are exact in fp32;
-// 1 + r in fp64 and the rest of the series, a sixteenth of it at most, in fp32.  Past 800 it
-// is 0 in fp64 too; a NaN is the caller's to keep.
+// exp(-a) for a >= 0, good to 1.1e-8 for every bf16 a up to 700: a = k ln 2 - r, |r| <=
+// ln 2 / 2, where k times the first 13 bits of ln 2 and its distance from a (of 8 bits, up
+// to 800) are exact in fp32; 1 + r in fp64 and the rest of the series, 0.07 at most, in
+// fp32.  Past 800 it is 0 in fp64 too; a NaN is the caller's to keep.
 __device__ __forceinline__ double exp_minus(float a) {
   constexpr float kHi = 0.693115234375f, kLo = (float)(0.69314718055994530942 - 0.693115234375);
   a = __builtin_fminf(a, 800.0f);
@@ -133,10 +133,12 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 //
 // Of the largest products (16384 x 11008 x 4096: gate and up 2.95 TFLOP) the forward
 // pass takes 2360 us with gate and up kept (1250 TFLOP/s) and 2270 without (1300), dx
-// 2110 (1400), dW 2270 (1300).  The chip's power is what bounds them: with zeros for
+// 2110 (1400), dW 2270 (1300).  The chip's power bounds most of that: with zeros for
 // operands, which cost it little, the same instructions take 1660 us (1780 TFLOP/s; dx
 // 1880), and multiplying random numbers out of registers alone, with nothing loaded,
-// reaches 1840.  Tiles of 256 x 256 by four waves read each operand from LDS least
+// reaches 1840.  The forward pass is further from that than dx (matrix cores busy 71% and
+// 80%): the way out of its tiles, with gate and up through LDS in fp32 and one turn of
+// pieces, is about 7 us, and each workgroup takes 22 of them.  Tiles of 256 x 256 by four waves read each operand from LDS least
 // often: a wave's 128 x 128 results take 256 accumulators a lane.  Two buffers of A and
 // three of B fill the 160 KB: loads are answered at some 25 bytes a cycle and CU when
 // all ask, and what is on its way has to cover that (two buffers of each, zeros: 1390
