@@ -38,7 +38,7 @@ sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."
 import swiglu_backward_int8_amd as sq  # noqa: E402
 
 EPS = 1e-6
-NORM, ACTIVATION = 0 << 32, 1 << 32  # offsets of the dropouts of a step (of a model: 2 * layer + 0 and + 1)
+NORM, ACTIVATION = 0 << 32, 1 << 32  # offsets of a step's dropouts (layer l of a model: 2 * l << 32 and 2 * l + 1 << 32)
 
 
 class Mx:

@@ -54,3 +54,21 @@ def test_fp32_with_a_residual(T, D):
         rows = slice(first, first + ROWS)
         v = torch.where(kept_rows(first, ROWS, D, 0.25), x[rows].cpu() * ln64.scale(0.25), torch.zeros(()))
         assert torch.equal(out[rows].cpu(), (r[rows].cpu().float() + v).to(bf16)), first
+
+
+def test_captured():
+    # a call of several launches is captured whole, and draws anew when the numbers change
+    T, D = 2**29 + 77, 1
+    x, out, numbers = torch.ones((T, D), dtype=bf16, device=DEV), torch.empty((T, D), dtype=bf16, device=DEV), rng()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sq.dropout_add(x, out, 0.25, numbers)
+    eager = torch.empty_like(out)
+    for step in (5, 6, 5):
+        numbers.copy_(torch.tensor([RNG[0], step]))
+        out.fill_(7)
+        graph.replay()
+        sq.dropout_add(x, eager, 0.25, numbers)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), step
+        assert torch.equal((out[:ROWS] != 0).cpu(), ln64.kept((RNG[0], step), ROWS, D, 0.25)), step
