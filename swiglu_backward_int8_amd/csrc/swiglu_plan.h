@@ -26,7 +26,7 @@ struct Plan {
 // loads into LDS; there is no term for bytes from memory, so that a few hundred rows of
 // a wide weight are told too low: gated 64, 128, 256, 512 and 2048 rows of 11008 x 4096
 // 29, 38, 65, 88 and 290 us where they take 45, 52, 80, 96 and 305.
-inline Plan plan(int64_t M, int64_t columns, int64_t K, bool by_k, bool sliced) {
+static inline Plan plan(int64_t M, int64_t columns, int64_t K, bool by_k, bool sliced) {
   constexpr double kCus = 256;
   const double stages = (double)((K + kStageK - 1) / kStageK);
   Plan best = {Plan::k256, 1};
@@ -58,7 +58,7 @@ inline Plan plan(int64_t M, int64_t columns, int64_t K, bool by_k, bool sliced) 
 // 4096 x 4096 16.9 and 24.2, of 5504 x 2048 17.8 and 14.5; 48 rows of 1376 x 2048 12.2
 // and 14.3, 64 rows of 4096 x 1024 8.2 and 9.4, of 2048 x 4096 24.0 and 24.3, of 5504 x
 // 2048 26.6 and 14.5.
-inline int streamed(int64_t M, int64_t N, int64_t K) {
+static inline int streamed(int64_t M, int64_t N, int64_t K) {
   if (!(M <= 8 || (M <= 16 && N <= 8192) || (M <= 32 && N <= 4096) || (M <= 64 && N <= 4096 && K <= 2048))) return 0;
   return M <= 16 ? 1 : M <= 32 ? 2 : 4;
 }

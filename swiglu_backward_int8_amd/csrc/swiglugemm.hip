@@ -487,6 +487,10 @@ swiglu_tile_kernel(const GemmArgs all, int per_xcd) {
     for (int i = 0; i < kFA; ++i)
 #pragma unroll
       for (int k = 0; k < kFB; ++k) acc[i][k] = (f32x16){};
+    // A wave that had nothing of a partial tile to store has read nothing back of what it
+    // wrote to its patch; the compiler's barrier does not wait for that on its own, and the
+    // others' loads go there from here on.
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
     if (stored_whole)
       asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kStoresAfter) : "memory");
     else
