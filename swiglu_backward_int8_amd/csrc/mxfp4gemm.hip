@@ -515,6 +515,10 @@ mx_gemm_tile_kernel(const GemmArgs a, int per_xcd) {
 #pragma unroll
       for (int k = 0; k < kFB; ++k) acc[i][k] = (f32x16){};
     if (!kWords && stages > 0) exponents(0, sa, sb);
+    // A wave that had nothing of a partial tile to store has read nothing back of what it
+    // wrote to its patch; the compiler's barrier does not wait for that on its own, and the
+    // others' loads go there from here on.
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
     if (kWords && stored_whole)
       asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kStoresAfter) : "memory");
     else

@@ -15,7 +15,7 @@ import pytest
 import isa
 from test_isa_waits import pytestmark  # noqa: F401
 
-SOURCES = ["siluquant", "i8gemm", "rmsnorm", "mxfp4", "layernorm", "swiglugemm"]
+SOURCES = ["siluquant", "i8gemm", "rmsnorm", "mxfp4", "mxfp4gemm", "layernorm", "swiglugemm"]
 
 
 def pending(kernel, which=r"ds_"):
